@@ -68,7 +68,11 @@ enum tabit_status {
   TABIT_ENOMEM = -7    /* host allocation failed                                 */
 };
 
-enum tabit_fmt { TABIT_FMT_INT8 = 0, TABIT_FMT_MXFP4 = 1 };
+enum tabit_fmt {
+  TABIT_FMT_INT8 = 0,
+  TABIT_FMT_MXFP4 = 1,
+  TABIT_FMT_BF16 = 2   /* tabit_block_norm's output only: not a schedule entry */
+};
 enum tabit_path {
   TABIT_PATH_MASKED = 0,
   TABIT_PATH_BITSERIAL = 1,
@@ -500,6 +504,160 @@ size_t tabit_mfma_probe_sink_ints(int num_cus);
 /* The configuration the automatic choice would take for (M, N, K) on a device
  * with num_cus compute units (num_cus <= 0: 256).  Makes no HIP call. */
 int tabit_gemm_config_choose(int M, int N, int K, int num_cus);
+
+/* ------------------------------------------------------------------------
+ * Operators between a block's linears.  Not from the cited pages: what a
+ * transformer block needs around its quantized linears to run.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Paged key / value cache in MXFP4 (OCP MX: E2M1 codes, one E8M0 scale per 32
+ * elements of a head), 4.25 bits an element.  Pages hold page_size tokens of
+ * every key head; slot s is token s % page_size of page s / page_size.
+ *   k_codes, v_codes    device [num_pages][num_kv_heads][page_size][Dp/2], element
+ *                       2i of a row in the low nibble of byte i, 16-byte aligned
+ *   k_scales, v_scales  device [num_pages][num_kv_heads][page_size][Dp/32], 4-byte
+ *                       aligned; Dp = 32 ceil(head_dim / 32), padding is zero
+ *   page_size           power of two, 16 .. 2^20
+ *   head_dim            multiple of 8, 8 .. 128
+ *   had_block           0, or 32: rows hold the unnormalized block-32 Walsh-
+ *                       Hadamard transform of the padded vectors (6Bit-Diffusion
+ *                       section 2A's local block Hadamard before a 4-bit format)
+ * A byte count may pass 2^32 (64-bit addressing).
+ */
+typedef struct tabit_kv_cache {
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  int num_pages, page_size, num_kv_heads, head_dim, had_block;
+} tabit_kv_cache;
+
+/*
+ * Position rotation of the first rope_dim elements of each head (multiple of 16,
+ * at most head_dim): pair i becomes (a c - b s, b c + a s) with c, s row
+ * `position`, column i of the tables, fp32 [num_positions][rope_dim/2], 16-byte
+ * aligned.  interleaved 0: pairs (i, i + rope_dim/2); 1: pairs (2i, 2i + 1).  A
+ * table row per token also serves rotations over several axes.
+ */
+typedef struct tabit_rope {
+  const float *cos, *sin;
+  int num_positions, rope_dim, interleaved;
+} tabit_rope;
+
+/*
+ * Write the keys and values of num_tokens tokens into the cache: keys rotated
+ * (rope, may be NULL) to positions[t], both transformed (had_block) and quantized
+ * to MXFP4 as tabit_hadamard_quant_act defines it, all in fp32 from the bf16
+ * inputs.
+ *   k_bf16, v_bf16  device, token t's [num_kv_heads][head_dim] at t * stride
+ *                   elements (stride a multiple of 8), 16-byte aligned: slices of a
+ *                   fused QKV output need no copy.
+ *   slots           device int64 [num_tokens].  A slot outside the cache (-1 for
+ *                   padding) writes nothing; slots of one call must be distinct.
+ *   positions       device int32 [num_tokens], or NULL without rope.
+ * A (token, head) whose key or value holds an infinity or NaN, or whose position
+ * is outside the tables, is stored as not a number: queries that see it answer
+ * NaN, no other query is touched by it.
+ */
+int tabit_kv_append(tabit_ctx* ctx, const tabit_kv_cache* cache, const uint16_t* k_bf16,
+                    int64_t k_stride, const uint16_t* v_bf16, int64_t v_stride, int num_tokens,
+                    const int64_t* slots, const tabit_rope* rope, const int32_t* positions,
+                    void* stream);
+
+/* The keys (as rotated by their append) and values that the cache holds at
+ * `slots`, turned back from the block transform, bf16 [num_tokens][num_kv_heads]
+ * [head_dim] each, 16-byte aligned; zeros for a slot outside the cache. */
+int tabit_kv_read(tabit_ctx* ctx, const tabit_kv_cache* cache, const int64_t* slots, int num_tokens,
+                  uint16_t* k_bf16, uint16_t* v_bf16, void* stream);
+
+/*
+ * Softmax attention of a ragged batch of query rows over the cache:
+ *   o_i = sum_j softmax_j(scale * (R q_i) . k_j) v_j
+ * over the first kv_lens[b] tokens of sequence b, through its row of the block
+ * table; with `causal` query i of the sequence's n sees j <= kv_lens[b] - n + i.
+ * Query head h reads key head h / (num_q_heads / num_kv_heads).  A query that sees
+ * no key answers zeros (lse -inf).  Scores, softmax and sums are fp32; a query
+ * keeps 13 bits below its block's largest element, a weight is rounded to bf16.
+ *   q            device bf16, token t's [num_q_heads][head_dim] at t * q_stride
+ *                elements (multiple of 8), 16-byte aligned
+ *   cu_q         device int32 [num_seqs + 1]: sequence b's rows are
+ *                [cu_q[b], cu_q[b+1]) of q and out, at most max_q of them (further
+ *                ones are not computed); rows of no sequence are left as they are
+ *   block_table  device int32 [num_seqs][table_stride] page numbers; tokens of a
+ *                page outside the cache are not seen
+ *   kv_lens      device int32 [num_seqs], taken as at most max_kv
+ *   max_kv       at most table_stride * page_size
+ *   rope, positions  rotation of the queries (positions int32 [num_tokens]), or
+ *                NULL; a row with a position outside the tables, or that is not
+ *                finite, answers NaN
+ *   out          device bf16 [num_tokens][num_q_heads][head_dim], 16-byte aligned
+ *   lse          device fp32 [num_tokens][num_q_heads] or NULL: natural logarithm
+ *                of the row's sum of exp(score)
+ *   ws           device workspace of tabit_kv_attention_workspace_bytes bytes,
+ *                16-byte aligned (NULL when that is 0)
+ * num_seqs and num_kv_heads at most 65535.  The result does not depend on timing:
+ * partial sums are joined in a fixed order.
+ */
+typedef struct tabit_kv_attention_args {
+  const uint16_t* q;
+  int64_t q_stride;
+  int num_tokens, num_q_heads;
+  const int32_t* cu_q;
+  int num_seqs, max_q;
+  const int32_t* block_table;
+  int table_stride;
+  const int32_t* kv_lens;
+  int max_kv;
+  float scale;
+  int causal;
+  const tabit_rope* rope;
+  const int32_t* positions;
+  uint16_t* out;
+  float* lse;
+  void* ws;
+  size_t ws_bytes;
+} tabit_kv_attention_args;
+int tabit_kv_attention(tabit_ctx* ctx, const tabit_kv_cache* cache, const tabit_kv_attention_args* args,
+                       void* stream);
+
+/* Bytes of workspace for such a call (0: none needed).  Makes no HIP call. */
+size_t tabit_kv_attention_workspace_bytes(int num_tokens, int num_q_heads, int num_kv_heads,
+                                          int head_dim, int num_seqs, int max_q, int max_kv);
+
+enum tabit_norm { TABIT_NORM_NONE = 0, TABIT_NORM_LAYER = 1, TABIT_NORM_RMS = 2 };
+
+/*
+ * The seam between two blocks in one pass over the tokens:
+ *   x' = res_scale * x + gate * N_post(y)      (x' = res_scale * x without y)
+ *   h  = N_pre(x') * (1 + scale) + shift
+ * N: identity, layer norm (v - mean) / sqrt(var + eps) or RMS norm
+ * v / sqrt(mean(v^2) + eps), times its weight if given.  fp32 throughout; h is
+ * computed from x' before x' is rounded.
+ *   x, y         device bf16 [rows][width]; y may be NULL (then no post norm or gate)
+ *   post_weight, pre_weight  device bf16 [width] or NULL (1)
+ *   gate, scale, shift       device bf16, sample s's row of width elements at
+ *                s * mod_stride (multiple of 8), or NULL (1, 0, 0); token row r is of
+ *                sample r / rows_per_sample, and there are num_samples
+ *   x_out        device bf16 [rows][width] or NULL; may be x or y itself
+ *   h            NULL (then no pre norm, scale or shift), or by fmt: TABIT_FMT_BF16
+ *                bf16 [rows][width]; TABIT_FMT_INT8 int8 [rows][width] with h_scale
+ *                fp32 [rows]; TABIT_FMT_MXFP4 codes [rows][width/2] with h_scale
+ *                uint8 [rows][width/32]: the codes tabit_hadamard_quant_act defines,
+ *                of the fp32 h, with its had_block choices
+ * width is a multiple of 32 in [32, 32768]; matrices and vectors 16-byte aligned.
+ */
+typedef struct tabit_block_norm_args {
+  const uint16_t *x, *y;
+  int rows, width;
+  int post_kind, pre_kind; /* TABIT_NORM_* */
+  const uint16_t *post_weight, *pre_weight;
+  const uint16_t *gate, *scale, *shift;
+  int64_t mod_stride;
+  int num_samples, rows_per_sample;
+  float res_scale, eps;
+  uint16_t* x_out;
+  void *h, *h_scale;
+  int fmt, had_block;
+} tabit_block_norm_args;
+int tabit_block_norm(tabit_ctx* ctx, const tabit_block_norm_args* args, void* stream);
 
 #ifdef __cplusplus
 }

@@ -19,13 +19,15 @@ LIB_PATH = os.path.join(_HERE, "libtabit.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "tabit.h")
 
 OK, EINVAL, ESHAPE, EALIGN, ERANGE, ENOSCHED, EHIP, ENOMEM = 0, -1, -2, -3, -4, -5, -6, -7
-FMT_INT8, FMT_MXFP4 = 0, 1
+FMT_INT8, FMT_MXFP4, FMT_BF16 = 0, 1, 2
 PATH_MASKED, PATH_BITSERIAL, PATH_PLANES, PATH_HQDM = 0, 1, 3, 4
 OPT_GEMM_CONFIG, OPT_MXFP4_CONFIG, OPT_PLANE_CONFIG, OPT_HQDM_CONFIG = 0, 1, 2, 3
 PATH_MXFP4_GEMM = 2
 ACT_NONE, ACT_GELU = 0, 1
+NORM_NONE, NORM_LAYER, NORM_RMS = 0, 1, 2
 
 _c_int, _c_void_p, _c_size_t, _c_float = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
+_c_int64 = ctypes.c_int64
 _PINT = ctypes.POINTER(ctypes.c_int)
 
 # name -> (restype, argtypes)
@@ -89,6 +91,13 @@ _SIGNATURES = {
     "tabit_gated_linear": (_c_int, [_c_void_p, _c_void_p, _c_int, _c_int, _c_void_p, _c_int, _c_int,
                                     _c_int, _c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                     _c_void_p, _c_size_t, _c_void_p, _c_void_p]),
+    "tabit_kv_append": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_int64, _c_void_p, _c_int64,
+                                 _c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    "tabit_kv_read": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_void_p,
+                               _c_void_p]),
+    "tabit_kv_attention": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    "tabit_kv_attention_workspace_bytes": (_c_size_t, [_c_int] * 7),
+    "tabit_block_norm": (_c_int, [_c_void_p, _c_void_p, _c_void_p]),
 }
 
 
@@ -100,6 +109,44 @@ class Layer(ctypes.Structure):
                 ("w_fp4", ctypes.c_void_p), ("w_e8m0", ctypes.c_void_p),
                 ("y_bf16", ctypes.c_void_p), ("input_from", ctypes.c_int),
                 ("input_act", ctypes.c_int)]
+
+
+class _KvCache(ctypes.Structure):
+    """tabit_kv_cache."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("num_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("had_block", ctypes.c_int)]
+
+
+class _Rope(ctypes.Structure):
+    """tabit_rope."""
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("num_positions", ctypes.c_int),
+                ("rope_dim", ctypes.c_int), ("interleaved", ctypes.c_int)]
+
+
+class _KvAttentionArgs(ctypes.Structure):
+    """tabit_kv_attention_args."""
+    _fields_ = [("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("num_tokens", ctypes.c_int),
+                ("num_q_heads", ctypes.c_int), ("cu_q", ctypes.c_void_p), ("num_seqs", ctypes.c_int),
+                ("max_q", ctypes.c_int), ("block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int), ("kv_lens", ctypes.c_void_p),
+                ("max_kv", ctypes.c_int), ("scale", ctypes.c_float), ("causal", ctypes.c_int),
+                ("rope", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
+
+
+class _BlockNormArgs(ctypes.Structure):
+    """tabit_block_norm_args."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("rows", ctypes.c_int),
+                ("width", ctypes.c_int), ("post_kind", ctypes.c_int), ("pre_kind", ctypes.c_int),
+                ("post_weight", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("shift", ctypes.c_void_p),
+                ("mod_stride", ctypes.c_int64), ("num_samples", ctypes.c_int),
+                ("rows_per_sample", ctypes.c_int), ("res_scale", ctypes.c_float),
+                ("eps", ctypes.c_float), ("x_out", ctypes.c_void_p), ("h", ctypes.c_void_p),
+                ("h_scale", ctypes.c_void_p), ("fmt", ctypes.c_int), ("had_block", ctypes.c_int)]
 
 
 _lib = None
@@ -155,6 +202,79 @@ def _dev(t: torch.Tensor, dtype, name: str, shape=None) -> None:
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows(t: torch.Tensor, name: str, tail, device) -> int:
+    """bf16 [T][heads][head_dim] whose tokens may be apart (a slice of a fused output):
+    the stride of a token in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != 3 or t.shape[1:] != tail:
+        raise ValueError(f"{name} must have shape [tokens, {tail[0]}, {tail[1]}], got {tuple(t.shape)}")
+    s = t.stride()
+    if (s[2] != 1 and tail[1] > 1) or (s[1] != tail[1] and tail[0] > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return s[0] if t.shape[0] > 1 else tail[0] * tail[1]
+
+
+def _on(t: torch.Tensor, dtype, name: str, shape, device) -> None:
+    _dev(t, dtype, name, shape)
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+class KVCache:
+    """A paged MXFP4 key / value cache (tabit_kv_cache): its four tensors, kept alive here.
+
+    k_codes, v_codes uint8 [pages][kv_heads][page_size][Dp/2]; k_scales, v_scales uint8
+    [pages][kv_heads][page_size][Dp/32]; Dp = 32 ceil(head_dim / 32).
+    """
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, head_dim: int, had_block: int = 0):
+        dp = (head_dim + 31) // 32 * 32
+        _dev(k_codes, torch.uint8, "k_codes")
+        if k_codes.dim() != 4 or k_codes.shape[3] != dp // 2:
+            raise ValueError(f"k_codes must be [pages][kv_heads][page_size][{dp // 2}]")
+        lead = tuple(k_codes.shape[:3])
+        _on(v_codes, torch.uint8, "v_codes", lead + (dp // 2,), k_codes.device)
+        _on(k_scales, torch.uint8, "k_scales", lead + (dp // 32,), k_codes.device)
+        _on(v_scales, torch.uint8, "v_scales", lead + (dp // 32,), k_codes.device)
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.num_pages, self.num_kv_heads, self.page_size = lead
+        self.head_dim, self.had_block, self.device = head_dim, had_block, k_codes.device
+        self._row = torch.Size((self.num_kv_heads, head_dim))
+        self._c = _KvCache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                           v_scales.data_ptr(), self.num_pages, self.page_size, self.num_kv_heads,
+                           head_dim, had_block)
+        self._ref = ctypes.addressof(self._c)
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,
+              had_block: int = 0, device="cuda:0") -> "KVCache":
+        """A cache of zeros."""
+        dp = (head_dim + 31) // 32 * 32
+        t = [torch.zeros((num_pages, num_kv_heads, page_size, w), dtype=torch.uint8, device=device)
+             for w in (dp // 2, dp // 32, dp // 2, dp // 32)]
+        return cls(*t, head_dim=head_dim, had_block=had_block)
+
+
+class Rope:
+    """Rotation tables (tabit_rope): cos and sin fp32 [positions][rope_dim/2]; interleaved
+    False: pairs (i, i + rope_dim/2), True: pairs (2i, 2i + 1)."""
+
+    def __init__(self, cos: torch.Tensor, sin: torch.Tensor, interleaved: bool = False):
+        _dev(cos, torch.float32, "cos")
+        if cos.dim() != 2:
+            raise ValueError("cos must be [positions][rope_dim/2]")
+        _on(sin, torch.float32, "sin", cos.shape, cos.device)
+        self.cos, self.sin, self.interleaved, self.device = cos, sin, interleaved, cos.device
+        self._c = _Rope(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1],
+                        1 if interleaved else 0)
+        self._ref = ctypes.addressof(self._c)
 
 
 def version() -> str:
@@ -603,3 +723,156 @@ class Context:
                                            y.data_ptr(), reps, ctypes.byref(best), _stream(y.device))
         self._check(st)
         return best.value
+
+    # ------------------------------------------------------------ between the linears
+    def _rope(self, cache: KVCache, rope: Optional[Rope], positions, tokens: int):
+        if rope is None:
+            return None, None
+        if rope.device != cache.device:
+            raise ValueError(f"rope must be on {cache.device}, got {rope.device}")
+        _on(positions, torch.int32, "positions", (tokens,), cache.device)
+        return rope._ref, positions.data_ptr()
+
+    def kv_append(self, cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                  rope: Optional[Rope] = None, positions: Optional[torch.Tensor] = None) -> None:
+        """Rotate k to `positions`, quantize k and v, write them at `slots` (int64 [T]; negative:
+        skipped).  k, v bf16 [T][kv_heads][head_dim], tokens of any stride of 8 elements."""
+        ks = _rows(k, "k", cache._row, cache.device)
+        vs = _rows(v, "v", cache._row, cache.device)
+        n = k.shape[0]
+        if v.shape[0] != n:
+            raise ValueError("k and v disagree on the number of tokens")
+        _on(slots, torch.int64, "slots", (n,), cache.device)
+        r, pos = self._rope(cache, rope, positions, n)
+        if n == 0:
+            return
+        self._check(self._lib.tabit_kv_append(self._h, cache._ref, k.data_ptr(), ks, v.data_ptr(), vs,
+                                              n, slots.data_ptr(), r, pos, _stream(cache.device)))
+
+    def kv_read(self, cache: KVCache, slots: torch.Tensor, k: Optional[torch.Tensor] = None,
+                v: Optional[torch.Tensor] = None):
+        """The keys and values held at `slots` as bf16 [T][kv_heads][head_dim] each."""
+        n = slots.shape[0]
+        _on(slots, torch.int64, "slots", (n,), cache.device)
+        shape = (n,) + tuple(cache._row)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
+        _on(k, torch.bfloat16, "k", shape, cache.device)
+        _on(v, torch.bfloat16, "v", shape, cache.device)
+        if n:
+            self._check(self._lib.tabit_kv_read(self._h, cache._ref, slots.data_ptr(), n, k.data_ptr(),
+                                                v.data_ptr(), _stream(cache.device)))
+        return k, v
+
+    def kv_attention_workspace(self, cache: KVCache, q: torch.Tensor, num_seqs: int, max_q: int,
+                               max_kv: int) -> Optional[torch.Tensor]:
+        """A workspace for such calls (None where none is needed)."""
+        n = int(self._lib.tabit_kv_attention_workspace_bytes(
+            q.shape[0], q.shape[1], cache.num_kv_heads, cache.head_dim, num_seqs, max_q, max_kv))
+        return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
+
+    def kv_attention(self, cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor,
+                     block_table: torch.Tensor, kv_lens: torch.Tensor, max_q: int, max_kv: int,
+                     scale: Optional[float] = None, causal: bool = False,
+                     rope: Optional[Rope] = None, positions: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                     ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Softmax attention of the ragged query rows q bf16 [T][q_heads][head_dim] over the cache.
+
+        cu_q int32 [B+1] row bounds, block_table int32 [B][pages], kv_lens int32 [B]; max_q and
+        max_kv bound the sequences' rows and keys.  scale defaults to head_dim ** -0.5.  Rows that
+        no sequence covers are left unwritten in `out`; lse fp32 [T][q_heads] is filled if given.
+        """
+        dev = cache.device
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be [tokens][q_heads][head_dim]")
+        T, hq = q.shape[0], q.shape[1]
+        stride = _rows(q, "q", torch.Size((hq, cache.head_dim)), dev)
+        B = kv_lens.shape[0]
+        _on(kv_lens, torch.int32, "kv_lens", (B,), dev)
+        _on(cu_q, torch.int32, "cu_q", (B + 1,), dev)
+        _on(block_table, torch.int32, "block_table", (B, block_table.shape[1]), dev)
+        r, pos = self._rope(cache, rope, positions, T)
+        if out is None:
+            out = torch.empty((T, hq, cache.head_dim), dtype=torch.bfloat16, device=dev)
+        else:
+            _on(out, torch.bfloat16, "out", (T, hq, cache.head_dim), dev)
+        if lse is not None:
+            _on(lse, torch.float32, "lse", (T, hq), dev)
+        if T == 0 or B == 0:
+            return out
+        if ws is None:
+            ws = self.kv_attention_workspace(cache, q, B, max_q, max_kv)
+        elif ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be contiguous and on {dev}")
+        a = _KvAttentionArgs(q.data_ptr(), stride, T, hq, cu_q.data_ptr(), B, max_q,
+                             block_table.data_ptr(), block_table.shape[1], kv_lens.data_ptr(), max_kv,
+                             cache.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0,
+                             r, pos, out.data_ptr(), _ptr(lse), _ptr(ws),
+                             0 if ws is None else ws.numel() * ws.element_size())
+        self._check(self._lib.tabit_kv_attention(self._h, cache._ref, ctypes.addressof(a),
+                                                 _stream(dev)))
+        return out
+
+    def block_norm(self, x: torch.Tensor, y: Optional[torch.Tensor] = None, post: int = NORM_NONE,
+                   post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                   res_scale: float = 1.0, pre: int = NORM_NONE,
+                   pre_weight: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                   shift: Optional[torch.Tensor] = None, eps: float = 1e-6, fmt: int = FMT_BF16,
+                   had_block: int = 0, want_x: bool = True, want_h: bool = True,
+                   x_out: Optional[torch.Tensor] = None):
+        """x' = res_scale x + gate N_post(y); h = N_pre(x') (1 + scale) + shift.
+
+        x, y bf16 [M][H]; weights bf16 [H]; gate, scale, shift bf16 [samples][H] with one row
+        stride for all three (slices of one conditioning output), M a multiple of samples.
+        Returns (x', h, h_scale): h bf16, or int8 with fp32 [M] scales (FMT_INT8), or packed
+        uint8 [M][H/2] with E8M0 uint8 [M][H/32] (FMT_MXFP4); None for what is not wanted.
+        """
+        _dev(x, torch.bfloat16, "x")
+        if x.dim() != 2:
+            raise ValueError("x must be [M][H]")
+        M, H = x.shape
+        dev = x.device
+        if y is not None:
+            _on(y, torch.bfloat16, "y", (M, H), dev)
+        for w, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
+            if w is not None:
+                _on(w, torch.bfloat16, name, (H,), dev)
+        samples, stride = 0, 0
+        for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
+            if t is None:
+                continue
+            if t.dtype != torch.bfloat16:
+                raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+            if t.device != dev or t.dim() != 2 or t.shape[1] != H or t.stride(1) != 1:
+                raise ValueError(f"{name} must be [samples][{H}] on {dev}, its rows contiguous")
+            s = t.stride(0) if t.shape[0] > 1 else H
+            if samples and (t.shape[0] != samples or s != stride):
+                raise ValueError("gate, scale and shift must have the same rows and row stride")
+            samples, stride = t.shape[0], s
+        if samples and M % samples != 0:
+            raise ValueError(f"{M} rows are not a multiple of {samples} samples")
+        if not samples and (gate is not None or scale is not None or shift is not None) and M:
+            raise ValueError("gate, scale and shift must have a row")
+        if x_out is not None:
+            _on(x_out, torch.bfloat16, "x_out", (M, H), dev)
+        elif want_x:
+            x_out = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
+        h = hs = None
+        if want_h:
+            if fmt == FMT_INT8:
+                h = torch.empty((M, H), dtype=torch.int8, device=dev)
+                hs = torch.empty((M,), dtype=torch.float32, device=dev)
+            elif fmt == FMT_MXFP4:
+                h = torch.empty((M, H // 2), dtype=torch.uint8, device=dev)
+                hs = torch.empty((M, H // 32), dtype=torch.uint8, device=dev)
+            else:
+                h = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
+        if M == 0:
+            return x_out, h, hs
+        a = _BlockNormArgs(x.data_ptr(), _ptr(y), M, H, post, pre, _ptr(post_weight), _ptr(pre_weight),
+                           _ptr(gate), _ptr(scale), _ptr(shift), stride, samples,
+                           M // samples if samples else 0, res_scale, eps, _ptr(x_out), _ptr(h),
+                           _ptr(hs), fmt, had_block)
+        self._check(self._lib.tabit_block_norm(self._h, ctypes.addressof(a), _stream(dev)))
+        return x_out, h, hs

@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libtabit.so")
 SOURCES = ["api.hip", "quant.hip", "gemm_i8.hip", "gemm_mxfp4.hip", "gemm_planes.hip", "dmpq.hip",
-           "gemm_hqdm.hip", "probe.hip"]
+           "gemm_hqdm.hip", "probe.hip", "api_block.hip", "kv_cache.hip", "kv_attention.hip",
+           "block_norm.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

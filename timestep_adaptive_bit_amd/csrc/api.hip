@@ -5,12 +5,10 @@
 // kernels on the caller's stream.  No device memory is allocated here.
 #include "../../include/tabit.h"
 
-#include <cstdarg>
-#include <cstdio>
 #include <mutex>
 #include <new>
 
-#include "tabit_internal.h"
+#include "api_common.h"
 
 namespace {
 
@@ -18,25 +16,6 @@ constexpr int kMaxK = 32768;
 // Buffer descriptors address operands with 32-bit byte offsets; the top bit marks
 // out-of-range reads, so every operand stays below 2^31 bytes.
 constexpr size_t kMaxOperandBytes = 0x7FFFFFFFu;
-
-int fail(tabit_ctx* ctx, int status, const char* fmt, ...) {
-  if (ctx != nullptr) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
-    va_end(ap);
-    ctx->err = buf;
-  }
-  return status;
-}
-
-int hip_status(tabit_ctx* ctx, hipError_t e, const char* what) {
-  if (e == hipSuccess) return TABIT_OK;
-  return fail(ctx, TABIT_EHIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 bool valid_block(int b) { return b == 0 || b == 32 || b == 64 || b == 128; }
 

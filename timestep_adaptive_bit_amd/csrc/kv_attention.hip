@@ -1,0 +1,449 @@
+// Attention over the paged MXFP4 cache.
+//
+//   s_j = c q'.k'_j,  p_j = softmax over the visible keys,  o = (1/32) H32 sum_j p_j v'_j
+//
+// with q' = H32 R(pos) q padded to blocks of 32 (H32 and the 1/32 only for a
+// rotated cache: H32 H32 = 32, so c = scale / 32 and the output is turned back
+// once per row).  Keys j < len are visible, with `causal` also only j <= len - n + i
+// to query i of the n of a sequence.  A row that sees no key answers 0.
+//
+// Rows of one key head are packed as (query, head of the group), so the heads
+// that share keys share every byte read of them.  A wave takes 64 keys at a time
+// and 16 rows:
+//
+//   scores  S = K Q'^T with the 16x16x128 block-scaled MFMA: the key codes go from
+//           memory into the matrix core as they are stored (lane l holds one MX
+//           block: key l%16, block l/16), scaled by their E8M0 bytes in the
+//           instruction.  q' is three FP6 (E2M3) terms with scales 2^e, 2^(e-4),
+//           2^(e-8) per block of 32: what is left of an element is below 2^-13 of
+//           the block's largest one, less than bf16 would lose, at 3/4 of the
+//           matrix time of one bf16 product.
+//   softmax every lane holds one row (l%16) and 16 of the 64 keys, in fp32, base 2,
+//           with a running maximum and sum.
+//   values  O^T += V^T P^T with the 16x16x32 bf16 MFMA.  The order of the summed
+//           keys is free, so it is chosen as the lanes already hold them: P needs
+//           no exchange, only its rounding to bf16 (2^-9 a weight: the sums stay in
+//           fp32).  V becomes bf16 exactly (a code has 2 bits) through LDS, and is
+//           read transposed by ds_read_b64_tr_b16.
+//
+// Long caches are split over workgroups (`splits` ranges of whole 64-key tiles of
+// each sequence's own length) whose fp32 partial sums a second kernel joins.
+#include "../../include/tabit.h"
+#include "kv_common.h"
+
+namespace tabit {
+namespace {
+
+using namespace kv;
+
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s* lds_v4s;
+
+constexpr float kNegInf = -__builtin_inff();
+constexpr int TILE = 64;      // keys a wave takes at a time
+constexpr int NUM_CUS = 256;  // MI355X
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Byte offset of 16-element run `c` (32 bytes) of key row `key` in the bf16 value
+// tile: rows of RS bytes, the run index XORed with the row so that the 16 rows one
+// transposed read touches fall on different banks.
+template <int RS>
+__device__ __forceinline__ int v_off(int key, int c) {
+  constexpr int RUNS = RS / 32;
+  const int x = RUNS == 8 ? (key & 7) : ((key >> 1) & 3);
+  return key * RS + ((c ^ x) << 5);
+}
+
+// 32 elements of a query row (block `blk` of the head vector), rotated and
+// transformed as the cache's keys are.
+__device__ __forceinline__ bool load_q_block(const KvAttnArgs& a, int token, int head, int blk,
+                                             float (&x)[32]) {
+  const uint16_t* p = a.q + (long long)token * a.q_stride + (long long)head * a.cache.head_dim;
+  RopeArgs rope = a.rope;
+  bool ok = true;
+  int pos = 0;
+  if (rope.rope_dim > 0) {
+    pos = a.positions[token];
+    if (pos < 0 || pos >= rope.num_positions) {
+      ok = false;
+      rope.rope_dim = 0;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e0 = blk * 32 + i * 8;
+    float v[8] = {};
+    if (e0 < a.cache.head_dim) load8_turned(p, e0, rope, pos, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[i * 8 + e] = v[e];
+  }
+  if (a.cache.had) fwht32_lane(x);
+#pragma unroll
+  for (int e = 0; e < 32; ++e) ok &= finite_f32(x[e]);
+  return ok;
+}
+
+// Three FP6 terms of a block of 32 with their E8M0 bytes (bytes 0..2 of `scales`).
+// A block that is not finite gets scale 255: its row answers NaN.
+__device__ __forceinline__ void q_terms(float (&x)[32], bool ok, v8i (&q)[3], uint32_t& scales) {
+  float top = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(x[e]));
+  const int ex = max(mx_exponent(top), -119);
+  scales = 0u;
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    const int E = ex - 4 * t + 127;
+    const float s = __uint_as_float((uint32_t)E << 23);
+    v16f lo, hi;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      lo[e] = ok ? x[2 * e] : 0.0f;
+      hi[e] = ok ? x[2 * e + 1] : 0.0f;
+    }
+    const v6u w = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(lo, hi, s);
+    const v32f d = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(w, s);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] -= d[e];
+    q[t] = v8i{(int)w[0], (int)w[1], (int)w[2], (int)w[3], (int)w[4], (int)w[5], 0, 0};
+    scales |= (uint32_t)(ok ? E : 255) << (8 * t);
+  }
+}
+
+// The range of tiles [t0, t1) of split `sp`, of `tiles` tiles in all.
+__device__ __forceinline__ void split_range(int tiles, int splits, int sp, int& t0, int& t1) {
+  const int per = (tiles + splits - 1) / splits;
+  t0 = min(sp * per, tiles);
+  t1 = min(t0 + per, tiles);
+}
+
+// First query row and number of queries of sequence b, inside [0, tokens].
+__device__ __forceinline__ void seq_rows(const KvAttnArgs& a, int b, int& q0, int& n) {
+  q0 = min(max(a.cu_q[b], 0), a.tokens);
+  n = min(max(a.cu_q[b + 1] - q0, 0), min(a.max_q, a.tokens - q0));
+}
+
+__device__ __forceinline__ int seq_keys(const KvAttnArgs& a, int b) {
+  return min(max(a.kv_lens[b], 0), a.max_kv);
+}
+
+// Keys that query i of n sees, of `len`.
+__device__ __forceinline__ int seen_keys(const KvAttnArgs& a, int len, int n, int i) {
+  return a.causal ? min(max(len - n + i + 1, 0), len) : len;
+}
+
+// One workgroup: 16 rows (queries x heads of the group) of one key head of one
+// sequence over one range of its keys; the range's tiles go to the waves in runs.
+template <int NB, int NW>
+__global__ void __launch_bounds__(NW * 64)
+kv_attention_rows16_kernel(KvAttnArgs a) {
+  constexpr int DP = NB * 32;
+  constexpr int RS = NB <= 2 ? 128 : 256;             // bytes of a staged value row
+  constexpr int STAGE = TILE * RS;
+  constexpr int MERGE = 16 * (DP + 4) * 4;            // one wave's sums, rows padded against banks
+  constexpr int PER_WAVE = STAGE > MERGE ? STAGE : MERGE;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NW * PER_WAVE + NW * 16 * 8];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int row = lane & 15, g = lane >> 4;
+  const int b = blockIdx.z, hk = blockIdx.y;
+  const int sp = blockIdx.x % a.splits, row_tile = blockIdx.x / a.splits;
+  const KvCacheArgs& c = a.cache;
+
+  int q0, n;
+  seq_rows(a, b, q0, n);
+  const int r0 = row_tile * 16;
+  if (r0 >= n * a.group) return;
+  const int len = seq_keys(a, b);
+  const int qi = (r0 + row) / a.group, qh = hk * a.group + (r0 + row) % a.group;
+  const bool row_ok = qi < n;
+  const int seen = row_ok ? seen_keys(a, len, n, qi) : 0;
+  int seen_max = seen;
+#pragma unroll
+  for (int m = 8; m > 0; m >>= 1) seen_max = max(seen_max, __shfl_xor(seen_max, m, 64));
+
+  // B operand: row l%16, block l/16
+  v8i q[3] = {};
+  uint32_t q_scales = 0u;
+  if (row_ok && g < NB) {
+    float x[32];
+    const bool ok = load_q_block(a, q0 + qi, qh, g, x);
+    q_terms(x, ok, q, q_scales);
+  }
+
+  const int tiles = (seen_max + TILE - 1) / TILE;
+  int t0, t1;
+  split_range(tiles, a.splits, sp, t0, t1);
+  const int per = (t1 - t0 + NW - 1) / NW;
+  const int w0 = min(t0 + wave * per, t1), w1 = min(w0 + per, t1);
+  const float scale2 = a.scale * 1.4426950408889634f / (c.had ? 32.0f : 1.0f);
+  const int page_size = 1 << c.page_shift;
+
+  float m = kNegInf, l = 0.0f;
+  v4f o[DP / 16];
+#pragma unroll
+  for (int d = 0; d < DP / 16; ++d) o[d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  uint8_t* stage = smem + wave * PER_WAVE;
+
+  for (int t = w0; t < w1; ++t) {
+    const int j0 = t * TILE;
+    // pages of the tile's four groups of 16 keys
+    long long base[4];
+    bool there[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = j0 + 16 * k;
+      const int pi = j >> c.page_shift;
+      int page = -1;
+      if (j < len && pi < a.table_stride) page = a.table[(long long)b * a.table_stride + pi];
+      there[k] = page >= 0 && page < c.num_pages;
+      base[k] = there[k] ? ((((long long)page * c.heads + hk) << c.page_shift) + (j & (page_size - 1))) : 0;
+    }
+    // scores: 16 keys an instruction
+    v4f s[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v4i kc = {0, 0, 0, 0};
+      int ks = 127;
+      if (there[k] && g < NB) {
+        const long long r = base[k] + row;
+        kc = *reinterpret_cast<const v4i*>(c.k_codes + r * (DP / 2) + g * 16);
+        ks = c.k_scales[r * NB + g];
+      }
+      const v8i ka = {kc[0], kc[1], kc[2], kc[3], 0, 0, 0, 0};
+      s[k] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      s[k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ka, q[0], s[k], 4, 2, 0, ks, 0, (int)q_scales);
+      s[k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ka, q[1], s[k], 4, 2, 0, ks, 1, (int)q_scales);
+      s[k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ka, q[2], s[k], 4, 2, 0, ks, 2, (int)q_scales);
+    }
+    // values to bf16 in LDS: one MX block a lane and step; keys past the end as zeros
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int u = i * 64 + lane, key = u / NB, blk = u % NB, k = key >> 4;
+      v4i vc = {0, 0, 0, 0};
+      uint32_t vs = 127u;
+      const long long bk = k == 0 ? base[0] : k == 1 ? base[1] : k == 2 ? base[2] : base[3];
+      const bool tk = k == 0 ? there[0] : k == 1 ? there[1] : k == 2 ? there[2] : there[3];
+      if (tk && j0 + key < len) {
+        const long long r = bk + (key & 15);
+        vc = *reinterpret_cast<const v4i*>(c.v_codes + r * (DP / 2) + blk * 16);
+        vs = c.v_scales[r * NB + blk];
+      }
+      const float f = __uint_as_float(vs << 23);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t x = (uint32_t)vc[w];
+        uint4 y;
+        y.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 0));
+        y.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 1));
+        y.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 2));
+        y.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 3));
+        *reinterpret_cast<uint4*>(stage + v_off<RS>(key, blk * 2 + (w >> 1)) + (w & 1) * 16) = y;
+      }
+    }
+    // softmax: lane holds keys 16 k + 4 g + r of its row
+    float top = kNegInf;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool vis = there[k] && j0 + 16 * k + 4 * g + r < seen;
+        s[k][r] = vis ? s[k][r] * scale2 : kNegInf;
+        top = fmaxf(top, s[k][r]);
+      }
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const float m_new = fmaxf(m, top);
+    const float ref = m_new == kNegInf ? 0.0f : m_new;
+    const float alpha = exp2_fast(m - ref);
+    m = m_new;
+    l *= alpha;
+#pragma unroll
+    for (int d = 0; d < DP / 16; ++d) o[d] *= alpha;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        s[k][r] = exp2_fast(s[k][r] - ref);
+        l += s[k][r];
+      }
+    // values: the wave's own staging, written above
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v8bf p;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        p[r] = (__bf16)s[2 * h][r];
+        p[4 + r] = (__bf16)s[2 * h + 1][r];
+      }
+#pragma unroll
+      for (int d = 0; d < DP / 16; ++d) {
+        const int key = 32 * h + 4 * g + (row >> 2);
+        const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_v4s)(stage + v_off<RS>(key, d) + (row & 3) * 8));
+        const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_v4s)(stage + v_off<RS>(key + 16, d) + (row & 3) * 8));
+        const v8bf v = __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p, o[d], 0, 0, 0);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    __builtin_amdgcn_wave_barrier();
+  }
+  l += __shfl_xor(l, 16, 64);
+  l += __shfl_xor(l, 32, 64);
+
+  // join the waves: sums to LDS as [row][d], then 16 rows x NB blocks
+  float* sums = reinterpret_cast<float*>(stage);
+  float* ml = reinterpret_cast<float*>(smem + NW * PER_WAVE);
+#pragma unroll
+  for (int d = 0; d < DP / 16; ++d)
+    *reinterpret_cast<v4f*>(sums + row * (DP + 4) + d * 16 + g * 4) = o[d];
+  if (g == 0) {
+    ml[(wave * 16 + row) * 2] = m;
+    ml[(wave * 16 + row) * 2 + 1] = l;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x >= 16 * NB) return;
+  const int fr = threadIdx.x / NB, fb = threadIdx.x % NB;
+  const int fi = (r0 + fr) / a.group, fh = hk * a.group + (r0 + fr) % a.group;
+  if (fi >= n) return;
+  float M = kNegInf;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * 16 + fr) * 2]);
+  const float ref = M == kNegInf ? 0.0f : M;
+  float x[32], L = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) x[e] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const float f = exp2_fast(ml[(w * 16 + fr) * 2] - ref);
+    L += f * ml[(w * 16 + fr) * 2 + 1];
+    const float* src = reinterpret_cast<const float*>(smem + w * PER_WAVE) + fr * (DP + 4) + fb * 32;
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      const v4f y = *reinterpret_cast<const v4f*>(src + e);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[e + k] += f * y[k];
+    }
+  }
+  const long long out_row = (long long)(q0 + fi) * a.q_heads + fh;
+  if (a.splits > 1) {
+    const long long rows = (long long)a.tokens * a.q_heads;
+    float* dst = a.part + ((long long)sp * rows + out_row) * DP + fb * 32;
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) *reinterpret_cast<v4f*>(dst + e) = v4f{x[e], x[e + 1], x[e + 2], x[e + 3]};
+    if (fb == 0) {
+      float* st = a.part + (long long)a.splits * rows * DP + ((long long)sp * rows + out_row) * 2;
+      st[0] = M;
+      st[1] = L;
+    }
+    return;
+  }
+  const float inv = L == 0.0f ? 0.0f : (c.had ? 0.03125f : 1.0f) / L;   // no visible key: 0
+  if (c.had) fwht32_lane(x);
+#pragma unroll
+  for (int e = 0; e < 32; e += 8) {
+    const int d = fb * 32 + e;
+    if (d < c.head_dim)
+      *reinterpret_cast<uint4*>(a.out + out_row * c.head_dim + d) =
+          make_uint4(pack_bf16(x[e] * inv, x[e + 1] * inv), pack_bf16(x[e + 2] * inv, x[e + 3] * inv),
+                     pack_bf16(x[e + 4] * inv, x[e + 5] * inv), pack_bf16(x[e + 6] * inv, x[e + 7] * inv));
+  }
+  if (a.lse != nullptr && fb == 0)
+    a.lse[out_row] = L == 0.0f ? kNegInf : (M + __builtin_log2f(L)) * 0.6931471805599453f;
+}
+
+// Joins the splits of each row: a lane holds four elements of one row, eight
+// lanes a block of 32.
+template <int NB>
+__global__ void __launch_bounds__(256)
+kv_attention_join_kernel(KvAttnArgs a) {
+  constexpr int DP = NB * 32;
+  constexpr int LPR = 8 * NB;              // lanes of a row
+  constexpr int RPW = 256 / LPR;           // rows of a workgroup
+  const int b = blockIdx.y;
+  int q0, n;
+  seq_rows(a, b, q0, n);
+  const int lr = threadIdx.x / LPR, li = threadIdx.x % LPR, lane = threadIdx.x & 63;
+  const int r = blockIdx.x * RPW + lr;
+  const bool ok = lr < RPW && r < n * a.q_heads;
+  const KvCacheArgs& c = a.cache;
+  const long long rows = (long long)a.tokens * a.q_heads;
+  const long long row = (long long)q0 * a.q_heads + (ok ? r : 0);
+  const float* st = a.part + (long long)a.splits * rows * DP;
+  float M = kNegInf, L = 0.0f;
+  v4f x = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (ok) {
+    for (int s = 0; s < a.splits; ++s) M = fmaxf(M, st[(s * rows + row) * 2]);
+    const float ref = M == kNegInf ? 0.0f : M;
+    for (int s = 0; s < a.splits; ++s) {
+      const float f = exp2_fast(st[(s * rows + row) * 2] - ref);
+      L += f * st[(s * rows + row) * 2 + 1];
+      x += f * *reinterpret_cast<const v4f*>(a.part + (s * rows + row) * DP + li * 4);
+    }
+  }
+  if (c.had) {
+    float v[4] = {x[0], x[1], x[2], x[3]};
+    const float a0 = v[0] + v[1], a1 = v[0] - v[1], a2 = v[2] + v[3], a3 = v[2] - v[3];
+    v[0] = a0 + a2; v[1] = a1 + a3; v[2] = a0 - a2; v[3] = a1 - a3;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float y = lane_xor<1>(v[e]);
+      v[e] = (lane & 1) ? y - v[e] : v[e] + y;
+      y = lane_xor<2>(v[e]);
+      v[e] = (lane & 2) ? y - v[e] : v[e] + y;
+      y = lane_xor<4>(v[e]);
+      v[e] = (lane & 4) ? y - v[e] : v[e] + y;
+    }
+    x = v4f{v[0], v[1], v[2], v[3]};
+  }
+  if (!ok) return;
+  const float inv = L == 0.0f ? 0.0f : (c.had ? 0.03125f : 1.0f) / L;
+  if (li * 4 < c.head_dim)
+    *reinterpret_cast<uint2*>(a.out + row * c.head_dim + li * 4) =
+        make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+  if (a.lse != nullptr && li == 0)
+    a.lse[row] = L == 0.0f ? kNegInf : (M + __builtin_log2f(L)) * 0.6931471805599453f;
+}
+
+template <int NB>
+hipError_t launch_nb(const KvAttnArgs& a, hipStream_t s) {
+  constexpr int NW = 4;
+  const int row_tiles = (int)(((long long)a.max_q * a.group + 15) / 16);
+  const dim3 grid((unsigned)((long long)row_tiles * a.splits), (unsigned)a.cache.heads, (unsigned)a.seqs);
+  kv_attention_rows16_kernel<NB, NW><<<grid, NW * 64, 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  constexpr int RPW = 256 / (8 * NB);
+  const dim3 jgrid((unsigned)(((long long)a.max_q * a.q_heads + RPW - 1) / RPW), (unsigned)a.seqs);
+  kv_attention_join_kernel<NB><<<jgrid, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int kv_attention_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_kv) {
+  if (seqs <= 0 || max_q <= 0 || kv_heads <= 0) return 1;
+  const long long row_tiles = ((long long)max_q * (q_heads / kv_heads) + 15) / 16;
+  const long long base = (long long)seqs * kv_heads * row_tiles;
+  const long long tiles = ((long long)max_kv + TILE - 1) / TILE;
+  long long want = (4ll * NUM_CUS + base - 1) / base;
+  want = want < (tiles + 3) / 4 ? want : (tiles + 3) / 4;
+  if (want > 128) want = 128;
+  return want < 1 ? 1 : (int)want;
+}
+
+hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t s) {
+  switch (a.cache.dim_pad) {
+    case 32: return launch_nb<1>(a, s);
+    case 64: return launch_nb<2>(a, s);
+    case 96: return launch_nb<3>(a, s);
+    case 128: return launch_nb<4>(a, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace tabit

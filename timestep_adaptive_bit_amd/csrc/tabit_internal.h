@@ -101,6 +101,67 @@ hipError_t launch_dmpq_select(const uint16_t* xin, const uint16_t* xout, int M, 
                               const float* theta, int n_layers, uint8_t* fmt, double* gamma,
                               hipStream_t s);
 
+// ---------------------------------------------------------------- paged MXFP4 cache
+// Arrays [num_pages][heads][2^page_shift][dim_pad/2 or dim_pad/32]; dim_pad =
+// 32 ceil(head_dim / 32); had: rows hold H32 of the padded vectors.
+struct KvCacheArgs {
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  int num_pages, page_shift, heads, head_dim, dim_pad, had;
+};
+// Rotation tables [num_positions][rope_dim/2]; rope_dim 0: no rotation.
+struct RopeArgs {
+  const float *cos, *sin;
+  int num_positions, rope_dim, interleaved;
+};
+hipError_t launch_kv_append(const KvCacheArgs& c, const uint16_t* k, long long k_stride,
+                            const uint16_t* v, long long v_stride, int tokens,
+                            const int64_t* slots, const RopeArgs& rope, const int* positions,
+                            hipStream_t s);
+hipError_t launch_kv_read(const KvCacheArgs& c, const int64_t* slots, int tokens, uint16_t* k,
+                          uint16_t* v, hipStream_t s);
+
+// Attention of packed query rows over the cache.  `part` holds, when splits > 1,
+// splits x tokens x q_heads partial results: dim_pad sums each, then (max, sum).
+struct KvAttnArgs {
+  KvCacheArgs cache;
+  RopeArgs rope;
+  const uint16_t* q;
+  long long q_stride;
+  int tokens, q_heads, group;
+  const int* cu_q;
+  int seqs, max_q;
+  const int* table;
+  int table_stride;
+  const int* kv_lens;
+  int max_kv;
+  float scale;
+  int causal;
+  const int* positions;
+  uint16_t* out;
+  float* lse;
+  float* part;
+  int splits;
+};
+// Number of ranges the keys of one sequence are split into for this problem.
+int kv_attention_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_kv);
+hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------- block norms
+struct BlockNormArgs {
+  const uint16_t *x, *y;
+  int rows, width;
+  int post_kind, pre_kind;              // TABIT_NORM_*
+  const uint16_t *post_w, *pre_w;       // [width] or null
+  const uint16_t *gate, *scale, *shift; // [samples][mod_stride] or null
+  long long mod_stride;
+  int rows_per_sample;
+  float res_scale, eps;
+  uint16_t* x_out;                      // may be null
+  void *h, *h_scale;                    // may be null
+  int fmt, had;
+};
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t s);
+
 // ---------------------------------------------------------------- matrix-core rate probe
 // kind 0: INT8 32x32x32 MFMA; kind 1: FP4 32x32x64 scaled MFMA.  sink holds
 // mfma_probe_sink_ints(num_cus) ints.  Returns the operations the launch performs.
