@@ -30,6 +30,7 @@
 // each sequence's own length) whose fp32 partial sums a second kernel joins.
 #include "../../include/tabit.h"
 #include "kv_common.h"
+#include "tile_common.h"
 
 namespace tabit {
 namespace {
@@ -56,7 +57,8 @@ __device__ __forceinline__ int v_off(int key, int c) {
 }
 
 // 32 elements of a query row (block `blk` of the head vector), rotated and
-// transformed as the cache's keys are.
+// transformed as the cache's keys are, negated for a negative scale (the kernels
+// then scale by its magnitude, so the largest score is the largest product).
 __device__ __forceinline__ bool load_q_block(const KvAttnArgs& a, int token, int head, int blk,
                                              float (&x)[32]) {
   const uint16_t* p = a.q + (long long)token * a.q_stride + (long long)head * a.cache.head_dim;
@@ -79,8 +81,12 @@ __device__ __forceinline__ bool load_q_block(const KvAttnArgs& a, int token, int
     for (int e = 0; e < 8; ++e) x[i * 8 + e] = v[e];
   }
   if (a.cache.had) fwht32_lane(x);
+  if (a.scale < 0.0f) {
 #pragma unroll
-  for (int e = 0; e < 32; ++e) ok &= finite_f32(x[e]);
+    for (int e = 0; e < 32; ++e) x[e] = -x[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 32; ++e) ok = ok && finite_f32(x[e]);
   return ok;
 }
 
@@ -133,6 +139,12 @@ __device__ __forceinline__ int seen_keys(const KvAttnArgs& a, int len, int n, in
   return a.causal ? min(max(len - n + i + 1, 0), len) : len;
 }
 
+// Factor of the products q'.k' that gives scores in base 2.  Not quite zero, so that a
+// masked key's -inf stays one under a scale of zero.
+__device__ __forceinline__ float base2_scale(const KvAttnArgs& a) {
+  return fmaxf(fabsf(a.scale) * 1.4426950408889634f / (a.cache.had ? 32.0f : 1.0f), 0x1p-120f);
+}
+
 // One workgroup: 16 rows (queries x heads of the group) of one key head of one
 // sequence over one range of its keys; the range's tiles go to the waves in runs.
 template <int NB, int NW>
@@ -176,7 +188,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   split_range(tiles, a.splits, sp, t0, t1);
   const int per = (t1 - t0 + NW - 1) / NW;
   const int w0 = min(t0 + wave * per, t1), w1 = min(w0 + per, t1);
-  const float scale2 = a.scale * 1.4426950408889634f / (c.had ? 32.0f : 1.0f);
+  const float scale2 = base2_scale(a);
   const int page_size = 1 << c.page_shift;
 
   float m = kNegInf, l = 0.0f;
@@ -356,6 +368,308 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
     a.lse[out_row] = L == 0.0f ? kNegInf : (M + __builtin_log2f(L)) * 0.6931471805599453f;
 }
 
+// Both halves' values of a lane pair (l, l ^ 32), in the order (lanes 0..31, 32..63).
+__device__ __forceinline__ void halves(float v, float& lo, float& hi) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  lo = __uint_as_float(r[0]);
+  hi = __uint_as_float(r[1]);
+}
+
+// One workgroup: 128 rows of one key head of one sequence, 32 a wave, over one range
+// of its keys.  The 64 keys of a tile are brought in once for all rows: codes and
+// scales through registers (loaded a tile ahead, their pages two ahead) into one of
+// two LDS stages, the values already as bf16, one barrier a tile.  A wave uses the
+// 32x32 forms of the same products: scores with 32x32x64 (lane l: one row, l%32, and
+// 32 of the 64 keys), values with 32x32x16, P staying in its lanes.  The running
+// maximum is raised only when a score exceeds it by 2^8, so most tiles rescale
+// nothing; sums stay below 2^8 times their true size.
+template <int NB>
+__global__ void __launch_bounds__(256, 2)
+kv_attention_rows128_kernel(KvAttnArgs a) {
+  constexpr int DP = NB * 32;
+  constexpr int ND = DP / 32;                        // 32-element output blocks
+  constexpr int NS = (NB + 1) / 2;                   // 64-element steps of a score
+  constexpr int RS = NB <= 2 ? 128 : 256;            // bytes of a staged value row
+  constexpr int KB = TILE * DP / 2;                  // bytes of a tile's key codes
+  constexpr int UNITS = TILE * NB;                   // MX blocks of a tile's keys (or values)
+  struct Stage {
+    uint8_t v[TILE * RS];
+    uint8_t k[KB];
+    uint8_t ks[2][32][4];                            // [block % 2][key % 32][key / 32 * 2 + block / 2]
+    int there[4];
+  };
+  __shared__ __attribute__((aligned(1024))) Stage st[2];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int row = lane & 31, half = lane >> 5;
+  const int b = blockIdx.z, hk = blockIdx.y;
+  const int sp = blockIdx.x % a.splits, row_tile = blockIdx.x / a.splits;
+  const KvCacheArgs& c = a.cache;
+
+  int q0, n;
+  seq_rows(a, b, q0, n);
+  const int rows = n * a.group;
+  // the last rows of a causal sequence see most: they start first
+  const int tiles_r = (rows + 127) / 128;
+  if (row_tile >= tiles_r) return;
+  const int r0 = (tiles_r - 1 - row_tile) * 128;
+  const int len = seq_keys(a, b);
+  const int rr = r0 + wave * 32 + row;
+  const bool row_ok = rr < rows;
+  const int qi = rr / a.group, qh = hk * a.group + rr % a.group;
+  const int seen_all = seen_keys(a, len, n, (min(r0 + 128, rows) - 1) / a.group);
+  const int seen = row_ok ? seen_keys(a, len, n, qi) : seen_all;   // idle rows mask nothing
+  const int first = r0 + wave * 32;
+  const int seen_lo = seen_keys(a, len, n, min(first, rows - 1) / a.group);
+  const int seen_hi = first < rows ? seen_keys(a, len, n, min(first + 31, rows - 1) / a.group) : 0;
+
+  // B operands: row l%32, block l/32 of each 64-element step
+  v8i q[NS][3];
+  uint32_t q_scales[NS];
+#pragma unroll
+  for (int ds = 0; ds < NS; ++ds) {
+    q_scales[ds] = 0u;
+#pragma unroll
+    for (int t = 0; t < 3; ++t) q[ds][t] = v8i{0, 0, 0, 0, 0, 0, 0, 0};
+    const int blk = 2 * ds + half;
+    if (row_ok && blk < NB) {
+      float x[32];
+      const bool ok = load_q_block(a, q0 + qi, qh, blk, x);
+      q_terms(x, ok, q[ds], q_scales[ds]);
+    }
+  }
+
+  int t0, t1;
+  split_range((seen_all + TILE - 1) / TILE, a.splits, sp, t0, t1);
+  const float scale2 = base2_scale(a);
+  const int in_page = (1 << c.page_shift) - 1;
+
+  // what this thread brings in: key block `tid`, value block `255 - tid`
+  const bool has_k = tid < UNITS, has_v = 255 - tid < UNITS;
+  const int kkey = tid / NB, kblk = tid % NB, vkey = (255 - tid) / NB, vblk = (255 - tid) % NB;
+  const int* table = a.table + (long long)b * a.table_stride;
+  auto page_of = [&](int j) -> int {
+    const int pi = j >> c.page_shift;
+    return j < len && pi < a.table_stride ? table[pi] : -1;
+  };
+  int kpage, vpage;
+  v4i kc, vc;
+  uint32_t ks, vs;
+  bool kthere;
+  auto fetch = [&](int t) {     // codes and scales of tile t through the pages at hand
+    kc = vc = v4i{0, 0, 0, 0};
+    ks = vs = 127u;
+    const int jk = t * TILE + kkey, jv = t * TILE + vkey;
+    kthere = kpage >= 0 && kpage < c.num_pages;
+    if (kthere) {
+      const long long r = (((long long)kpage * c.heads + hk) << c.page_shift) + (jk & in_page);
+      kc = *reinterpret_cast<const v4i*>(c.k_codes + r * (DP / 2) + kblk * 16);
+      ks = c.k_scales[r * NB + kblk];
+    }
+    if (vpage >= 0 && vpage < c.num_pages) {
+      const long long r = (((long long)vpage * c.heads + hk) << c.page_shift) + (jv & in_page);
+      vc = *reinterpret_cast<const v4i*>(c.v_codes + r * (DP / 2) + vblk * 16);
+      vs = c.v_scales[r * NB + vblk];
+    }
+  };
+  // 16-byte block `blk` of key row `key`: rows share a 256-byte bank window, the XOR
+  // spreads the 16 rows one read touches over it (48-byte rows spread by themselves)
+  auto k_off = [](int key, int blk) {
+    if constexpr (NB == 4) return key * 64 + ((blk ^ ((key >> 2) & 3)) << 4);
+    else if constexpr (NB == 2) return key * 32 + ((blk ^ ((key >> 3) & 1)) << 4);
+    else return key * (DP / 2) + (blk << 4);
+  };
+
+  float m = kNegInf, l = 0.0f;
+  v16f o[ND];
+#pragma unroll
+  for (int d = 0; d < ND; ++d) o[d] = v16f{};
+
+  auto next_pages = [&](int t) {
+    kpage = has_k && t < t1 ? page_of(t * TILE + kkey) : -1;
+    vpage = has_v && t < t1 ? page_of(t * TILE + vkey) : -1;
+  };
+  next_pages(t0);
+  fetch(t0);
+  next_pages(t0 + 1);
+  if constexpr (NB % 2 != 0) {   // scale bytes of blocks that do not exist: any finite scale
+    for (int i = tid; i < 64; i += 256) {
+      reinterpret_cast<uint32_t*>(st[0].ks)[i] = 0x7F7F7F7Fu;
+      reinterpret_cast<uint32_t*>(st[1].ks)[i] = 0x7F7F7F7Fu;
+    }
+    __syncthreads();
+  }
+  for (int t = t0; t < t1; ++t) {
+    Stage& s = st[(t - t0) & 1];
+    if (has_k) {
+      *reinterpret_cast<v4i*>(s.k + k_off(kkey, kblk)) = kc;
+      s.ks[kblk & 1][kkey & 31][(kkey >> 5) * 2 + (kblk >> 1)] = (uint8_t)ks;
+      if ((kkey & 15) == 0 && kblk == 0) s.there[kkey >> 4] = kthere;
+    }
+    if (has_v) {
+      const float f = __uint_as_float(vs << 23);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t x = (uint32_t)vc[w];
+        uint4 y;
+        y.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 0));
+        y.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 1));
+        y.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 2));
+        y.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 3));
+        *reinterpret_cast<uint4*>(s.v + v_off<RS>(vkey, vblk * 2 + (w >> 1)) + (w & 1) * 16) = y;
+      }
+    }
+    fetch(t + 1);              // past the range: no pages, no loads
+    next_pages(t + 2);
+    tile::lds_barrier();
+    const int j0 = t * TILE;
+    if (j0 >= seen_hi) continue;                     // no row of the wave sees the tile
+
+    v16f sc[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      sc[kb] = v16f{};
+      const int ksw = *reinterpret_cast<const int*>(s.ks[half][row]);
+#pragma unroll
+      for (int ds = 0; ds < NS; ++ds) {
+        const int blk = 2 * ds + half;
+        v4i x = {0, 0, 0, 0};
+        if (NB % 2 == 0 || blk < NB) x = *reinterpret_cast<const v4i*>(s.k + k_off(kb * 32 + row, blk));
+        const v8i ka = {x[0], x[1], x[2], x[3], 0, 0, 0, 0};
+#define TABIT_QK(T_)                                                                                     \
+  sc[kb] = kb == 0 ? (ds == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                          \
+                                    ka, q[ds][T_], sc[kb], 4, 2, 0, ksw, T_, (int)q_scales[ds])           \
+                              : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                          \
+                                    ka, q[ds][T_], sc[kb], 4, 2, 1, ksw, T_, (int)q_scales[ds]))          \
+                   : (ds == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                          \
+                                    ka, q[ds][T_], sc[kb], 4, 2, 2, ksw, T_, (int)q_scales[ds])           \
+                              : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                          \
+                                    ka, q[ds][T_], sc[kb], 4, 2, 3, ksw, T_, (int)q_scales[ds]));
+        TABIT_QK(0) TABIT_QK(1) TABIT_QK(2)
+#undef TABIT_QK
+      }
+    }
+    // lane: keys 32 kb + 8 (r / 4) + 4 half + r % 4 of its row
+    const v4i there = *reinterpret_cast<const v4i*>(s.there);
+    const bool whole = (there[0] & there[1] & there[2] & there[3]) != 0;
+    if (j0 + TILE > seen_lo || !whole) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int key = kb * 32 + (r >> 2) * 8 + half * 4 + (r & 3);
+          if (j0 + key >= seen || there[kb * 2 + (r >> 3)] == 0) sc[kb][r] = kNegInf;
+        }
+    }
+    float top = kNegInf;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) top = fmaxf(fmaxf(top, sc[0][r]), sc[1][r]);
+    float tl, th;
+    halves(top, tl, th);
+    top = fmaxf(tl, th) * scale2;
+    if (__any(top > m + 8.0f)) {
+      const float m_new = fmaxf(m, top);
+      const float ref = m_new == kNegInf ? 0.0f : m_new;
+      const float alpha = exp2_fast(m - ref);
+      m = m_new;
+      l *= alpha;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[d] *= alpha;
+    }
+    const float ref = m == kNegInf ? 0.0f : m;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        sc[kb][r] = exp2_fast(__builtin_fmaf(sc[kb][r], scale2, -ref));
+        l += sc[kb][r];
+      }
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        v8bf p;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) p[r] = (__bf16)sc[kb][8 * u + r];
+        const int key = kb * 32 + 16 * u + 4 * half + ((lane & 15) >> 2);
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          const int run = 2 * d + ((lane >> 4) & 1);
+          const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_v4s)(s.v + v_off<RS>(key, run) + (lane & 3) * 8));
+          const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_v4s)(s.v + v_off<RS>(key + 8, run) + (lane & 3) * 8));
+          const v8bf v = __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p, o[d], 0, 0, 0);
+        }
+      }
+  }
+  {
+    float lo, hi;
+    halves(l, lo, hi);
+    l = lo + hi;
+  }
+  // lane: elements 32 d + 8 (r / 4) + 4 half + r % 4 of its row
+  const long long out_row = (long long)(q0 + qi) * a.q_heads + qh;
+  if (a.splits > 1) {
+    if (!row_ok) return;
+    const long long all = (long long)a.tokens * a.q_heads;
+    float* dst = a.part + ((long long)sp * all + out_row) * DP + half * 4;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<v4f*>(dst + d * 32 + g * 8) =
+            v4f{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
+    if (half == 0) {
+      float* ml = a.part + (long long)a.splits * all * DP + ((long long)sp * all + out_row) * 2;
+      ml[0] = m;
+      ml[1] = l;
+    }
+    return;
+  }
+  const float inv = l == 0.0f ? 0.0f : (c.had ? 0.03125f : 1.0f) / l;
+#pragma unroll
+  for (int d = 0; d < ND; ++d) {
+    if (c.had) {   // element bits 0, 1 and 3, 4 are register bits, bit 2 is the lane half
+#pragma unroll
+      for (int h = 1; h < 16; h <<= 1) {
+        if (h == 4) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            float lo, hi;
+            halves(o[d][r], lo, hi);
+            o[d][r] = half ? lo - hi : lo + hi;
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (!(r & h)) {
+            const float x = o[d][r], y = o[d][r + h];
+            o[d][r] = x + y;
+            o[d][r + h] = x - y;
+          }
+      }
+    }
+    uint32_t w[4][2];
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        w[g][e] = pack_bf16(o[d][4 * g + 2 * e] * inv, o[d][4 * g + 2 * e + 1] * inv);
+    // runs g and g + 1 of eight elements: the low half ends with run g, the high one with g + 1
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {
+      const auto x = __builtin_amdgcn_permlane32_swap(w[g][0], w[g + 1][0], false, false);
+      const auto y = __builtin_amdgcn_permlane32_swap(w[g][1], w[g + 1][1], false, false);
+      const int at = d * 32 + (g + half) * 8;
+      if (row_ok && at < c.head_dim)
+        *reinterpret_cast<uint4*>(a.out + out_row * c.head_dim + at) = make_uint4(x[0], y[0], x[1], y[1]);
+    }
+  }
+  if (a.lse != nullptr && half == 0 && row_ok)
+    a.lse[out_row] = l == 0.0f ? kNegInf : (m + __builtin_log2f(l)) * 0.6931471805599453f;
+}
+
 // Joins the splits of each row: a lane holds four elements of one row, eight
 // lanes a block of 32.
 template <int NB>
@@ -409,12 +723,18 @@ kv_attention_join_kernel(KvAttnArgs a) {
     a.lse[row] = L == 0.0f ? kNegInf : (M + __builtin_log2f(L)) * 0.6931471805599453f;
 }
 
+// Rows of a (sequence, key head) that one workgroup takes: 16 (the keys split over its
+// waves) while they fit, else 128.
+inline bool few_rows(int max_q, int group) { return (long long)max_q * group <= 16; }
+
 template <int NB>
 hipError_t launch_nb(const KvAttnArgs& a, hipStream_t s) {
-  constexpr int NW = 4;
-  const int row_tiles = (int)(((long long)a.max_q * a.group + 15) / 16);
+  const bool few = few_rows(a.max_q, a.group);
+  const int per = few ? 16 : 128;
+  const int row_tiles = (int)(((long long)a.max_q * a.group + per - 1) / per);
   const dim3 grid((unsigned)((long long)row_tiles * a.splits), (unsigned)a.cache.heads, (unsigned)a.seqs);
-  kv_attention_rows16_kernel<NB, NW><<<grid, NW * 64, 0, s>>>(a);
+  if (few) kv_attention_rows16_kernel<NB, 4><<<grid, 256, 0, s>>>(a);
+  else kv_attention_rows128_kernel<NB><<<grid, 256, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   constexpr int RPW = 256 / (8 * NB);
@@ -427,11 +747,15 @@ hipError_t launch_nb(const KvAttnArgs& a, hipStream_t s) {
 
 int kv_attention_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_kv) {
   if (seqs <= 0 || max_q <= 0 || kv_heads <= 0) return 1;
-  const long long row_tiles = ((long long)max_q * (q_heads / kv_heads) + 15) / 16;
+  const int group = q_heads / kv_heads;
+  const bool few = few_rows(max_q, group);
+  const long long row_tiles = ((long long)max_q * group + (few ? 15 : 127)) / (few ? 16 : 128);
   const long long base = (long long)seqs * kv_heads * row_tiles;
   const long long tiles = ((long long)max_kv + TILE - 1) / TILE;
-  long long want = (4ll * NUM_CUS + base - 1) / base;
-  want = want < (tiles + 3) / 4 ? want : (tiles + 3) / 4;
+  long long want = ((few ? 4ll : 2ll) * NUM_CUS + base - 1) / base;
+  if (!few && base >= NUM_CUS) want = 1;
+  const long long most = (tiles + 3) / 4;   // a range of at least four tiles
+  want = want < most ? want : most;
   if (want > 128) want = 128;
   return want < 1 ? 1 : (int)want;
 }
