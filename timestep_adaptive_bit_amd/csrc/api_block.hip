@@ -160,8 +160,10 @@ int tabit_kv_attention(tabit_ctx* ctx, const tabit_kv_cache* cache, const tabit_
     return fail(ctx, TABIT_EALIGN, "q, out and ws must be 16-byte aligned, the others 4-byte");
   if (a->num_tokens == 0 || a->num_seqs == 0 || a->max_q == 0) return TABIT_OK;
   k.splits = tabit::kv_attention_splits(a->num_seqs, a->max_q, a->num_q_heads, k.cache.heads, a->max_kv);
-  if ((int64_t)a->max_q * a->num_q_heads * k.splits > INT_MAX)
-    return fail(ctx, TABIT_ESHAPE, "max_q * num_q_heads is too large (%d * %d)", a->max_q, a->num_q_heads);
+  if ((int64_t)a->max_q * a->num_q_heads > INT_MAX / 64 ||
+      (int64_t)a->max_q * a->num_q_heads * k.splits * a->num_seqs > INT_MAX)
+    return fail(ctx, TABIT_ESHAPE, "max_q * num_q_heads * num_seqs is too large (%d * %d * %d)", a->max_q,
+                a->num_q_heads, a->num_seqs);
   const size_t need =
       tabit_kv_attention_workspace_bytes(a->num_tokens, a->num_q_heads, k.cache.heads, k.cache.head_dim,
                                          a->num_seqs, a->max_q, a->max_kv);

@@ -41,52 +41,124 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s* lds_v4s;
 
 constexpr float kNegInf = -__builtin_inff();
+constexpr uint32_t kMaxValueScale = 252;   // 6 * 2^(252 - 127) is the largest finite value
 constexpr int TILE = 64;      // keys a wave takes at a time
 constexpr int NUM_CUS = 256;  // MI355X
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Byte offset of 16-element run `c` (32 bytes) of key row `key` in the bf16 value
-// tile: rows of RS bytes, the run index XORed with the row so that the 16 rows one
-// transposed read touches fall on different banks.
+// Byte offset of 16-byte piece `half` of 16-element run `c` of key row `key` in the
+// bf16 value tile: rows of RS bytes.  Runs are XORed with bits of the key so that what
+// one access touches fills a 256-byte bank window: the 4 keys x 2 runs (or 8 keys x 1
+// run) of 32 lanes of a transposed read, and, with the pieces of every other eight
+// keys swapped, the 16 keys that 16 lanes write at once.
 template <int RS>
-__device__ __forceinline__ int v_off(int key, int c) {
-  constexpr int RUNS = RS / 32;
-  const int x = RUNS == 8 ? (key & 7) : ((key >> 1) & 3);
-  return key * RS + ((c ^ x) << 5);
+__device__ __forceinline__ int v_off(int key, int c, int half) {
+  const int x = RS == 256 ? ((key & 3) << 1 | ((key >> 2) & 1)) : ((key & 2) | ((key >> 2) & 1));
+  return key * RS + ((c ^ x) << 5) + ((half ^ ((key >> 3) & 1)) << 4);
+}
+
+// Keys and MX blocks of the units that consecutive lanes bring in: 16 keys, block by block.
+template <int NB>
+__device__ __forceinline__ int unit_key(int unit) { return unit / (16 * NB) * 16 + unit % 16; }
+template <int NB>
+__device__ __forceinline__ int unit_block(int unit) { return unit % (16 * NB) / 16; }
+
+// Factor of the products q'.k' that gives scores in base 2.
+__device__ __forceinline__ float base2_scale(const KvAttnArgs& a) {
+  return a.scale * 1.4426950408889634f / (a.cache.had ? 32.0f : 1.0f);
 }
 
 // 32 elements of a query row (block `blk` of the head vector), rotated and
-// transformed as the cache's keys are, negated for a negative scale (the kernels
-// then scale by its magnitude, so the largest score is the largest product).
+// transformed as the cache's keys are, times `factor`.  All loads are issued before
+// the first use: elements past the head, and tables outside the rotated part, are
+// read at a valid place and replaced.
 __device__ __forceinline__ bool load_q_block(const KvAttnArgs& a, int token, int head, int blk,
-                                             float (&x)[32]) {
-  const uint16_t* p = a.q + (long long)token * a.q_stride + (long long)head * a.cache.head_dim;
-  RopeArgs rope = a.rope;
+                                             float factor, float (&x)[32]) {
+  const int D = a.cache.head_dim, R = a.rope.rope_dim;
+  const uint16_t* p = a.q + (long long)token * a.q_stride + (long long)head * D;
   bool ok = true;
-  int pos = 0;
-  if (rope.rope_dim > 0) {
-    pos = a.positions[token];
-    if (pos < 0 || pos >= rope.num_positions) {
-      ok = false;
-      rope.rope_dim = 0;
-    }
-  }
+  uint4 own[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int e0 = blk * 32 + i * 8;
-    float v[8] = {};
-    if (e0 < a.cache.head_dim) load8_turned(p, e0, rope, pos, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[i * 8 + e] = v[e];
+    own[i] = *reinterpret_cast<const uint4*>(p + (e0 < D ? e0 : 0));
   }
+  auto spread = [](uint4 w, float* v) {
+    v[0] = bf_lo(w.x); v[1] = bf_hi(w.x); v[2] = bf_lo(w.y); v[3] = bf_hi(w.y);
+    v[4] = bf_lo(w.z); v[5] = bf_hi(w.z); v[6] = bf_lo(w.w); v[7] = bf_hi(w.w);
+  };
+  if (R > 0) {
+    const int pos = a.positions[token];
+    ok = pos >= 0 && pos < a.rope.num_positions;
+    const int half = R >> 1;
+    const float* cos = a.rope.cos + (ok ? (size_t)pos * half : 0);
+    const float* sin = a.rope.sin + (ok ? (size_t)pos * half : 0);
+    if (a.rope.interleaved) {
+      float4 c[4], s[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e0 = blk * 32 + i * 8, at = e0 < R ? e0 >> 1 : 0;
+        c[i] = *reinterpret_cast<const float4*>(cos + at);
+        s[i] = *reinterpret_cast<const float4*>(sin + at);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        spread(own[i], x + 8 * i);
+        if (blk * 32 + i * 8 < R) {
+          turn(x[8 * i], x[8 * i + 1], c[i].x, s[i].x);
+          turn(x[8 * i + 2], x[8 * i + 3], c[i].y, s[i].y);
+          turn(x[8 * i + 4], x[8 * i + 5], c[i].z, s[i].z);
+          turn(x[8 * i + 6], x[8 * i + 7], c[i].w, s[i].w);
+        }
+      }
+    } else {
+      uint4 other[4];
+      float4 c[8], s[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e0 = blk * 32 + i * 8;
+        const bool second = e0 >= half;
+        const int at = e0 < R ? (second ? e0 - half : e0) : 0;
+        other[i] = *reinterpret_cast<const uint4*>(p + (e0 < R ? (second ? e0 - half : e0 + half) : 0));
+        c[2 * i] = *reinterpret_cast<const float4*>(cos + at);
+        c[2 * i + 1] = *reinterpret_cast<const float4*>(cos + at + 4);
+        s[2 * i] = *reinterpret_cast<const float4*>(sin + at);
+        s[2 * i + 1] = *reinterpret_cast<const float4*>(sin + at + 4);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e0 = blk * 32 + i * 8;
+        spread(own[i], x + 8 * i);
+        float y[8];
+        spread(other[i], y);
+        const float cc[8] = {c[2 * i].x, c[2 * i].y, c[2 * i].z, c[2 * i].w,
+                             c[2 * i + 1].x, c[2 * i + 1].y, c[2 * i + 1].z, c[2 * i + 1].w};
+        const float ss[8] = {s[2 * i].x, s[2 * i].y, s[2 * i].z, s[2 * i].w,
+                             s[2 * i + 1].x, s[2 * i + 1].y, s[2 * i + 1].z, s[2 * i + 1].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float u = x[8 * i + e] * cc[e], w = y[e] * ss[e];
+          x[8 * i + e] = e0 >= R ? x[8 * i + e] : e0 >= half ? u + w : u - w;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) spread(own[i], x + 8 * i);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (blk * 32 + i * 8 >= D) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[8 * i + e] = 0.0f;
+    }
   if (a.cache.had) fwht32_lane(x);
-  if (a.scale < 0.0f) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) x[e] = -x[e];
+  for (int e = 0; e < 32; ++e) {
+    x[e] *= factor;
+    ok = ok && finite_f32(x[e]);
   }
-#pragma unroll
-  for (int e = 0; e < 32; ++e) ok = ok && finite_f32(x[e]);
   return ok;
 }
 
@@ -139,12 +211,6 @@ __device__ __forceinline__ int seen_keys(const KvAttnArgs& a, int len, int n, in
   return a.causal ? min(max(len - n + i + 1, 0), len) : len;
 }
 
-// Factor of the products q'.k' that gives scores in base 2.  Not quite zero, so that a
-// masked key's -inf stays one under a scale of zero.
-__device__ __forceinline__ float base2_scale(const KvAttnArgs& a) {
-  return fmaxf(fabsf(a.scale) * 1.4426950408889634f / (a.cache.had ? 32.0f : 1.0f), 0x1p-120f);
-}
-
 // One workgroup: 16 rows (queries x heads of the group) of one key head of one
 // sequence over one range of its keys; the range's tiles go to the waves in runs.
 template <int NB, int NW>
@@ -179,7 +245,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   uint32_t q_scales = 0u;
   if (row_ok && g < NB) {
     float x[32];
-    const bool ok = load_q_block(a, q0 + qi, qh, g, x);
+    const bool ok = load_q_block(a, q0 + qi, qh, g, base2_scale(a), x);
     q_terms(x, ok, q, q_scales);
   }
 
@@ -188,7 +254,6 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   split_range(tiles, a.splits, sp, t0, t1);
   const int per = (t1 - t0 + NW - 1) / NW;
   const int w0 = min(t0 + wave * per, t1), w1 = min(w0 + per, t1);
-  const float scale2 = base2_scale(a);
   const int page_size = 1 << c.page_shift;
 
   float m = kNegInf, l = 0.0f;
@@ -231,7 +296,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
     // values to bf16 in LDS: one MX block a lane and step; keys past the end as zeros
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      const int u = i * 64 + lane, key = u / NB, blk = u % NB, k = key >> 4;
+      const int key = unit_key<NB>(i * 64 + lane), blk = unit_block<NB>(i * 64 + lane), k = key >> 4;
       v4i vc = {0, 0, 0, 0};
       uint32_t vs = 127u;
       const long long bk = k == 0 ? base[0] : k == 1 ? base[1] : k == 2 ? base[2] : base[3];
@@ -250,7 +315,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
         y.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 1));
         y.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 2));
         y.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 3));
-        *reinterpret_cast<uint4*>(stage + v_off<RS>(key, blk * 2 + (w >> 1)) + (w & 1) * 16) = y;
+        *reinterpret_cast<uint4*>(stage + v_off<RS>(key, blk * 2 + (w >> 1), w & 1)) = y;
       }
     }
     // softmax: lane holds keys 16 k + 4 g + r of its row
@@ -260,7 +325,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const bool vis = there[k] && j0 + 16 * k + 4 * g + r < seen;
-        s[k][r] = vis ? s[k][r] * scale2 : kNegInf;
+        s[k][r] = vis ? s[k][r] : kNegInf;
         top = fmaxf(top, s[k][r]);
       }
     top = fmaxf(top, __shfl_xor(top, 16, 64));
@@ -294,9 +359,9 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
       for (int d = 0; d < DP / 16; ++d) {
         const int key = 32 * h + 4 * g + (row >> 2);
         const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds_v4s)(stage + v_off<RS>(key, d) + (row & 3) * 8));
+            (lds_v4s)(stage + v_off<RS>(key, d, (row >> 1) & 1) + (row & 1) * 8));
         const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds_v4s)(stage + v_off<RS>(key + 16, d) + (row & 3) * 8));
+            (lds_v4s)(stage + v_off<RS>(key + 16, d, (row >> 1) & 1) + (row & 1) * 8));
         const v8bf v = __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
         o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p, o[d], 0, 0, 0);
       }
@@ -375,48 +440,75 @@ __device__ __forceinline__ void halves(float v, float& lo, float& hi) {
   hi = __uint_as_float(r[1]);
 }
 
-// One workgroup: 128 rows of one key head of one sequence, 32 a wave, over one range
+// s + K_block Q'^T for term `t` of q'; `byte` picks the keys' scale in ksw.
+__device__ __forceinline__ v16f score_term(v4i x, const v8i& q, v16f s, int byte, int ksw, int t, int qsw) {
+  const v8i k = {x[0], x[1], x[2], x[3], 0, 0, 0, 0};
+#define TABIT_TERM(B_, T_) \
+  if (byte == B_ && t == T_) return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k, q, s, 4, 2, B_, ksw, T_, qsw);
+  TABIT_TERM(0, 0) TABIT_TERM(0, 1) TABIT_TERM(0, 2)
+  TABIT_TERM(1, 0) TABIT_TERM(1, 1) TABIT_TERM(1, 2)
+  TABIT_TERM(2, 0) TABIT_TERM(2, 1) TABIT_TERM(2, 2)
+  TABIT_TERM(3, 0) TABIT_TERM(3, 1) TABIT_TERM(3, 2)
+#undef TABIT_TERM
+  return s;
+}
+
+// One workgroup: 32 NW rows of one key head of one sequence, 32 a wave, over one range
 // of its keys.  The 64 keys of a tile are brought in once for all rows: codes and
 // scales through registers (loaded a tile ahead, their pages two ahead) into one of
-// two LDS stages, the values already as bf16, one barrier a tile.  A wave uses the
+// three LDS stages, the values already as bf16, one barrier a tile; the scores of a
+// tile are computed beside the weights of the one before.  A wave uses the
 // 32x32 forms of the same products: scores with 32x32x64 (lane l: one row, l%32, and
-// 32 of the 64 keys), values with 32x32x16, P staying in its lanes.  The running
-// maximum is raised only when a score exceeds it by 2^8, so most tiles rescale
-// nothing; sums stay below 2^8 times their true size.
-template <int NB>
-__global__ void __launch_bounds__(256, 2)
-kv_attention_rows128_kernel(KvAttnArgs a) {
+// 32 of the 64 keys), values with 32x32x16, P staying in its lanes.
+//
+// The vector units, not the matrix cores, bound this kernel, so a tile costs them one
+// exponential a score, half a rounding to bf16 and half an addition: exp2(s - ref) has
+// the same relative precision for any reference that neither over- nor underflows, so
+// the maximum is taken for the first tile a row sees (`exact`), and again only for a
+// tile in which a sum of exponentials passes 2^40; the matrix core subtracts ref by
+// starting its sums at -ref; the sum of the weights is a dot product of the rounded
+// weights with ones, two an instruction.
+// Keeps the instructions before it before those after it: a wave issues in order, so what
+// is to run beside a matrix instruction has to be placed between it and the next.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
+template <int NB, int NW>
+__global__ void __launch_bounds__(NW * 64, 2)
+kv_attention_rows_kernel(KvAttnArgs a) {
+  constexpr int ROWS = NW * 32;
   constexpr int DP = NB * 32;
   constexpr int ND = DP / 32;                        // 32-element output blocks
   constexpr int NS = (NB + 1) / 2;                   // 64-element steps of a score
   constexpr int RS = NB <= 2 ? 128 : 256;            // bytes of a staged value row
   constexpr int KB = TILE * DP / 2;                  // bytes of a tile's key codes
-  constexpr int UNITS = TILE * NB;                   // MX blocks of a tile's keys (or values)
   struct Stage {
     uint8_t v[TILE * RS];
     uint8_t k[KB];
     uint8_t ks[2][32][4];                            // [block % 2][key % 32][key / 32 * 2 + block / 2]
     int there[4];
   };
-  __shared__ __attribute__((aligned(1024))) Stage st[2];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  __shared__ __attribute__((aligned(1024))) Stage st[3];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = lane & 31, half = lane >> 5;
-  const int b = blockIdx.z, hk = blockIdx.y;
-  const int sp = blockIdx.x % a.splits, row_tile = blockIdx.x / a.splits;
+  const int per = gridDim.x / (unsigned)(a.cache.heads * a.seqs);   // row tiles x splits
+  const int at_x = blockIdx.x / (unsigned)per, at_y = blockIdx.x % (unsigned)per;
+  const int b = at_x / a.cache.heads, hk = at_x % a.cache.heads;
+  const int sp = at_y % a.splits, row_tile = at_y / a.splits;
   const KvCacheArgs& c = a.cache;
 
   int q0, n;
   seq_rows(a, b, q0, n);
   const int rows = n * a.group;
   // the last rows of a causal sequence see most: they start first
-  const int tiles_r = (rows + 127) / 128;
+  const int tiles_r = (rows + ROWS - 1) / ROWS;
   if (row_tile >= tiles_r) return;
-  const int r0 = (tiles_r - 1 - row_tile) * 128;
+  const int r0 = (tiles_r - 1 - row_tile) * ROWS;
   const int len = seq_keys(a, b);
   const int rr = r0 + wave * 32 + row;
   const bool row_ok = rr < rows;
   const int qi = rr / a.group, qh = hk * a.group + rr % a.group;
-  const int seen_all = seen_keys(a, len, n, (min(r0 + 128, rows) - 1) / a.group);
+  const int seen_all = seen_keys(a, len, n, (min(r0 + ROWS, rows) - 1) / a.group);
   const int seen = row_ok ? seen_keys(a, len, n, qi) : seen_all;   // idle rows mask nothing
   const int first = r0 + wave * 32;
   const int seen_lo = seen_keys(a, len, n, min(first, rows - 1) / a.group);
@@ -433,43 +525,60 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     const int blk = 2 * ds + half;
     if (row_ok && blk < NB) {
       float x[32];
-      const bool ok = load_q_block(a, q0 + qi, qh, blk, x);
+      const bool ok = load_q_block(a, q0 + qi, qh, blk, base2_scale(a), x);
       q_terms(x, ok, q[ds], q_scales[ds]);
     }
   }
 
   int t0, t1;
   split_range((seen_all + TILE - 1) / TILE, a.splits, sp, t0, t1);
-  const float scale2 = base2_scale(a);
   const int in_page = (1 << c.page_shift) - 1;
 
-  // what this thread brings in: key block `tid`, value block `255 - tid`
-  const bool has_k = tid < UNITS, has_v = 255 - tid < UNITS;
-  const int kkey = tid / NB, kblk = tid % NB, vkey = (255 - tid) / NB, vblk = (255 - tid) % NB;
+  // A wave brings in KPW keys of a tile, which lie in one page: their rows are one run of
+  // memory at a uniform base, a lane's offset in it never changes.  Key codes: lane =
+  // block * KPW + key; value codes: likewise, VH pieces a block where that fits the wave.
+  constexpr int KPW = TILE / NW;                     // 16 or 8
+  constexpr int VH = 64 / KPW / NB >= 4 ? 4 : 64 / KPW / NB >= 2 ? 2 : 1;
+  constexpr int VW = 4 / VH;                         // dwords of a piece
+  const int lkey = lane % KPW, unit = lane / KPW;
+  const int kblk = unit, vblk = unit / VH, vpart = unit % VH;
+  const bool has_k = kblk < NB, has_v = vblk < NB;
+  const unsigned k_at = has_k ? lkey * (DP / 2) + kblk * 16 : tile::kOOB;
+  const unsigned v_at = has_v ? lkey * (DP / 2) + vblk * 16 + vpart * VW * 4 : tile::kOOB;
+  const unsigned ks_at = has_k ? lkey * NB + kblk : tile::kOOB, vs_at = has_v ? lkey * NB + vblk : tile::kOOB;
   const int* table = a.table + (long long)b * a.table_stride;
-  auto page_of = [&](int j) -> int {
-    const int pi = j >> c.page_shift;
-    return j < len && pi < a.table_stride ? table[pi] : -1;
+  int page;
+  auto next_page = [&](int t) {
+    const int j = t * TILE + wave * KPW, pi = j >> c.page_shift;
+    page = t < t1 && j < len && pi < a.table_stride ? table[pi] : -1;
   };
-  int kpage, vpage;
   v4i kc, vc;
   uint32_t ks, vs;
-  bool kthere;
-  auto fetch = [&](int t) {     // codes and scales of tile t through the pages at hand
-    kc = vc = v4i{0, 0, 0, 0};
-    ks = vs = 127u;
-    const int jk = t * TILE + kkey, jv = t * TILE + vkey;
-    kthere = kpage >= 0 && kpage < c.num_pages;
-    if (kthere) {
-      const long long r = (((long long)kpage * c.heads + hk) << c.page_shift) + (jk & in_page);
-      kc = *reinterpret_cast<const v4i*>(c.k_codes + r * (DP / 2) + kblk * 16);
-      ks = c.k_scales[r * NB + kblk];
+  bool there_w;
+  // Codes and scales of tile t through the page at hand.  Buffer loads whose range is the
+  // keys there are: keys of no page, and values past the sequence's end, arrive as zeros.
+  auto fetch = [&](int t) {
+    const int pg = __builtin_amdgcn_readfirstlane(page);
+    const int j = t * TILE + wave * KPW;
+    there_w = pg >= 0 && pg < c.num_pages;
+    const long long r = there_w ? (((long long)pg * c.heads + hk) << c.page_shift) + (j & in_page) : 0;
+    const int nk = there_w ? KPW : 0, nv = there_w ? min(len - j, KPW) : 0;
+    const auto rk = tile::make_rsrc(c.k_codes + r * (DP / 2), nk * (DP / 2));
+    const auto rv = tile::make_rsrc(c.v_codes + r * (DP / 2), nv * (DP / 2));
+    const auto rks = tile::make_rsrc(c.k_scales + r * NB, nk * NB);
+    const auto rvs = tile::make_rsrc(c.v_scales + r * NB, nv * NB);
+    kc = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rk, k_at, 0, 0));
+    if constexpr (VW == 4) {
+      vc = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rv, v_at, 0, 0));
+    } else if constexpr (VW == 2) {
+      const auto w = __builtin_amdgcn_raw_buffer_load_b64(rv, v_at, 0, 0);
+      vc[0] = (int)w[0];
+      vc[1] = (int)w[1];
+    } else {
+      vc[0] = (int)__builtin_amdgcn_raw_buffer_load_b32(rv, v_at, 0, 0);
     }
-    if (vpage >= 0 && vpage < c.num_pages) {
-      const long long r = (((long long)vpage * c.heads + hk) << c.page_shift) + (jv & in_page);
-      vc = *reinterpret_cast<const v4i*>(c.v_codes + r * (DP / 2) + vblk * 16);
-      vs = c.v_scales[r * NB + vblk];
-    }
+    ks = __builtin_amdgcn_raw_buffer_load_b8(rks, ks_at, 0, 0);
+    vs = __builtin_amdgcn_raw_buffer_load_b8(rvs, vs_at, 0, 0);
   };
   // 16-byte block `blk` of key row `key`: rows share a 256-byte bank window, the XOR
   // spreads the 16 rows one read touches over it (48-byte rows spread by themselves)
@@ -479,129 +588,240 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     else return key * (DP / 2) + (blk << 4);
   };
 
-  float m = kNegInf, l = 0.0f;
+  // scores come out of the matrix core relative to `ref` (the accumulators start at
+  // -ref); `fresh`: the row has seen no key yet
+  float ref = 0.0f, l = 0.0f;
+  bool fresh = true;
   v16f o[ND];
 #pragma unroll
   for (int d = 0; d < ND; ++d) o[d] = v16f{};
 
-  auto next_pages = [&](int t) {
-    kpage = has_k && t < t1 ? page_of(t * TILE + kkey) : -1;
-    vpage = has_v && t < t1 ? page_of(t * TILE + vkey) : -1;
+  const int skey = wave * KPW + lkey;
+  // A value scale beyond bf16 (or NaN): the key's scores become NaN and its values zero,
+  // so that rows that do not see the key (weight 0) are not touched by it.
+  auto settle = [&]() {
+    const unsigned long long bad = __ballot(vs > kMaxValueScale);
+    constexpr unsigned long long kSameKey = KPW == 16 ? 0x0001000100010001ull : 0x0101010101010101ull;
+    if (bad != 0 && ((bad >> lkey) & kSameKey) != 0) {
+      ks = 255u;
+      vs = 127u;
+      vc = v4i{0, 0, 0, 0};
+    }
   };
-  next_pages(t0);
-  fetch(t0);
-  next_pages(t0 + 1);
-  if constexpr (NB % 2 != 0) {   // scale bytes of blocks that do not exist: any finite scale
-    for (int i = tid; i < 64; i += 256) {
-      reinterpret_cast<uint32_t*>(st[0].ks)[i] = 0x7F7F7F7Fu;
-      reinterpret_cast<uint32_t*>(st[1].ks)[i] = 0x7F7F7F7Fu;
-    }
-    __syncthreads();
-  }
-  for (int t = t0; t < t1; ++t) {
-    Stage& s = st[(t - t0) & 1];
+  auto store_keys = [&](Stage& s) {
     if (has_k) {
-      *reinterpret_cast<v4i*>(s.k + k_off(kkey, kblk)) = kc;
-      s.ks[kblk & 1][kkey & 31][(kkey >> 5) * 2 + (kblk >> 1)] = (uint8_t)ks;
-      if ((kkey & 15) == 0 && kblk == 0) s.there[kkey >> 4] = kthere;
+      *reinterpret_cast<v4i*>(s.k + k_off(skey, kblk)) = kc;
+      s.ks[kblk & 1][skey & 31][(skey >> 5) * 2 + (kblk >> 1)] = (uint8_t)ks;
     }
+    if (lane == 0) s.there[wave * KPW / 16] = there_w;
+  };
+  auto store_values = [&](Stage& s, int w) {         // w: dword of the piece
     if (has_v) {
       const float f = __uint_as_float(vs << 23);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t x = (uint32_t)vc[w];
-        uint4 y;
-        y.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 0));
-        y.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 1));
-        y.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 2));
-        y.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 3));
-        *reinterpret_cast<uint4*>(s.v + v_off<RS>(vkey, vblk * 2 + (w >> 1)) + (w & 1) * 16) = y;
-      }
+      const uint32_t x = (uint32_t)vc[w];
+      uint4 y;
+      y.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 0));
+      y.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 1));
+      y.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 2));
+      y.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 3));
+      const int g = vpart * VW + w;                  // 16 bytes of the block
+      *reinterpret_cast<uint4*>(s.v + v_off<RS>(skey, vblk * 2 + (g >> 1), g & 1)) = y;
     }
-    fetch(t + 1);              // past the range: no pages, no loads
-    next_pages(t + 2);
-    tile::lds_barrier();
-    const int j0 = t * TILE;
-    if (j0 >= seen_hi) continue;                     // no row of the wave sees the tile
-
-    v16f sc[2];
+  };
+  auto store = [&](Stage& s) {
+    store_keys(s);
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      sc[kb] = v16f{};
-      const int ksw = *reinterpret_cast<const int*>(s.ks[half][row]);
+    for (int w = 0; w < VW; ++w) store_values(s, w);
+  };
+  // Scores of a tile.  Lane: keys 32 kb + 8 (r / 4) + 4 half + r % 4 of its row.
+  auto scores = [&](const Stage& s, v16f (&sc)[2]) {
+    const int ksw = *reinterpret_cast<const int*>(s.ks[half][row]);
+    sc[0] = sc[1] = v16f{};
 #pragma unroll
-      for (int ds = 0; ds < NS; ++ds) {
-        const int blk = 2 * ds + half;
-        v4i x = {0, 0, 0, 0};
-        if (NB % 2 == 0 || blk < NB) x = *reinterpret_cast<const v4i*>(s.k + k_off(kb * 32 + row, blk));
-        const v8i ka = {x[0], x[1], x[2], x[3], 0, 0, 0, 0};
-#define TABIT_QK(T_)                                                                                     \
-  sc[kb] = kb == 0 ? (ds == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                          \
-                                    ka, q[ds][T_], sc[kb], 4, 2, 0, ksw, T_, (int)q_scales[ds])           \
-                              : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                          \
-                                    ka, q[ds][T_], sc[kb], 4, 2, 1, ksw, T_, (int)q_scales[ds]))          \
-                   : (ds == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                          \
-                                    ka, q[ds][T_], sc[kb], 4, 2, 2, ksw, T_, (int)q_scales[ds])           \
-                              : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                          \
-                                    ka, q[ds][T_], sc[kb], 4, 2, 3, ksw, T_, (int)q_scales[ds]));
-        TABIT_QK(0) TABIT_QK(1) TABIT_QK(2)
-#undef TABIT_QK
-      }
-    }
-    // lane: keys 32 kb + 8 (r / 4) + 4 half + r % 4 of its row
-    const v4i there = *reinterpret_cast<const v4i*>(s.there);
-    const bool whole = (there[0] & there[1] & there[2] & there[3]) != 0;
-    if (j0 + TILE > seen_lo || !whole) {
+    for (int ds = 0; ds < NS; ++ds) {
+      const int blk = 2 * ds + half;
+      v4i x[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
+        if (NB % 2 == 0 || blk < NB) x[kb] = *reinterpret_cast<const v4i*>(s.k + k_off(kb * 32 + row, blk));
+      // the two accumulators in turn: neither waits for its own last product
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int key = kb * 32 + (r >> 2) * 8 + half * 4 + (r & 3);
-          if (j0 + key >= seen || there[kb * 2 + (r >> 3)] == 0) sc[kb][r] = kNegInf;
-        }
+      for (int t = 0; t < 3; ++t)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+          sc[kb] = score_term(x[kb], q[ds][t], sc[kb], kb * 2 + ds, ksw, t, (int)q_scales[ds]);
     }
+  };
+  // Raises the reference to the largest score where a row needs it; what is summed so far is
+  // to be scaled by alpha.
+  float alpha = 1.0f;
+  bool any_fresh = true, any_ref = false, any_alpha = false;     // over the wave
+  auto raise = [&](const v16f (&sc)[2]) {
     float top = kNegInf;
 #pragma unroll
     for (int r = 0; r < 16; ++r) top = fmaxf(fmaxf(top, sc[0][r]), sc[1][r]);
     float tl, th;
     halves(top, tl, th);
-    top = fmaxf(tl, th) * scale2;
-    if (__any(top > m + 8.0f)) {
-      const float m_new = fmaxf(m, top);
-      const float ref = m_new == kNegInf ? 0.0f : m_new;
-      const float alpha = exp2_fast(m - ref);
-      m = m_new;
-      l *= alpha;
+    top = fmaxf(tl, th);
+    const bool first = fresh && top > kNegInf;
+    fresh = fresh && !first;
+    any_fresh = __any(fresh);
+    // 2^s is as exact as 2^(s - ref): a reference is needed only for large scores
+    const bool up = first ? fabsf(top) > 40.0f : !fresh && top > ref;
+    const float by = up ? top - ref : 0.0f;
+    alpha = first ? 1.0f : exp2_fast(-by);           // a fresh row's sums are zero
+    ref += by;
+    l *= alpha;
+    any_ref = __any(ref != 0.0f);
+    any_alpha = __any(alpha != 1.0f);
+  };
+  uint32_t p[16];                // pairs of weights, in the order of the value products
+  float sum[2];
+  auto weight_pair = [&](const v16f (&sc)[2], int i) {
+    const float x = exp2_fast(sc[i >> 3][2 * (i & 7)]), y = exp2_fast(sc[i >> 3][2 * (i & 7) + 1]);
+    sum[0] += x;
+    sum[1] += y;
+    p[i] = pack_bf16(x, y);
+  };
+  // The weights of `sc` beside the scores of the next tile.
+  auto weights_and_scores = [&](const v16f (&sc)[2], const Stage& s, v16f (&nx)[2]) {
+    constexpr int N = 6 * NS, HEAD = 4;              // products; pairs done while the keys come in
+    const int ksw = *reinterpret_cast<const int*>(s.ks[half][row]);
+    v4i x[NS][2];
 #pragma unroll
-      for (int d = 0; d < ND; ++d) o[d] *= alpha;
+    for (int ds = 0; ds < NS; ++ds)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        const int blk = 2 * ds + half;
+        x[ds][kb] = v4i{0, 0, 0, 0};
+        if (NB % 2 == 0 || blk < NB) x[ds][kb] = *reinterpret_cast<const v4i*>(s.k + k_off(kb * 32 + row, blk));
+      }
+    keep_order();
+    sum[0] = sum[1] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < HEAD; ++i) weight_pair(sc, i);
+    nx[0] = nx[1] = v16f{};
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      keep_order();
+      const int ds = i / 6, t = i % 6 / 2, kb = i & 1;
+      nx[kb] = score_term(x[ds][kb], q[ds][t], nx[kb], kb * 2 + ds, ksw, t, (int)q_scales[ds]);
+      keep_order();
+#pragma unroll
+      for (int k = HEAD + (16 - HEAD) * i / N; k < HEAD + (16 - HEAD) * (i + 1) / N; ++k) weight_pair(sc, k);
     }
-    const float ref = m == kNegInf ? 0.0f : m;
+  };
+  // The values of a tile, read three products ahead, with `side(k)`, k = 0 .. SIDES - 1,
+  // spread between the products.
+  constexpr int SIDES = 7 + VW;
+  auto values = [&](const Stage& s, auto side) {
+    constexpr int N = 4 * ND, AHEAD = 3;             // products: 16 keys x 32 elements each
+    const int key0 = 4 * half + ((lane & 15) >> 2), run0 = (lane >> 4) & 1, piece = (lane >> 1) & 1;
+    v4s x[N], y[N];
+    auto read = [&](int i) {
+      const int key = key0 + i / ND * 16, run = 2 * (i % ND) + run0;
+      x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(s.v + v_off<RS>(key, run, piece) + (lane & 1) * 8));
+      y[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(s.v + v_off<RS>(key + 8, run, piece) + (lane & 1) * 8));
+    };
+    keep_order();
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int i = 0; i < AHEAD; ++i) read(i);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        sc[kb][r] = exp2_fast(__builtin_fmaf(sc[kb][r], scale2, -ref));
-        l += sc[kb][r];
+    for (int i = 0; i < N; ++i) {
+      keep_order();
+      if (i + AHEAD < N) read(i + AHEAD);
+      const v8bf v = __builtin_bit_cast(v8bf, __builtin_shufflevector(x[i], y[i], 0, 1, 2, 3, 4, 5, 6, 7));
+      const int u = i / ND;
+      const v8bf w = __builtin_bit_cast(v8bf, make_uint4(p[4 * u], p[4 * u + 1], p[4 * u + 2], p[4 * u + 3]));
+      o[i % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w, o[i % ND], 0, 0, 0);
+      keep_order();
+#pragma unroll
+      for (int k = SIDES * i / N; k < SIDES * (i + 1) / N; ++k) side(k);
+    }
+  };
+
+  next_page(t0);
+  fetch(t0);
+  next_page(t0 + 1);
+  if constexpr (NB % 2 != 0) {   // scale bytes of blocks that do not exist: any finite scale
+    for (int i = tid; i < 3 * 64; i += NW * 64)
+      reinterpret_cast<uint32_t*>(st[i / 64].ks)[i % 64] = 0x7F7F7F7Fu;
+    __syncthreads();
+  }
+  settle();
+  store(st[0]);
+  fetch(t0 + 1);
+  next_page(t0 + 2);
+  settle();
+  store(st[1]);
+  fetch(t0 + 2);
+  next_page(t0 + 3);
+  tile::lds_barrier();
+  v16f sc[2], nx[2];
+  scores(st[0], sc);
+  v4i there_t = *reinterpret_cast<const v4i*>(st[0].there);
+  int at = 0;                    // stage of tile t
+  for (int t = t0; t < t1; ++t) {
+    const int at1 = at == 2 ? 0 : at + 1, at2 = at == 0 ? 2 : at - 1;
+    const Stage& s = st[at];
+    const int j0 = t * TILE;
+    if (j0 < seen_hi) {          // else no row of the wave sees the tile, nor a later one
+      const v4i there = there_t;
+      if (j0 + TILE > seen_lo || (there[0] & there[1] & there[2] & there[3]) == 0) {
+        const int left = seen - j0 - half * 4;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (kb * 32 + (r >> 2) * 8 + (r & 3) >= left || there[kb * 2 + (r >> 3)] == 0) sc[kb][r] = kNegInf;
       }
+      const bool exact = any_fresh && __any(fresh && j0 < seen);
+      if (exact) raise(sc);
+      if (any_ref) {
+        sc[0] -= ref;
+        sc[1] -= ref;
+      }
+      weights_and_scores(sc, st[at1], nx);     // of tile t + 1 (a stale stage at the end)
+      asm volatile("" : "+v"(nx[0]), "+v"(nx[1]));   // or the products would sink below the branches
+      if (!exact && __any(!(sum[0] + sum[1] < 0x1p40f))) {
+        const float old = ref;
+        sc[0] += old;
+        sc[1] += old;
+        raise(sc);
+        sc[0] -= ref;
+        sc[1] -= ref;
+        sum[0] = sum[1] = 0.0f;
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+        for (int i = 0; i < 16; ++i) weight_pair(sc, i);
+      }
+      l += sum[0] + sum[1];
+      if (any_alpha) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        v8bf p;
+        for (int d = 0; d < ND; ++d) o[d] *= alpha;
+        any_alpha = false;
+      }
+      // beside the values: tile t + 2 into the stage whose readers were done before the last
+      // barrier, then tile t + 3 from memory (past the range: no page, no loads)
+      settle();
+      there_t = *reinterpret_cast<const v4i*>(st[at1].there);
+      values(s, [&](int k) {
+        if (k == 0) store_keys(st[at2]);
+        else if (k <= VW) store_values(st[at2], k - 1);
+        else if (k == VW + 1) fetch(t + 3);
+        else if (k == VW + 2) next_page(t + 4);
+        else {                     // and the next scores take their place
 #pragma unroll
-        for (int r = 0; r < 8; ++r) p[r] = (__bf16)sc[kb][8 * u + r];
-        const int key = kb * 32 + 16 * u + 4 * half + ((lane & 15) >> 2);
-#pragma unroll
-        for (int d = 0; d < ND; ++d) {
-          const int run = 2 * d + ((lane >> 4) & 1);
-          const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_v4s)(s.v + v_off<RS>(key, run) + (lane & 3) * 8));
-          const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_v4s)(s.v + v_off<RS>(key + 8, run) + (lane & 3) * 8));
-          const v8bf v = __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p, o[d], 0, 0, 0);
+          for (int r = 0; r < 8; ++r) sc[(k - VW - 3) >> 1][(k - VW - 3) % 2 * 8 + r] = nx[(k - VW - 3) >> 1][(k - VW - 3) % 2 * 8 + r];
         }
-      }
+      });
+    } else {
+      settle();
+      store(st[at2]);
+      fetch(t + 3);
+      next_page(t + 4);
+    }
+    at = at1;
+    tile::lds_barrier();
   }
   {
     float lo, hi;
@@ -622,7 +842,7 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
             v4f{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
     if (half == 0) {
       float* ml = a.part + (long long)a.splits * all * DP + ((long long)sp * all + out_row) * 2;
-      ml[0] = m;
+      ml[0] = fresh ? kNegInf : ref;
       ml[1] = l;
     }
     return;
@@ -667,7 +887,7 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     }
   }
   if (a.lse != nullptr && half == 0 && row_ok)
-    a.lse[out_row] = l == 0.0f ? kNegInf : (m + __builtin_log2f(l)) * 0.6931471805599453f;
+    a.lse[out_row] = l == 0.0f ? kNegInf : (ref + __builtin_log2f(l)) * 0.6931471805599453f;
 }
 
 // Joins the splits of each row: a lane holds four elements of one row, eight
@@ -723,6 +943,7 @@ kv_attention_join_kernel(KvAttnArgs a) {
     a.lse[row] = L == 0.0f ? kNegInf : (M + __builtin_log2f(L)) * 0.6931471805599453f;
 }
 
+constexpr int kWaves = 4;
 // Rows of a (sequence, key head) that one workgroup takes: 16 (the keys split over its
 // waves) while they fit, else 128.
 inline bool few_rows(int max_q, int group) { return (long long)max_q * group <= 16; }
@@ -730,11 +951,11 @@ inline bool few_rows(int max_q, int group) { return (long long)max_q * group <= 
 template <int NB>
 hipError_t launch_nb(const KvAttnArgs& a, hipStream_t s) {
   const bool few = few_rows(a.max_q, a.group);
-  const int per = few ? 16 : 128;
+  const int per = few ? 16 : kWaves * 32;
   const int row_tiles = (int)(((long long)a.max_q * a.group + per - 1) / per);
   const dim3 grid((unsigned)((long long)row_tiles * a.splits), (unsigned)a.cache.heads, (unsigned)a.seqs);
   if (few) kv_attention_rows16_kernel<NB, 4><<<grid, 256, 0, s>>>(a);
-  else kv_attention_rows128_kernel<NB><<<grid, 256, 0, s>>>(a);
+  else kv_attention_rows_kernel<NB, kWaves><<<grid.x * grid.y * grid.z, kWaves * 64, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   constexpr int RPW = 256 / (8 * NB);
@@ -749,15 +970,31 @@ int kv_attention_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_
   if (seqs <= 0 || max_q <= 0 || kv_heads <= 0) return 1;
   const int group = q_heads / kv_heads;
   const bool few = few_rows(max_q, group);
-  const long long row_tiles = ((long long)max_q * group + (few ? 15 : 127)) / (few ? 16 : 128);
+  const long long row_tiles = ((long long)max_q * group + (few ? 15 : kWaves * 32 - 1)) / (few ? 16 : kWaves * 32);
   const long long base = (long long)seqs * kv_heads * row_tiles;
   const long long tiles = ((long long)max_kv + TILE - 1) / TILE;
-  long long want = ((few ? 4ll : 2ll) * NUM_CUS + base - 1) / base;
-  if (!few && base >= NUM_CUS) want = 1;
-  const long long most = (tiles + 3) / 4;   // a range of at least four tiles
-  want = want < most ? want : most;
-  if (want > 128) want = 128;
-  return want < 1 ? 1 : (int)want;
+  if (few) {
+    long long want = (4ll * NUM_CUS + base - 1) / base;
+    const long long most = (tiles + 3) / 4;   // a range of at least four tiles
+    want = want < most ? want : most;
+    if (want > 128) want = 128;
+    return want < 1 ? 1 : (int)want;
+  }
+  // 128 rows: the splits whose rounds of workgroups over the chip's slots take least.  A
+  // range costs its tiles and about six more to start; each split's partial sums cost the
+  // chip about one tile's time a row tile in two slots.
+  const long long slots = (kWaves == 8 ? 1ll : 2ll) * NUM_CUS;
+  long long best = 0;
+  int splits = 1;
+  for (int n = 1; n <= 64 && n <= (tiles + 3) / 4; ++n) {
+    const long long rounds = (base * n + slots - 1) / slots;
+    const long long cost = rounds * ((tiles + n - 1) / n + 6) + (n > 1 ? (base * n + slots - 1) / slots * 4 : 0);
+    if (n == 1 || cost < best) {
+      best = cost;
+      splits = n;
+    }
+  }
+  return splits;
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t s) {
