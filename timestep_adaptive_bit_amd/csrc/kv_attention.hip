@@ -468,14 +468,10 @@ __device__ __forceinline__ v16f score_term(v4i x, const v8i& q, v16f s, int byte
 // tile in which a sum of exponentials passes 2^40; the matrix core subtracts ref by
 // starting its sums at -ref; the sum of the weights is a dot product of the rounded
 // weights with ones, two an instruction.
-// Keeps the instructions before it before those after it: a wave issues in order, so what
-// is to run beside a matrix instruction has to be placed between it and the next.
-__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
-
-template <int NB, int NW>
-__global__ void __launch_bounds__(NW * 64, 2)
-kv_attention_rows_kernel(KvAttnArgs a) {
-  constexpr int ROWS = NW * 32;
+template <int NB>
+__global__ void __launch_bounds__(256, NB <= 2 ? 3 : 2)
+kv_attention_rows128_kernel(KvAttnArgs a) {
+  constexpr int NW = 4, ROWS = NW * 32;              // waves, rows
   constexpr int DP = NB * 32;
   constexpr int ND = DP / 32;                        // 32-element output blocks
   constexpr int NS = (NB + 1) / 2;                   // 64-element steps of a score
@@ -485,9 +481,8 @@ kv_attention_rows_kernel(KvAttnArgs a) {
     uint8_t v[TILE * RS];
     uint8_t k[KB];
     uint8_t ks[2][32][4];                            // [block % 2][key % 32][key / 32 * 2 + block / 2]
-    int there[4];
   };
-  __shared__ __attribute__((aligned(1024))) Stage st[3];
+  __shared__ __attribute__((aligned(1024))) Stage st[2];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = lane & 31, half = lane >> 5;
@@ -537,49 +532,63 @@ kv_attention_rows_kernel(KvAttnArgs a) {
   // A wave brings in KPW keys of a tile, which lie in one page: their rows are one run of
   // memory at a uniform base, a lane's offset in it never changes.  Key codes: lane =
   // block * KPW + key; value codes: likewise, VH pieces a block where that fits the wave.
-  constexpr int KPW = TILE / NW;                     // 16 or 8
+  constexpr int KPW = TILE / NW;
   constexpr int VH = 64 / KPW / NB >= 4 ? 4 : 64 / KPW / NB >= 2 ? 2 : 1;
   constexpr int VW = 4 / VH;                         // dwords of a piece
   const int lkey = lane % KPW, unit = lane / KPW;
   const int kblk = unit, vblk = unit / VH, vpart = unit % VH;
   const bool has_k = kblk < NB, has_v = vblk < NB;
-  const unsigned k_at = has_k ? lkey * (DP / 2) + kblk * 16 : tile::kOOB;
-  const unsigned v_at = has_v ? lkey * (DP / 2) + vblk * 16 + vpart * VW * 4 : tile::kOOB;
-  const unsigned ks_at = has_k ? lkey * NB + kblk : tile::kOOB, vs_at = has_v ? lkey * NB + vblk : tile::kOOB;
+  // (lanes without a block read the first one)
+  const unsigned k_at = lkey * (DP / 2) + (has_k ? kblk * 16 : 0);
+  const unsigned v_at = lkey * (DP / 2) + (has_v ? vblk * 16 + vpart * VW * 4 : 0);
+  const unsigned ks_at = lkey * NB + (has_k ? kblk : 0), vs_at = lkey * NB + (has_v ? vblk : 0);
   const int* table = a.table + (long long)b * a.table_stride;
   int page;
   auto next_page = [&](int t) {
-    const int j = t * TILE + wave * KPW, pi = j >> c.page_shift;
-    page = t < t1 && j < len && pi < a.table_stride ? table[pi] : -1;
+    const int j = t * TILE + wave * KPW;
+    page = t < t1 && j < len ? table[min(j >> c.page_shift, a.table_stride - 1)] : -1;
   };
+  const long long page_rows = (long long)c.heads << c.page_shift, head_row = (long long)hk << c.page_shift;
   v4i kc, vc;
   uint32_t ks, vs;
-  bool there_w;
-  // Codes and scales of tile t through the page at hand.  Buffer loads whose range is the
-  // keys there are: keys of no page, and values past the sequence's end, arrive as zeros.
+  // Codes and scales of tile t through the page at hand.  Keys of no page, and values past
+  // the sequence's end, are zeros.
   auto fetch = [&](int t) {
     const int pg = __builtin_amdgcn_readfirstlane(page);
     const int j = t * TILE + wave * KPW;
-    there_w = pg >= 0 && pg < c.num_pages;
-    const long long r = there_w ? (((long long)pg * c.heads + hk) << c.page_shift) + (j & in_page) : 0;
-    const int nk = there_w ? KPW : 0, nv = there_w ? min(len - j, KPW) : 0;
-    const auto rk = tile::make_rsrc(c.k_codes + r * (DP / 2), nk * (DP / 2));
-    const auto rv = tile::make_rsrc(c.v_codes + r * (DP / 2), nv * (DP / 2));
-    const auto rks = tile::make_rsrc(c.k_scales + r * NB, nk * NB);
-    const auto rvs = tile::make_rsrc(c.v_scales + r * NB, nv * NB);
-    kc = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rk, k_at, 0, 0));
-    if constexpr (VW == 4) {
-      vc = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rv, v_at, 0, 0));
-    } else if constexpr (VW == 2) {
-      const auto w = __builtin_amdgcn_raw_buffer_load_b64(rv, v_at, 0, 0);
-      vc[0] = (int)w[0];
-      vc[1] = (int)w[1];
+    const bool there = (unsigned)pg < (unsigned)c.num_pages;
+    const long long r = pg * page_rows + head_row + (j & in_page);
+    if (there && j + KPW <= len) {
+      kc = *reinterpret_cast<const v4i*>(c.k_codes + r * (DP / 2) + k_at);
+      const uint8_t* vp = c.v_codes + r * (DP / 2) + v_at;
+      if constexpr (VW == 4) {
+        vc = *reinterpret_cast<const v4i*>(vp);
+      } else if constexpr (VW == 2) {
+        const int2 w = *reinterpret_cast<const int2*>(vp);
+        vc[0] = w.x;
+        vc[1] = w.y;
+      } else {
+        vc[0] = *reinterpret_cast<const int*>(vp);
+      }
+      ks = (c.k_scales + r * NB)[ks_at];
+      vs = (c.v_scales + r * NB)[vs_at];
     } else {
-      vc[0] = (int)__builtin_amdgcn_raw_buffer_load_b32(rv, v_at, 0, 0);
+      kc = vc = v4i{0, 0, 0, 0};
+      ks = vs = 127u;
+      if (there && lkey < len - j) {
+        kc = *reinterpret_cast<const v4i*>(c.k_codes + r * (DP / 2) + k_at);
+        ks = (c.k_scales + r * NB)[ks_at];
+#pragma unroll
+        for (int w = 0; w < VW; ++w) vc[w] = *reinterpret_cast<const int*>(c.v_codes + r * (DP / 2) + v_at + 4 * w);
+        vs = (c.v_scales + r * NB)[vs_at];
+      }
     }
-    ks = __builtin_amdgcn_raw_buffer_load_b8(rks, ks_at, 0, 0);
-    vs = __builtin_amdgcn_raw_buffer_load_b8(rvs, vs_at, 0, 0);
   };
+  // Whether a page of the range is not in the cache: its keys are then hidden tile by tile.
+  bool holes = false;
+  for (int i = (t0 * TILE >> c.page_shift) + lane; i < a.table_stride && i <= (min(t1 * TILE, len) - 1) >> c.page_shift; i += 64)
+    holes = holes || (unsigned)table[i] >= (unsigned)c.num_pages;
+  holes = __any(holes);
   // 16-byte block `blk` of key row `key`: rows share a 256-byte bank window, the XOR
   // spreads the 16 rows one read touches over it (48-byte rows spread by themselves)
   auto k_off = [](int key, int blk) {
@@ -601,8 +610,7 @@ kv_attention_rows_kernel(KvAttnArgs a) {
   // so that rows that do not see the key (weight 0) are not touched by it.
   auto settle = [&]() {
     const unsigned long long bad = __ballot(vs > kMaxValueScale);
-    constexpr unsigned long long kSameKey = KPW == 16 ? 0x0001000100010001ull : 0x0101010101010101ull;
-    if (bad != 0 && ((bad >> lkey) & kSameKey) != 0) {
+    if (bad != 0 && ((bad >> lkey) & 0x0001000100010001ull) != 0) {   // lanes of the same key
       ks = 255u;
       vs = 127u;
       vc = v4i{0, 0, 0, 0};
@@ -613,7 +621,6 @@ kv_attention_rows_kernel(KvAttnArgs a) {
       *reinterpret_cast<v4i*>(s.k + k_off(skey, kblk)) = kc;
       s.ks[kblk & 1][skey & 31][(skey >> 5) * 2 + (kblk >> 1)] = (uint8_t)ks;
     }
-    if (lane == 0) s.there[wave * KPW / 16] = there_w;
   };
   auto store_values = [&](Stage& s, int w) {         // w: dword of the piece
     if (has_v) {
@@ -676,67 +683,31 @@ kv_attention_rows_kernel(KvAttnArgs a) {
     any_alpha = __any(alpha != 1.0f);
   };
   uint32_t p[16];                // pairs of weights, in the order of the value products
-  float sum[2];
-  auto weight_pair = [&](const v16f (&sc)[2], int i) {
-    const float x = exp2_fast(sc[i >> 3][2 * (i & 7)]), y = exp2_fast(sc[i >> 3][2 * (i & 7) + 1]);
-    sum[0] += x;
-    sum[1] += y;
-    p[i] = pack_bf16(x, y);
-  };
-  // The weights of `sc` beside the scores of the next tile.
-  auto weights_and_scores = [&](const v16f (&sc)[2], const Stage& s, v16f (&nx)[2]) {
-    constexpr int N = 6 * NS, HEAD = 4;              // products; pairs done while the keys come in
-    const int ksw = *reinterpret_cast<const int*>(s.ks[half][row]);
-    v4i x[NS][2];
+  float sum;
+  auto weights = [&](const v16f (&sc)[2], float from) __attribute__((always_inline)) {
+    float even = 0.0f, odd = 0.0f;
 #pragma unroll
-    for (int ds = 0; ds < NS; ++ds)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        const int blk = 2 * ds + half;
-        x[ds][kb] = v4i{0, 0, 0, 0};
-        if (NB % 2 == 0 || blk < NB) x[ds][kb] = *reinterpret_cast<const v4i*>(s.k + k_off(kb * 32 + row, blk));
-      }
-    keep_order();
-    sum[0] = sum[1] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < HEAD; ++i) weight_pair(sc, i);
-    nx[0] = nx[1] = v16f{};
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      keep_order();
-      const int ds = i / 6, t = i % 6 / 2, kb = i & 1;
-      nx[kb] = score_term(x[ds][kb], q[ds][t], nx[kb], kb * 2 + ds, ksw, t, (int)q_scales[ds]);
-      keep_order();
-#pragma unroll
-      for (int k = HEAD + (16 - HEAD) * i / N; k < HEAD + (16 - HEAD) * (i + 1) / N; ++k) weight_pair(sc, k);
+    for (int i = 0; i < 16; ++i) {
+      const float x = exp2_fast(sc[i >> 3][2 * (i & 7)] - from), y = exp2_fast(sc[i >> 3][2 * (i & 7) + 1] - from);
+      even += x;
+      odd += y;
+      p[i] = pack_bf16(x, y);
     }
+    sum = even + odd;
   };
-  // The values of a tile, read three products ahead, with `side(k)`, k = 0 .. SIDES - 1,
-  // spread between the products.
-  constexpr int SIDES = 7 + VW;
-  auto values = [&](const Stage& s, auto side) {
-    constexpr int N = 4 * ND, AHEAD = 3;             // products: 16 keys x 32 elements each
+  auto values = [&](const Stage& s) {
     const int key0 = 4 * half + ((lane & 15) >> 2), run0 = (lane >> 4) & 1, piece = (lane >> 1) & 1;
-    v4s x[N], y[N];
-    auto read = [&](int i) {
-      const int key = key0 + i / ND * 16, run = 2 * (i % ND) + run0;
-      x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(s.v + v_off<RS>(key, run, piece) + (lane & 1) * 8));
-      y[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(s.v + v_off<RS>(key + 8, run, piece) + (lane & 1) * 8));
-    };
-    keep_order();
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) read(i);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      keep_order();
-      if (i + AHEAD < N) read(i + AHEAD);
-      const v8bf v = __builtin_bit_cast(v8bf, __builtin_shufflevector(x[i], y[i], 0, 1, 2, 3, 4, 5, 6, 7));
-      const int u = i / ND;
+    for (int u = 0; u < 4; ++u) {                    // 16 keys each
       const v8bf w = __builtin_bit_cast(v8bf, make_uint4(p[4 * u], p[4 * u + 1], p[4 * u + 2], p[4 * u + 3]));
-      o[i % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w, o[i % ND], 0, 0, 0);
-      keep_order();
 #pragma unroll
-      for (int k = SIDES * i / N; k < SIDES * (i + 1) / N; ++k) side(k);
+      for (int d = 0; d < ND; ++d) {
+        const int key = key0 + 16 * u, run = 2 * d + run0;
+        const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(s.v + v_off<RS>(key, run, piece) + (lane & 1) * 8));
+        const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(s.v + v_off<RS>(key + 8, run, piece) + (lane & 1) * 8));
+        const v8bf v = __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w, o[d], 0, 0, 0);
+      }
     }
   };
 
@@ -744,7 +715,7 @@ kv_attention_rows_kernel(KvAttnArgs a) {
   fetch(t0);
   next_page(t0 + 1);
   if constexpr (NB % 2 != 0) {   // scale bytes of blocks that do not exist: any finite scale
-    for (int i = tid; i < 3 * 64; i += NW * 64)
+    for (int i = tid; i < 2 * 64; i += NW * 64)
       reinterpret_cast<uint32_t*>(st[i / 64].ks)[i % 64] = 0x7F7F7F7Fu;
     __syncthreads();
   }
@@ -752,75 +723,54 @@ kv_attention_rows_kernel(KvAttnArgs a) {
   store(st[0]);
   fetch(t0 + 1);
   next_page(t0 + 2);
-  settle();
-  store(st[1]);
-  fetch(t0 + 2);
-  next_page(t0 + 3);
   tile::lds_barrier();
-  v16f sc[2], nx[2];
-  scores(st[0], sc);
-  v4i there_t = *reinterpret_cast<const v4i*>(st[0].there);
-  int at = 0;                    // stage of tile t
   for (int t = t0; t < t1; ++t) {
-    const int at1 = at == 2 ? 0 : at + 1, at2 = at == 0 ? 2 : at - 1;
-    const Stage& s = st[at];
+    const Stage& s = st[(t - t0) & 1];
     const int j0 = t * TILE;
-    if (j0 < seen_hi) {          // else no row of the wave sees the tile, nor a later one
-      const v4i there = there_t;
-      if (j0 + TILE > seen_lo || (there[0] & there[1] & there[2] & there[3]) == 0) {
+    // The next tile goes to the other stage, whose readers were done before the last
+    // barrier, between this tile's weights and values: the loads have had a tile's time to
+    // arrive, the writes have the value products to land.
+    auto bring = [&]() {
+      settle();
+      store(st[(t + 1 - t0) & 1]);
+      fetch(t + 2);              // past the range: no page, no loads
+      next_page(t + 3);
+    };
+    if (j0 >= seen_hi) {         // no row of the wave sees the tile, nor a later one
+      bring();
+    } else {
+      v16f sc[2];
+      scores(s, sc);
+      if (j0 + TILE > seen_lo || holes) {
         const int left = seen - j0 - half * 4;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (kb * 32 + (r >> 2) * 8 + (r & 3) >= left || there[kb * 2 + (r >> 3)] == 0) sc[kb][r] = kNegInf;
-      }
-      const bool exact = any_fresh && __any(fresh && j0 < seen);
-      if (exact) raise(sc);
-      if (any_ref) {
-        sc[0] -= ref;
-        sc[1] -= ref;
-      }
-      weights_and_scores(sc, st[at1], nx);     // of tile t + 1 (a stale stage at the end)
-      asm volatile("" : "+v"(nx[0]), "+v"(nx[1]));   // or the products would sink below the branches
-      if (!exact && __any(!(sum[0] + sum[1] < 0x1p40f))) {
-        const float old = ref;
-        sc[0] += old;
-        sc[1] += old;
-        raise(sc);
-        sc[0] -= ref;
-        sc[1] -= ref;
-        sum[0] = sum[1] = 0.0f;
+          for (int g = 0; g < 2; ++g) {
+            const int pi = (j0 + kb * 32 + g * 16) >> c.page_shift;
+            const bool there = !holes || (pi < a.table_stride && (unsigned)table[pi] < (unsigned)c.num_pages);
+            const int mine = there ? left : 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) weight_pair(sc, i);
+            for (int r = g * 8; r < g * 8 + 8; ++r)
+              if (kb * 32 + (r >> 2) * 8 + (r & 3) >= mine) sc[kb][r] = kNegInf;
+          }
       }
-      l += sum[0] + sum[1];
+      bool exact = any_fresh && __any(fresh && j0 < seen);
+      for (;;) {
+        if (exact) raise(sc);
+        if (any_ref) weights(sc, ref); else weights(sc, 0.0f);
+        if (exact || !__any(!(sum < 0x1p40f))) break;
+        exact = true;
+      }
+      l += sum;
       if (any_alpha) {
 #pragma unroll
         for (int d = 0; d < ND; ++d) o[d] *= alpha;
         any_alpha = false;
       }
-      // beside the values: tile t + 2 into the stage whose readers were done before the last
-      // barrier, then tile t + 3 from memory (past the range: no page, no loads)
-      settle();
-      there_t = *reinterpret_cast<const v4i*>(st[at1].there);
-      values(s, [&](int k) {
-        if (k == 0) store_keys(st[at2]);
-        else if (k <= VW) store_values(st[at2], k - 1);
-        else if (k == VW + 1) fetch(t + 3);
-        else if (k == VW + 2) next_page(t + 4);
-        else {                     // and the next scores take their place
-#pragma unroll
-          for (int r = 0; r < 8; ++r) sc[(k - VW - 3) >> 1][(k - VW - 3) % 2 * 8 + r] = nx[(k - VW - 3) >> 1][(k - VW - 3) % 2 * 8 + r];
-        }
-      });
-    } else {
-      settle();
-      store(st[at2]);
-      fetch(t + 3);
-      next_page(t + 4);
+      bring();
+      values(s);
     }
-    at = at1;
     tile::lds_barrier();
   }
   {
@@ -943,7 +893,6 @@ kv_attention_join_kernel(KvAttnArgs a) {
     a.lse[row] = L == 0.0f ? kNegInf : (M + __builtin_log2f(L)) * 0.6931471805599453f;
 }
 
-constexpr int kWaves = 4;
 // Rows of a (sequence, key head) that one workgroup takes: 16 (the keys split over its
 // waves) while they fit, else 128.
 inline bool few_rows(int max_q, int group) { return (long long)max_q * group <= 16; }
@@ -951,11 +900,11 @@ inline bool few_rows(int max_q, int group) { return (long long)max_q * group <= 
 template <int NB>
 hipError_t launch_nb(const KvAttnArgs& a, hipStream_t s) {
   const bool few = few_rows(a.max_q, a.group);
-  const int per = few ? 16 : kWaves * 32;
+  const int per = few ? 16 : 128;
   const int row_tiles = (int)(((long long)a.max_q * a.group + per - 1) / per);
   const dim3 grid((unsigned)((long long)row_tiles * a.splits), (unsigned)a.cache.heads, (unsigned)a.seqs);
   if (few) kv_attention_rows16_kernel<NB, 4><<<grid, 256, 0, s>>>(a);
-  else kv_attention_rows_kernel<NB, kWaves><<<grid.x * grid.y * grid.z, kWaves * 64, 0, s>>>(a);
+  else kv_attention_rows128_kernel<NB><<<grid.x * grid.y * grid.z, 256, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   constexpr int RPW = 256 / (8 * NB);
@@ -970,7 +919,7 @@ int kv_attention_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_
   if (seqs <= 0 || max_q <= 0 || kv_heads <= 0) return 1;
   const int group = q_heads / kv_heads;
   const bool few = few_rows(max_q, group);
-  const long long row_tiles = ((long long)max_q * group + (few ? 15 : kWaves * 32 - 1)) / (few ? 16 : kWaves * 32);
+  const long long row_tiles = ((long long)max_q * group + (few ? 15 : 127)) / (few ? 16 : 128);
   const long long base = (long long)seqs * kv_heads * row_tiles;
   const long long tiles = ((long long)max_kv + TILE - 1) / TILE;
   if (few) {
@@ -983,7 +932,7 @@ int kv_attention_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_
   // 128 rows: the splits whose rounds of workgroups over the chip's slots take least.  A
   // range costs its tiles and about six more to start; each split's partial sums cost the
   // chip about one tile's time a row tile in two slots.
-  const long long slots = (kWaves == 8 ? 1ll : 2ll) * NUM_CUS;
+  const long long slots = 2ll * NUM_CUS;
   long long best = 0;
   int splits = 1;
   for (int n = 1; n <= 64 && n <= (tiles + 3) / 4; ++n) {
