@@ -212,17 +212,24 @@ __device__ __forceinline__ int seen_keys(const KvAttnArgs& a, int len, int n, in
 }
 
 // One workgroup: 16 rows (queries x heads of the group) of one key head of one
-// sequence over one range of its keys; the range's tiles go to the waves in runs.
-template <int NB, int NW>
-__global__ void __launch_bounds__(NW * 64)
+// sequence over one range of its keys; the range's tiles go to the waves in runs and
+// every wave works by itself until the end.  Bound by the cache's bytes: a wave asks
+// for the next tile's codes and scales (8.7 KB at 128 elements) as soon as this one's
+// are in LDS or in the matrix core, and four workgroups fit a CU (8.4 KB of LDS a
+// wave: values are staged 32 keys at a time).
+template <int NB>
+__global__ void __launch_bounds__(256, NB <= 2 ? 4 : 3)
 kv_attention_rows16_kernel(KvAttnArgs a) {
+  constexpr int NW = 4;
   constexpr int DP = NB * 32;
+  constexpr int ND = DP / 16;                         // 16-element output blocks
   constexpr int RS = NB <= 2 ? 128 : 256;             // bytes of a staged value row
-  constexpr int STAGE = TILE * RS;
+  constexpr int STAGE = 32 * RS;
   constexpr int MERGE = 16 * (DP + 4) * 4;            // one wave's sums, rows padded against banks
   constexpr int PER_WAVE = STAGE > MERGE ? STAGE : MERGE;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NW * PER_WAVE + NW * 16 * 8];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, g = lane >> 4;
   const int b = blockIdx.z, hk = blockIdx.y;
   const int sp = blockIdx.x % a.splits, row_tile = blockIdx.x / a.splits;
@@ -235,139 +242,189 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   const int len = seq_keys(a, b);
   const int qi = (r0 + row) / a.group, qh = hk * a.group + (r0 + row) % a.group;
   const bool row_ok = qi < n;
-  const int seen = row_ok ? seen_keys(a, len, n, qi) : 0;
-  int seen_max = seen;
+  const int last = (min(r0 + 16, n * a.group) - 1) / a.group;
+  const int seen_hi = seen_keys(a, len, n, last), seen_lo = seen_keys(a, len, n, r0 / a.group);
+  const int seen = row_ok ? seen_keys(a, len, n, qi) : seen_hi;     // idle rows hide nothing
+
+  int t0, t1;
+  split_range((seen_hi + TILE - 1) / TILE, a.splits, sp, t0, t1);
+  const int per = (t1 - t0 + NW - 1) / NW;
+  const int w0 = min(t0 + wave * per, t1), w1 = min(w0 + per, t1);
+
+  const int* table = a.table + (long long)b * a.table_stride;
+  const int in_page = (1 << c.page_shift) - 1;
+  const long long page_rows = (long long)c.heads << c.page_shift, head_row = (long long)hk << c.page_shift;
+  // lane: key l%16 and block l/16 of each group of 16 keys, which lie in one page
+  const bool has = g < NB;
+  const unsigned c_at = row * (DP / 2) + (has ? g * 16 : 0), s_at = row * NB + (has ? g : 0);
+  bool holes = false;            // whether a page of the range is not in the cache
+  for (int i = (w0 * TILE >> c.page_shift) + lane; i < a.table_stride && i <= (min(w1 * TILE, len) - 1) >> c.page_shift; i += 64)
+    holes = holes || (unsigned)table[i] >= (unsigned)c.num_pages;
+  holes = __any(holes);
+  v4i kc[4], vc[4];
+  uint32_t ks[4], vs[4];
+  int page[4];
+  auto pages = [&](int t) {
 #pragma unroll
-  for (int m = 8; m > 0; m >>= 1) seen_max = max(seen_max, __shfl_xor(seen_max, m, 64));
+    for (int k = 0; k < 4; ++k) {
+      const int j = t * TILE + 16 * k;
+      page[k] = t < w1 && j < len ? table[min(j >> c.page_shift, a.table_stride - 1)] : -1;
+    }
+  };
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int pg = __builtin_amdgcn_readfirstlane(page[k]);
+      const int j = t * TILE + 16 * k;
+      const bool there = (unsigned)pg < (unsigned)c.num_pages;
+      const long long r = pg * page_rows + head_row + (j & in_page);
+      if (there && j + 16 <= len) {
+        kc[k] = *reinterpret_cast<const v4i*>(c.k_codes + r * (DP / 2) + c_at);
+        vc[k] = *reinterpret_cast<const v4i*>(c.v_codes + r * (DP / 2) + c_at);
+        ks[k] = (c.k_scales + r * NB)[s_at];
+        vs[k] = (c.v_scales + r * NB)[s_at];
+      } else {
+        kc[k] = vc[k] = v4i{0, 0, 0, 0};
+        ks[k] = vs[k] = 127u;
+        if (there && row < len - j) {
+          kc[k] = *reinterpret_cast<const v4i*>(c.k_codes + r * (DP / 2) + c_at);
+          vc[k] = *reinterpret_cast<const v4i*>(c.v_codes + r * (DP / 2) + c_at);
+          ks[k] = (c.k_scales + r * NB)[s_at];
+          vs[k] = (c.v_scales + r * NB)[s_at];
+        }
+      }
+    }
+  };
+  pages(w0);
+  fetch(w0);
+  pages(w0 + 1);
 
   // B operand: row l%16, block l/16
-  v8i q[3] = {};
+  v8i q[3];
   uint32_t q_scales = 0u;
-  if (row_ok && g < NB) {
+#pragma unroll
+  for (int t = 0; t < 3; ++t) q[t] = v8i{0, 0, 0, 0, 0, 0, 0, 0};
+  if (row_ok && has) {
     float x[32];
     const bool ok = load_q_block(a, q0 + qi, qh, g, base2_scale(a), x);
     q_terms(x, ok, q, q_scales);
   }
 
-  const int tiles = (seen_max + TILE - 1) / TILE;
-  int t0, t1;
-  split_range(tiles, a.splits, sp, t0, t1);
-  const int per = (t1 - t0 + NW - 1) / NW;
-  const int w0 = min(t0 + wave * per, t1), w1 = min(w0 + per, t1);
-  const int page_size = 1 << c.page_shift;
-
-  float m = kNegInf, l = 0.0f;
-  v4f o[DP / 16];
+  float ref = 0.0f, l = 0.0f;
+  bool fresh = true, any_fresh = true;
+  v4f o[ND];
 #pragma unroll
-  for (int d = 0; d < DP / 16; ++d) o[d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int d = 0; d < ND; ++d) o[d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   uint8_t* stage = smem + wave * PER_WAVE;
 
   for (int t = w0; t < w1; ++t) {
     const int j0 = t * TILE;
-    // pages of the tile's four groups of 16 keys
-    long long base[4];
-    bool there[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int j = j0 + 16 * k;
-      const int pi = j >> c.page_shift;
-      int page = -1;
-      if (j < len && pi < a.table_stride) page = a.table[(long long)b * a.table_stride + pi];
-      there[k] = page >= 0 && page < c.num_pages;
-      base[k] = there[k] ? ((((long long)page * c.heads + hk) << c.page_shift) + (j & (page_size - 1))) : 0;
-    }
-    // scores: 16 keys an instruction
     v4f s[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      v4i kc = {0, 0, 0, 0};
-      int ks = 127;
-      if (there[k] && g < NB) {
-        const long long r = base[k] + row;
-        kc = *reinterpret_cast<const v4i*>(c.k_codes + r * (DP / 2) + g * 16);
-        ks = c.k_scales[r * NB + g];
+      // a value scale beyond bf16 (or NaN): the key's scores become NaN, its values zero
+      const unsigned long long bad = __ballot(has && vs[k] > kMaxValueScale);
+      if (bad != 0 && ((bad >> row) & 0x0001000100010001ull) != 0) {
+        ks[k] = 255u;
+        vs[k] = 127u;
+        vc[k] = v4i{0, 0, 0, 0};
       }
-      const v8i ka = {kc[0], kc[1], kc[2], kc[3], 0, 0, 0, 0};
+      // blocks that do not exist (lanes past NB) are zeros on the side of q
+      const v8i ka = {kc[k][0], kc[k][1], kc[k][2], kc[k][3], 0, 0, 0, 0};
+      const int kw = has ? (int)ks[k] : 127;
       s[k] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      s[k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ka, q[0], s[k], 4, 2, 0, ks, 0, (int)q_scales);
-      s[k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ka, q[1], s[k], 4, 2, 0, ks, 1, (int)q_scales);
-      s[k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ka, q[2], s[k], 4, 2, 0, ks, 2, (int)q_scales);
+      s[k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ka, q[0], s[k], 4, 2, 0, kw, 0, (int)q_scales);
+      s[k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ka, q[1], s[k], 4, 2, 0, kw, 1, (int)q_scales);
+      s[k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ka, q[2], s[k], 4, 2, 0, kw, 2, (int)q_scales);
     }
-    // values to bf16 in LDS: one MX block a lane and step; keys past the end as zeros
+    // lane: keys 16 k + 4 g + r of its row
+    if (j0 + TILE > seen_lo || holes) {
+      const int left = seen - j0 - 4 * g;
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int key = unit_key<NB>(i * 64 + lane), blk = unit_block<NB>(i * 64 + lane), k = key >> 4;
-      v4i vc = {0, 0, 0, 0};
-      uint32_t vs = 127u;
-      const long long bk = k == 0 ? base[0] : k == 1 ? base[1] : k == 2 ? base[2] : base[3];
-      const bool tk = k == 0 ? there[0] : k == 1 ? there[1] : k == 2 ? there[2] : there[3];
-      if (tk && j0 + key < len) {
-        const long long r = bk + (key & 15);
-        vc = *reinterpret_cast<const v4i*>(c.v_codes + r * (DP / 2) + blk * 16);
-        vs = c.v_scales[r * NB + blk];
-      }
-      const float f = __uint_as_float(vs << 23);
+      for (int k = 0; k < 4; ++k) {
+        const int pi = (j0 + 16 * k) >> c.page_shift;
+        const bool there = !holes || (pi < a.table_stride && (unsigned)table[pi] < (unsigned)c.num_pages);
+        const int mine = there ? left : 0;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t x = (uint32_t)vc[w];
-        uint4 y;
-        y.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 0));
-        y.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 1));
-        y.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 2));
-        y.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 3));
-        *reinterpret_cast<uint4*>(stage + v_off<RS>(key, blk * 2 + (w >> 1), w & 1)) = y;
+        for (int r = 0; r < 4; ++r)
+          if (16 * k + r >= mine) s[k][r] = kNegInf;
       }
     }
-    // softmax: lane holds keys 16 k + 4 g + r of its row
-    float top = kNegInf;
+    // weights: as in the kernel for 128 rows, 2^(s - ref) with a reference only where needed
+    float sum;
+    uint32_t p[8];
+    bool exact = any_fresh && __any(fresh && j0 < seen);
+    for (;;) {
+      if (exact) {
+        float top = kNegInf;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const bool vis = there[k] && j0 + 16 * k + 4 * g + r < seen;
-        s[k][r] = vis ? s[k][r] : kNegInf;
-        top = fmaxf(top, s[k][r]);
+          for (int r = 0; r < 4; ++r) top = fmaxf(top, s[k][r]);
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const bool first = fresh && top > kNegInf;
+        fresh = fresh && !first;
+        any_fresh = __any(fresh);
+        const bool up = first ? fabsf(top) > 40.0f : !fresh && top > ref;
+        const float by = up ? top - ref : 0.0f;
+        const float alpha = first ? 1.0f : exp2_fast(-by);
+        ref += by;
+        l *= alpha;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[d] *= alpha;
       }
-    top = fmaxf(top, __shfl_xor(top, 16, 64));
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
-    const float m_new = fmaxf(m, top);
-    const float ref = m_new == kNegInf ? 0.0f : m_new;
-    const float alpha = exp2_fast(m - ref);
-    m = m_new;
-    l *= alpha;
+      sum = 0.0f;
 #pragma unroll
-    for (int d = 0; d < DP / 16; ++d) o[d] *= alpha;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        s[k][r] = exp2_fast(s[k][r] - ref);
-        l += s[k][r];
+      for (int k = 0; k < 4; ++k) {
+        const float w0_ = exp2_fast(s[k][0] - ref), w1_ = exp2_fast(s[k][1] - ref);
+        const float w2_ = exp2_fast(s[k][2] - ref), w3_ = exp2_fast(s[k][3] - ref);
+        sum += (w0_ + w1_) + (w2_ + w3_);
+        p[2 * k] = pack_bf16(w0_, w1_);
+        p[2 * k + 1] = pack_bf16(w2_, w3_);
       }
-    // values: the wave's own staging, written above
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_wave_barrier();
+      if (exact || !__any(!(sum < 0x1p40f))) break;
+      exact = true;
+    }
+    l += sum;
+    // values, 32 keys at a time through the wave's own staging (LDS serves a wave in order)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      v8bf p;
+      if (has) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        p[r] = (__bf16)s[2 * h][r];
-        p[4 + r] = (__bf16)s[2 * h + 1][r];
+        for (int k = 2 * h; k < 2 * h + 2; ++k) {
+          const float f = __uint_as_float(vs[k] << 23);
+          const int key = (k & 1) * 16 + row;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t x = (uint32_t)vc[k][w];
+            uint4 y;
+            y.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 0));
+            y.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 1));
+            y.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 2));
+            y.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 3));
+            *reinterpret_cast<uint4*>(stage + v_off<RS>(key, g * 2 + (w >> 1), w & 1)) = y;
+          }
+        }
       }
+      if (h == 1) {                                    // the tile's registers are free
+        fetch(t + 1);                                  // past the range: no page, no loads
+        pages(t + 2);
+      }
+      __builtin_amdgcn_wave_barrier();
+      const v8bf w = __builtin_bit_cast(v8bf, make_uint4(p[4 * h], p[4 * h + 1], p[4 * h + 2], p[4 * h + 3]));
 #pragma unroll
-      for (int d = 0; d < DP / 16; ++d) {
-        const int key = 32 * h + 4 * g + (row >> 2);
+      for (int d = 0; d < ND; ++d) {
+        const int key = 4 * g + (row >> 2);
         const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (lds_v4s)(stage + v_off<RS>(key, d, (row >> 1) & 1) + (row & 1) * 8));
         const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (lds_v4s)(stage + v_off<RS>(key + 16, d, (row >> 1) & 1) + (row & 1) * 8));
         const v8bf v = __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p, o[d], 0, 0, 0);
+        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w, o[d], 0, 0, 0);
       }
+      __builtin_amdgcn_wave_barrier();
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-    __builtin_amdgcn_wave_barrier();
   }
   l += __shfl_xor(l, 16, 64);
   l += __shfl_xor(l, 32, 64);
@@ -376,10 +433,10 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   float* sums = reinterpret_cast<float*>(stage);
   float* ml = reinterpret_cast<float*>(smem + NW * PER_WAVE);
 #pragma unroll
-  for (int d = 0; d < DP / 16; ++d)
+  for (int d = 0; d < ND; ++d)
     *reinterpret_cast<v4f*>(sums + row * (DP + 4) + d * 16 + g * 4) = o[d];
   if (g == 0) {
-    ml[(wave * 16 + row) * 2] = m;
+    ml[(wave * 16 + row) * 2] = fresh ? kNegInf : ref;
     ml[(wave * 16 + row) * 2 + 1] = l;
   }
   __syncthreads();
@@ -390,13 +447,13 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   float M = kNegInf;
 #pragma unroll
   for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * 16 + fr) * 2]);
-  const float ref = M == kNegInf ? 0.0f : M;
+  const float base = M == kNegInf ? 0.0f : M;
   float x[32], L = 0.0f;
 #pragma unroll
   for (int e = 0; e < 32; ++e) x[e] = 0.0f;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    const float f = exp2_fast(ml[(w * 16 + fr) * 2] - ref);
+    const float f = exp2_fast(ml[(w * 16 + fr) * 2] - base);
     L += f * ml[(w * 16 + fr) * 2 + 1];
     const float* src = reinterpret_cast<const float*>(smem + w * PER_WAVE) + fr * (DP + 4) + fb * 32;
 #pragma unroll
@@ -840,20 +897,24 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     a.lse[out_row] = l == 0.0f ? kNegInf : (ref + __builtin_log2f(l)) * 0.6931471805599453f;
 }
 
-// Joins the splits of each row: a lane holds four elements of one row, eight
-// lanes a block of 32.
-template <int NB>
+// Joins the splits of each row: a lane holds four elements of one row, eight lanes a
+// block of 32.  WIDE: the groups of lanes of a workgroup share one row's splits (every
+// GROUPS-th each) and add up through LDS, for few rows of many splits; else each has a
+// row of its own.  Both orders are fixed.
+template <int NB, bool WIDE>
 __global__ void __launch_bounds__(256)
 kv_attention_join_kernel(KvAttnArgs a) {
   constexpr int DP = NB * 32;
   constexpr int LPR = 8 * NB;              // lanes of a row
-  constexpr int RPW = 256 / LPR;           // rows of a workgroup
+  constexpr int GROUPS = 256 / LPR;
+  __shared__ float part[WIDE ? GROUPS : 1][DP + 2];
   const int b = blockIdx.y;
   int q0, n;
   seq_rows(a, b, q0, n);
-  const int lr = threadIdx.x / LPR, li = threadIdx.x % LPR, lane = threadIdx.x & 63;
-  const int r = blockIdx.x * RPW + lr;
-  const bool ok = lr < RPW && r < n * a.q_heads;
+  const int gr = threadIdx.x / LPR, li = threadIdx.x % LPR, lane = threadIdx.x & 63;
+  const int r = WIDE ? blockIdx.x : blockIdx.x * GROUPS + gr;
+  if (WIDE && r >= n * a.q_heads) return;
+  const bool ok = gr < GROUPS && r < n * a.q_heads;
   const KvCacheArgs& c = a.cache;
   const long long rows = (long long)a.tokens * a.q_heads;
   const long long row = (long long)q0 * a.q_heads + (ok ? r : 0);
@@ -863,10 +924,25 @@ kv_attention_join_kernel(KvAttnArgs a) {
   if (ok) {
     for (int s = 0; s < a.splits; ++s) M = fmaxf(M, st[(s * rows + row) * 2]);
     const float ref = M == kNegInf ? 0.0f : M;
-    for (int s = 0; s < a.splits; ++s) {
+    for (int s = WIDE ? gr : 0; s < a.splits; s += WIDE ? GROUPS : 1) {
       const float f = exp2_fast(st[(s * rows + row) * 2] - ref);
       L += f * st[(s * rows + row) * 2 + 1];
       x += f * *reinterpret_cast<const v4f*>(a.part + (s * rows + row) * DP + li * 4);
+    }
+  }
+  if constexpr (WIDE) {
+    if (gr < GROUPS) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[gr][li * 4 + e] = x[e];
+      if (li == 0) part[gr][DP] = L;
+    }
+    __syncthreads();
+    if (gr == 0) {
+      for (int k = 1; k < GROUPS; ++k) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] += part[k][li * 4 + e];
+        L += part[k][DP];
+      }
     }
   }
   if (c.had) {
@@ -884,7 +960,7 @@ kv_attention_join_kernel(KvAttnArgs a) {
     }
     x = v4f{v[0], v[1], v[2], v[3]};
   }
-  if (!ok) return;
+  if (!ok || (WIDE && gr != 0)) return;
   const float inv = L == 0.0f ? 0.0f : (c.had ? 0.03125f : 1.0f) / L;
   if (li * 4 < c.head_dim)
     *reinterpret_cast<uint2*>(a.out + row * c.head_dim + li * 4) =
@@ -903,13 +979,17 @@ hipError_t launch_nb(const KvAttnArgs& a, hipStream_t s) {
   const int per = few ? 16 : 128;
   const int row_tiles = (int)(((long long)a.max_q * a.group + per - 1) / per);
   const dim3 grid((unsigned)((long long)row_tiles * a.splits), (unsigned)a.cache.heads, (unsigned)a.seqs);
-  if (few) kv_attention_rows16_kernel<NB, 4><<<grid, 256, 0, s>>>(a);
+  if (few) kv_attention_rows16_kernel<NB><<<grid, 256, 0, s>>>(a);
   else kv_attention_rows128_kernel<NB><<<grid.x * grid.y * grid.z, 256, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  constexpr int RPW = 256 / (8 * NB);
-  const dim3 jgrid((unsigned)(((long long)a.max_q * a.q_heads + RPW - 1) / RPW), (unsigned)a.seqs);
-  kv_attention_join_kernel<NB><<<jgrid, 256, 0, s>>>(a);
+  const long long rows = (long long)a.max_q * a.q_heads;
+  if (a.splits > 8) {
+    kv_attention_join_kernel<NB, true><<<dim3((unsigned)rows, (unsigned)a.seqs), 256, 0, s>>>(a);
+  } else {
+    constexpr int RPW = 256 / (8 * NB);
+    kv_attention_join_kernel<NB, false><<<dim3((unsigned)((rows + RPW - 1) / RPW), (unsigned)a.seqs), 256, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 
