@@ -44,6 +44,7 @@ constexpr float kNegInf = -__builtin_inff();
 constexpr uint32_t kMaxValueScale = 252;   // 6 * 2^(252 - 127) is the largest finite value
 constexpr int TILE = 64;      // keys a wave takes at a time
 constexpr int NUM_CUS = 256;  // MI355X
+constexpr int kMaxSplits = 128;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -189,11 +190,25 @@ __device__ __forceinline__ void q_terms(float (&x)[32], bool ok, v8i (&q)[3], ui
   }
 }
 
-// The range of tiles [t0, t1) of split `sp`, of `tiles` tiles in all.
-__device__ __forceinline__ void split_range(int tiles, int splits, int sp, int& t0, int& t1) {
-  const int per = (tiles + splits - 1) / splits;
+// The range of tiles [t0, t1) of split `sp`, of `tiles` tiles in all.  A sequence has as
+// many splits as its length needs at the share of the longest one there may be, alike in
+// length: the workgroups of a ragged batch cost about the same.
+__device__ __forceinline__ void split_range(const KvAttnArgs& a, int tiles, int sp, int& t0, int& t1) {
+  const int most = (a.max_kv + TILE - 1) / TILE, share = max((most + a.splits - 1) / a.splits, 1);
+  const int parts = max((tiles + share - 1) / share, 1), per = (tiles + parts - 1) / parts;
   t0 = min(sp * per, tiles);
   t1 = min(t0 + per, tiles);
+}
+
+// Where the partial result of split `sp` for row `row` of tokens x q_heads goes: dim_pad
+// sums at part_sums, (maximum, sum) at part_stats.  A split without keys writes (-inf, 0)
+// and no sums.
+__device__ __forceinline__ float* part_sums(const KvAttnArgs& a, int sp, long long row) {
+  return a.part + ((long long)sp * a.tokens * a.q_heads + row) * a.cache.dim_pad;
+}
+__device__ __forceinline__ float2* part_stats(const KvAttnArgs& a, int sp, long long row) {
+  const long long rows = (long long)a.tokens * a.q_heads;
+  return reinterpret_cast<float2*>(a.part + (long long)a.splits * rows * a.cache.dim_pad) + sp * rows + row;
 }
 
 // First query row and number of queries of sequence b, inside [0, tokens].
@@ -218,7 +233,7 @@ __device__ __forceinline__ int seen_keys(const KvAttnArgs& a, int len, int n, in
 // are in LDS or in the matrix core, and four workgroups fit a CU (8.4 KB of LDS a
 // wave: values are staged 32 keys at a time).
 template <int NB>
-__global__ void __launch_bounds__(256, NB <= 2 ? 4 : 3)
+__global__ void __launch_bounds__(256, 3)
 kv_attention_rows16_kernel(KvAttnArgs a) {
   constexpr int NW = 4;
   constexpr int DP = NB * 32;
@@ -247,7 +262,12 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   const int seen = row_ok ? seen_keys(a, len, n, qi) : seen_hi;     // idle rows hide nothing
 
   int t0, t1;
-  split_range((seen_hi + TILE - 1) / TILE, a.splits, sp, t0, t1);
+  split_range(a, (seen_hi + TILE - 1) / TILE, sp, t0, t1);
+  if (a.splits > 1 && t0 >= t1) {
+    if (threadIdx.x < 16 && row_ok)
+      *part_stats(a, sp, (long long)(q0 + qi) * a.q_heads + qh) = make_float2(kNegInf, 0.0f);
+    return;
+  }
   const int per = (t1 - t0 + NW - 1) / NW;
   const int w0 = min(t0 + wave * per, t1), w1 = min(w0 + per, t1);
 
@@ -299,16 +319,55 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   fetch(w0);
   pages(w0 + 1);
 
-  // B operand: row l%16, block l/16
+  // q': eight elements a thread, through LDS to the B operand (row l%16, block l/16)
+  float* qs = reinterpret_cast<float*>(smem);
+  constexpr int QROW = DP + 4;
+  static_assert(16 * QROW * 4 <= NW * PER_WAVE, "q' fits the staging");
+  if ((int)threadIdx.x < 64 * NB) {
+    const int qr = threadIdx.x / (4 * NB), e0 = threadIdx.x % (4 * NB) * 8;
+    const int i = (r0 + qr) / a.group, h = hk * a.group + (r0 + qr) % a.group;
+    float x[8] = {};
+    if (i < n && e0 < c.head_dim) {
+      RopeArgs rope = a.rope;
+      int pos = 0;
+      if (rope.rope_dim > 0) {
+        pos = a.positions[q0 + i];
+        if (pos < 0 || pos >= rope.num_positions) rope.rope_dim = -1;
+      }
+      if (rope.rope_dim < 0) {                 // no such table row: not a number
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __builtin_nanf("");
+      } else {
+        load8_turned(a.q + (long long)(q0 + i) * a.q_stride + (long long)h * c.head_dim, e0, rope, pos, x);
+      }
+    }
+    if (c.had) fwht32_lanes(x, lane);
+    const float factor = base2_scale(a);
+#pragma unroll
+    for (int e = 0; e < 8; e += 4)
+      *reinterpret_cast<v4f*>(qs + qr * QROW + e0 + e) =
+          v4f{x[e] * factor, x[e + 1] * factor, x[e + 2] * factor, x[e + 3] * factor};
+  }
+  __syncthreads();
   v8i q[3];
   uint32_t q_scales = 0u;
 #pragma unroll
   for (int t = 0; t < 3; ++t) q[t] = v8i{0, 0, 0, 0, 0, 0, 0, 0};
-  if (row_ok && has) {
+  if (has) {
     float x[32];
-    const bool ok = load_q_block(a, q0 + qi, qh, g, base2_scale(a), x);
+    bool ok = true;
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      const v4f y = *reinterpret_cast<const v4f*>(qs + row * QROW + g * 32 + e);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[e + k] = y[k];
+        ok = ok && finite_f32(y[k]);
+      }
+    }
     q_terms(x, ok, q, q_scales);
   }
+  __syncthreads();
 
   float ref = 0.0f, l = 0.0f;
   bool fresh = true, any_fresh = true;
@@ -465,15 +524,10 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   }
   const long long out_row = (long long)(q0 + fi) * a.q_heads + fh;
   if (a.splits > 1) {
-    const long long rows = (long long)a.tokens * a.q_heads;
-    float* dst = a.part + ((long long)sp * rows + out_row) * DP + fb * 32;
+    float* dst = part_sums(a, sp, out_row) + fb * 32;
 #pragma unroll
     for (int e = 0; e < 32; e += 4) *reinterpret_cast<v4f*>(dst + e) = v4f{x[e], x[e + 1], x[e + 2], x[e + 3]};
-    if (fb == 0) {
-      float* st = a.part + (long long)a.splits * rows * DP + ((long long)sp * rows + out_row) * 2;
-      st[0] = M;
-      st[1] = L;
-    }
+    if (fb == 0) *part_stats(a, sp, out_row) = make_float2(M, L);
     return;
   }
   const float inv = L == 0.0f ? 0.0f : (c.had ? 0.03125f : 1.0f) / L;   // no visible key: 0
@@ -566,6 +620,14 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   const int seen_lo = seen_keys(a, len, n, min(first, rows - 1) / a.group);
   const int seen_hi = first < rows ? seen_keys(a, len, n, min(first + 31, rows - 1) / a.group) : 0;
 
+  int t0, t1;
+  split_range(a, (seen_all + TILE - 1) / TILE, sp, t0, t1);
+  const long long out_row = (long long)(q0 + qi) * a.q_heads + qh;
+  if (a.splits > 1 && t0 >= t1) {
+    if (half == 0 && row_ok) *part_stats(a, sp, out_row) = make_float2(kNegInf, 0.0f);
+    return;
+  }
+
   // B operands: row l%32, block l/32 of each 64-element step
   v8i q[NS][3];
   uint32_t q_scales[NS];
@@ -582,8 +644,6 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     }
   }
 
-  int t0, t1;
-  split_range((seen_all + TILE - 1) / TILE, a.splits, sp, t0, t1);
   const int in_page = (1 << c.page_shift) - 1;
 
   // A wave brings in KPW keys of a tile, which lie in one page: their rows are one run of
@@ -836,22 +896,16 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     l = lo + hi;
   }
   // lane: elements 32 d + 8 (r / 4) + 4 half + r % 4 of its row
-  const long long out_row = (long long)(q0 + qi) * a.q_heads + qh;
   if (a.splits > 1) {
     if (!row_ok) return;
-    const long long all = (long long)a.tokens * a.q_heads;
-    float* dst = a.part + ((long long)sp * all + out_row) * DP + half * 4;
+    float* dst = part_sums(a, sp, out_row) + half * 4;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
       for (int g = 0; g < 4; ++g)
         *reinterpret_cast<v4f*>(dst + d * 32 + g * 8) =
             v4f{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
-    if (half == 0) {
-      float* ml = a.part + (long long)a.splits * all * DP + ((long long)sp * all + out_row) * 2;
-      ml[0] = fresh ? kNegInf : ref;
-      ml[1] = l;
-    }
+    if (half == 0) *part_stats(a, sp, out_row) = make_float2(fresh ? kNegInf : ref, l);
     return;
   }
   const float inv = l == 0.0f ? 0.0f : (c.had ? 0.03125f : 1.0f) / l;
@@ -907,7 +961,8 @@ kv_attention_join_kernel(KvAttnArgs a) {
   constexpr int DP = NB * 32;
   constexpr int LPR = 8 * NB;              // lanes of a row
   constexpr int GROUPS = 256 / LPR;
-  __shared__ float part[WIDE ? GROUPS : 1][DP + 2];
+  __shared__ float part[WIDE ? GROUPS : 1][DP], weight[WIDE ? 256 : 1], stats[8];
+  static_assert(kMaxSplits <= 256, "one thread a split");
   const int b = blockIdx.y;
   int q0, n;
   seq_rows(a, b, q0, n);
@@ -916,32 +971,59 @@ kv_attention_join_kernel(KvAttnArgs a) {
   if (WIDE && r >= n * a.q_heads) return;
   const bool ok = gr < GROUPS && r < n * a.q_heads;
   const KvCacheArgs& c = a.cache;
-  const long long rows = (long long)a.tokens * a.q_heads;
   const long long row = (long long)q0 * a.q_heads + (ok ? r : 0);
-  const float* st = a.part + (long long)a.splits * rows * DP;
   float M = kNegInf, L = 0.0f;
   v4f x = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (ok) {
-    for (int s = 0; s < a.splits; ++s) M = fmaxf(M, st[(s * rows + row) * 2]);
-    const float ref = M == kNegInf ? 0.0f : M;
-    for (int s = WIDE ? gr : 0; s < a.splits; s += WIDE ? GROUPS : 1) {
-      const float f = exp2_fast(st[(s * rows + row) * 2] - ref);
-      L += f * st[(s * rows + row) * 2 + 1];
-      x += f * *reinterpret_cast<const v4f*>(a.part + (s * rows + row) * DP + li * 4);
+  if constexpr (WIDE) {
+    // one thread a split: maxima and sums at once, the weights to LDS
+    float m = kNegInf, w = 0.0f;
+    if ((int)threadIdx.x < a.splits) {
+      const float2 st = *part_stats(a, threadIdx.x, row);
+      m = st.x;
+      w = st.y;
+    }
+    const bool none = m == kNegInf && w == 0.0f;     // no keys: there are no sums to read
+    M = m;
+#pragma unroll
+    for (int k = 32; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor(M, k, 64));
+    if (lane == 0) stats[threadIdx.x >> 6] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(stats[0], stats[1]), fmaxf(stats[2], stats[3]));
+    const float f = exp2_fast(m - (M == kNegInf ? 0.0f : M));
+    weight[threadIdx.x] = none ? -1.0f : f;
+    w *= f;
+#pragma unroll
+    for (int k = 32; k > 0; k >>= 1) w += __shfl_xor(w, k, 64);
+    if (lane == 0) stats[4 + (threadIdx.x >> 6)] = w;
+    __syncthreads();
+    L = (stats[4] + stats[5]) + (stats[6] + stats[7]);
+    if (ok) {
+#pragma unroll 4
+      for (int s = gr; s < a.splits; s += GROUPS)
+        if (!(weight[s] < 0.0f)) x += weight[s] * *reinterpret_cast<const v4f*>(part_sums(a, s, row) + li * 4);
+    }
+  } else if (ok) {
+    for (int s = 0; s < a.splits; ++s) M = fmaxf(M, part_stats(a, s, row)->x);
+    const float base = M == kNegInf ? 0.0f : M;
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+      const float2 st = *part_stats(a, s, row);
+      if (st.x == kNegInf && st.y == 0.0f) continue;   // no keys: there are no sums to read
+      const float f = exp2_fast(st.x - base);
+      L += f * st.y;
+      x += f * *reinterpret_cast<const v4f*>(part_sums(a, s, row) + li * 4);
     }
   }
   if constexpr (WIDE) {
     if (gr < GROUPS) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) part[gr][li * 4 + e] = x[e];
-      if (li == 0) part[gr][DP] = L;
     }
     __syncthreads();
     if (gr == 0) {
       for (int k = 1; k < GROUPS; ++k) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] += part[k][li * 4 + e];
-        L += part[k][DP];
       }
     }
   }
@@ -1006,7 +1088,7 @@ int kv_attention_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_
     long long want = (4ll * NUM_CUS + base - 1) / base;
     const long long most = (tiles + 3) / 4;   // a range of at least four tiles
     want = want < most ? want : most;
-    if (want > 128) want = 128;
+    if (want > kMaxSplits) want = kMaxSplits;
     return want < 1 ? 1 : (int)want;
   }
   // 128 rows: the splits whose rounds of workgroups over the chip's slots take least.  A
