@@ -277,10 +277,6 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   // lane: key l%16 and block l/16 of each group of 16 keys, which lie in one page
   const bool has = g < NB;
   const unsigned c_at = row * (DP / 2) + (has ? g * 16 : 0), s_at = row * NB + (has ? g : 0);
-  bool holes = false;            // whether a page of the range is not in the cache
-  for (int i = (w0 * TILE >> c.page_shift) + lane; i < a.table_stride && i <= (min(w1 * TILE, len) - 1) >> c.page_shift; i += 64)
-    holes = holes || (unsigned)table[i] >= (unsigned)c.num_pages;
-  holes = __any(holes);
   v4i kc[4], vc[4];
   uint32_t ks[4], vs[4];
   int page[4];
@@ -315,30 +311,70 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
       }
     }
   };
+  // The start is a chain of dependent loads, so each link asks for all it can: what
+  // depends on the sequence's bounds alone (pages, positions, query rows), then the table
+  // rows and the first tile, which arrives while the queries are turned.
   pages(w0);
-  fetch(w0);
-  pages(w0 + 1);
-
+  const int hole0 = (w0 * TILE) >> c.page_shift, hole1 = min(((min(w1 * TILE, len) - 1) >> c.page_shift) + 1, a.table_stride);
+  const int probe = hole0 + lane < hole1 ? table[hole0 + lane] : 0;
   // q': eight elements a thread, through LDS to the B operand (row l%16, block l/16)
   float* qs = reinterpret_cast<float*>(smem);
   constexpr int QROW = DP + 4;
   static_assert(16 * QROW * 4 <= NW * PER_WAVE, "q' fits the staging");
+  const int qr = threadIdx.x / (4 * NB), e0 = threadIdx.x % (4 * NB) * 8;
+  const int ti = (r0 + qr) / a.group, th = hk * a.group + (r0 + qr) % a.group;
+  const bool turns = e0 < a.rope.rope_dim, mine = (int)threadIdx.x < 64 * NB && ti < n && e0 < c.head_dim;
+  const int rhalf = a.rope.rope_dim >> 1;
+  const bool second = !a.rope.interleaved && e0 >= rhalf;
+  const int pair0 = a.rope.interleaved ? e0 >> 1 : second ? e0 - rhalf : e0;
+  uint4 own = make_uint4(0, 0, 0, 0), other = own;
+  int pos = 0;
+  if (mine) {
+    const uint16_t* qp = a.q + (long long)(q0 + ti) * a.q_stride + (long long)th * c.head_dim;
+    if (turns) {
+      pos = a.positions[q0 + ti];
+      if (!a.rope.interleaved) other = *reinterpret_cast<const uint4*>(qp + (second ? e0 - rhalf : e0 + rhalf));
+    }
+    own = *reinterpret_cast<const uint4*>(qp + e0);
+  }
+  const bool pos_ok = pos >= 0 && pos < a.rope.num_positions;
+  float4 cs[4] = {};             // cos, sin: four pairs, or eight
+  if (mine && turns && pos_ok) {
+    const size_t at = (size_t)pos * rhalf + pair0;
+    cs[0] = *reinterpret_cast<const float4*>(a.rope.cos + at);
+    cs[2] = *reinterpret_cast<const float4*>(a.rope.sin + at);
+    if (!a.rope.interleaved) {
+      cs[1] = *reinterpret_cast<const float4*>(a.rope.cos + at + 4);
+      cs[3] = *reinterpret_cast<const float4*>(a.rope.sin + at + 4);
+    }
+  }
+  fetch(w0);
+  pages(w0 + 1);
+  bool holes = (unsigned)probe >= (unsigned)c.num_pages && hole0 + lane < hole1;
+  for (int i = hole0 + 64 + lane; i < hole1; i += 64) holes = holes || (unsigned)table[i] >= (unsigned)c.num_pages;
+  holes = __any(holes);          // whether a page of the wave's keys is not in the cache
   if ((int)threadIdx.x < 64 * NB) {
-    const int qr = threadIdx.x / (4 * NB), e0 = threadIdx.x % (4 * NB) * 8;
-    const int i = (r0 + qr) / a.group, h = hk * a.group + (r0 + qr) % a.group;
-    float x[8] = {};
-    if (i < n && e0 < c.head_dim) {
-      RopeArgs rope = a.rope;
-      int pos = 0;
-      if (rope.rope_dim > 0) {
-        pos = a.positions[q0 + i];
-        if (pos < 0 || pos >= rope.num_positions) rope.rope_dim = -1;
-      }
-      if (rope.rope_dim < 0) {                 // no such table row: not a number
+    float x[8] = {bf_lo(own.x), bf_hi(own.x), bf_lo(own.y), bf_hi(own.y),
+                  bf_lo(own.z), bf_hi(own.z), bf_lo(own.w), bf_hi(own.w)};
+    if (mine && turns) {
+      if (!pos_ok) {             // no such table row: not a number
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = __builtin_nanf("");
+      } else if (a.rope.interleaved) {
+        turn(x[0], x[1], cs[0].x, cs[2].x);
+        turn(x[2], x[3], cs[0].y, cs[2].y);
+        turn(x[4], x[5], cs[0].z, cs[2].z);
+        turn(x[6], x[7], cs[0].w, cs[2].w);
       } else {
-        load8_turned(a.q + (long long)(q0 + i) * a.q_stride + (long long)h * c.head_dim, e0, rope, pos, x);
+        const float y[8] = {bf_lo(other.x), bf_hi(other.x), bf_lo(other.y), bf_hi(other.y),
+                            bf_lo(other.z), bf_hi(other.z), bf_lo(other.w), bf_hi(other.w)};
+        const float cc[8] = {cs[0].x, cs[0].y, cs[0].z, cs[0].w, cs[1].x, cs[1].y, cs[1].z, cs[1].w};
+        const float ss[8] = {cs[2].x, cs[2].y, cs[2].z, cs[2].w, cs[3].x, cs[3].y, cs[3].z, cs[3].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float u = x[e] * cc[e], w = y[e] * ss[e];
+          x[e] = second ? u + w : u - w;
+        }
       }
     }
     if (c.had) fwht32_lanes(x, lane);
@@ -1085,8 +1121,12 @@ int kv_attention_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_
   const long long base = (long long)seqs * kv_heads * row_tiles;
   const long long tiles = ((long long)max_kv + TILE - 1) / TILE;
   if (few) {
-    long long want = (4ll * NUM_CUS + base - 1) / base;
-    const long long most = (tiles + 3) / 4;   // a range of at least four tiles
+    // Two workgroups a CU, of at least four tiles (one a wave) each: a workgroup spends
+    // about 8 us on its start and end, so more of them cost more than they balance (one
+    // row of 131072 keys: 64 splits 44 us, 96 45, 128 52; 64 rows of up to 8192 keys:
+    // 98 us unsplit, 105 in halves, 94 in thirds).
+    long long want = (2ll * NUM_CUS + base - 1) / base;
+    const long long most = (tiles + 3) / 4;
     want = want < most ? want : most;
     if (want > kMaxSplits) want = kMaxSplits;
     return want < 1 ? 1 : (int)want;
