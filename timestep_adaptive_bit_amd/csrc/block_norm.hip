@@ -116,21 +116,6 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                     pack_bf16(v[6], v[7]));
 }
 
-__device__ __forceinline__ void unpack8(uint4 a, float (&v)[8]) {
-  v[0] = bf_lo(a.x); v[1] = bf_hi(a.x); v[2] = bf_lo(a.y); v[3] = bf_hi(a.y);
-  v[4] = bf_lo(a.z); v[5] = bf_hi(a.z); v[6] = bf_lo(a.w); v[7] = bf_hi(a.w);
-}
-
-// One cross-lane butterfly of the transform: partner + (+-v), the sign bit of v turned in
-// the lane that keeps the difference (the same rounding as first - second).
-template <int MASK>
-__device__ __forceinline__ void butterfly(float (&v)[8], int lane) {
-  const uint32_t turn = (lane & MASK) ? 0x80000000u : 0u;
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    v[e] = lane_xor<MASK>(v[e]) + __uint_as_float(__float_as_uint(v[e]) ^ turn);
-}
-
 // INT8 codes of four values: v * r is at most 127 (1 + 2^-24) for the row's largest, so
 // adding 1.5 * 2^23 rounds it to the nearest even whole number in the low byte.
 __device__ __forceinline__ uint32_t i8x4(float a, float b, float c, float d, float r) {
@@ -286,11 +271,9 @@ block_norm_kernel(BlockNormArgs a, int rows_per) {
     if (a.had > 0) {
 #pragma unroll
       for (int i = 0; i < S; ++i) {
-        fwht8(x[i]);
-        butterfly<1>(x[i], lane);
-        butterfly<2>(x[i], lane);
-        if (a.had >= 64) butterfly<4>(x[i], lane);
-        if (a.had >= 128) butterfly<8>(x[i], lane);
+        fwht32_lanes(x[i], lane);
+        if (a.had >= 64) fwht_cross8<4>(x[i], lane);
+        if (a.had >= 128) fwht_cross8<8>(x[i], lane);
       }
     }
     if (a.fmt == TABIT_FMT_INT8) {

@@ -23,11 +23,9 @@ using namespace kv;
 
 constexpr int NT = 256;
 
-// Codes and scale byte of one lane's eight elements of a block (four lanes).
-__device__ __forceinline__ void mx_encode(float (&v)[8], uint32_t& codes, uint32_t& scale) {
-  float m = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+// Codes and scale byte of one lane's eight elements of a block (four lanes); m is the
+// largest magnitude of the lane's.
+__device__ __forceinline__ void mx_encode(float (&v)[8], float m, uint32_t& codes, uint32_t& scale) {
   m = fmaxf(m, lane_xor<1>(m));
   m = fmaxf(m, lane_xor<2>(m));
   const int X = mx_exponent(m);
@@ -38,48 +36,81 @@ __device__ __forceinline__ void mx_encode(float (&v)[8], uint32_t& codes, uint32
   scale = (uint32_t)(X + 127);
 }
 
+// The (token, head) of this group of GL lanes: a workgroup has a tile of `hb` = 1, 2 or
+// 4 heads, which divide the head count, times as many tokens as fit, so that it reads
+// runs of hb vectors and a head's rows of consecutive slots are one run of one
+// workgroup's: spread over workgroups of different dies, 32 bytes each, a line of codes
+// went through four L2s.
+struct Place {
+  int t, h;
+};
+template <int GL>
+__device__ __forceinline__ Place place(int heads, int hb_shift) {
+  const unsigned tiles = (unsigned)heads >> hb_shift;         // head tiles, the fastest index
+  const unsigned tt = blockIdx.x / tiles, th = blockIdx.x - tt * tiles;
+  const int g = threadIdx.x / GL;
+  return {(int)(tt * ((NT / GL) >> hb_shift)) + (g >> hb_shift),
+          (int)(th << hb_shift) + (g & ((1 << hb_shift) - 1))};
+}
+
+// 0 when a is finite everywhere, NaN or infinity otherwise: infinities stand out in the
+// largest magnitude m, NaN in a sum (which may also overflow, and then is infinite).
+__device__ __forceinline__ bool any_bad(const float (&v)[8], float m) {
+  float s = v[0];
+#pragma unroll
+  for (int e = 1; e < 8; ++e) s += v[e];
+  return s != s || !finite_f32(m);
+}
+
 template <int GL>
 __global__ void __launch_bounds__(NT)
-kv_append_kernel(KvCacheArgs c, const uint16_t* __restrict__ k, long long k_stride,
+kv_append_kernel(KvCacheArgs c, int hb_shift, const uint16_t* __restrict__ k, long long k_stride,
                  const uint16_t* __restrict__ v, long long v_stride, int tokens,
                  const int64_t* __restrict__ slots, RopeArgs rope,
                  const int* __restrict__ positions) {
   const int lane = threadIdx.x & 63;
   const int gl = threadIdx.x % GL;
-  const long long pair = (long long)blockIdx.x * (NT / GL) + threadIdx.x / GL;
-  const int t = (int)(pair / c.heads), h = (int)(pair % c.heads);
+  const auto [t, h] = place<GL>(c.heads, hb_shift);
   if (t >= tokens) return;                       // whole groups leave together
-  const int64_t slot = slots[t];
-  if (slot < 0 || slot >= (long long)c.num_pages << c.page_shift) return;
   const int e0 = gl * 8;
   const int blocks = c.dim_pad / 32;
-  bool bad = false;
-  float a[8] = {}, b[8] = {};
+  // everything but the tables' rows is asked for at once
+  const int64_t slot = slots[t];
+  int pos = rope.rope_dim > 0 ? positions[t] : 0;
+  uint4 kw = make_uint4(0, 0, 0, 0), ko = kw, vw = kw;
   if (e0 < c.head_dim) {
-    int pos = 0;
-    RopeArgs r = rope;
-    if (r.rope_dim > 0) {
-      pos = positions[t];
-      if (pos < 0 || pos >= r.num_positions) {   // no such table row: stored as not a number
-        bad = true;
-        r.rope_dim = 0;
-      }
-    }
-    load8_turned(k + t * k_stride + (long long)h * c.head_dim, e0, r, pos, a);
-    load8(v + t * v_stride + (long long)h * c.head_dim + e0, b);
+    const uint16_t* kp = k + t * k_stride + (long long)h * c.head_dim;
+    kw = *reinterpret_cast<const uint4*>(kp + e0);
+    if (!rope.interleaved && e0 < rope.rope_dim)
+      ko = *reinterpret_cast<const uint4*>(kp + turn_partner(e0, rope));
+    vw = *reinterpret_cast<const uint4*>(v + t * v_stride + (long long)h * c.head_dim + e0);
   }
+  if (slot < 0 || slot >= (long long)c.num_pages << c.page_shift) return;
+  bool bad = false;
+  if (rope.rope_dim > 0 && (pos < 0 || pos >= rope.num_positions)) {
+    bad = true;                                  // no such table row: stored as not a number
+    pos = 0;
+  }
+  float a[8], b[8];
+  turned8(kw, ko, e0, rope, pos, a);
+  unpack8(vw, b);
   if (c.had) {
     fwht32_lanes(a, lane);
     fwht32_lanes(b, lane);
   }
+  float ma = 0.0f, mb = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) bad = bad || !finite_f32(a[e]) || !finite_f32(b[e]);
+  for (int e = 0; e < 8; ++e) {
+    ma = fmaxf(ma, fabsf(a[e]));
+    mb = fmaxf(mb, fabsf(b[e]));
+  }
+  bad = bad || any_bad(a, ma) || any_bad(b, mb);
   // one bad element in the head's key or value marks the whole token
   const unsigned long long group = ((1ull << GL) - 1) << (lane / GL * GL);
   bad = (__ballot(bad) & group) != 0;
   uint32_t kc, ks, vc, vs;
-  mx_encode(a, kc, ks);
-  mx_encode(b, vc, vs);
+  mx_encode(a, ma, kc, ks);
+  mx_encode(b, mb, vc, vs);
   if (bad) {   // a query that sees the token answers NaN, others never touch it
     kc = vc = 0u;
     ks = 255u;
@@ -118,12 +149,11 @@ __device__ __forceinline__ void write8(uint16_t* p, const float (&v)[8]) {
 
 template <int GL>
 __global__ void __launch_bounds__(NT)
-kv_read_kernel(KvCacheArgs c, const int64_t* __restrict__ slots, int tokens,
+kv_read_kernel(KvCacheArgs c, int hb_shift, const int64_t* __restrict__ slots, int tokens,
                uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
   const int lane = threadIdx.x & 63;
   const int gl = threadIdx.x % GL;
-  const long long pair = (long long)blockIdx.x * (NT / GL) + threadIdx.x / GL;
-  const int t = (int)(pair / c.heads), h = (int)(pair % c.heads);
+  const auto [t, h] = place<GL>(c.heads, hb_shift);
   if (t >= tokens) return;
   const int64_t slot = slots[t];
   const int e0 = gl * 8;
@@ -147,9 +177,25 @@ kv_read_kernel(KvCacheArgs c, const int64_t* __restrict__ slots, int tokens,
     }
   }
   if (e0 >= c.head_dim) return;
-  const long long o = pair * c.head_dim + e0;
+  const long long o = ((long long)t * c.heads + h) * c.head_dim + e0;
   write8(k + o, a);
   write8(v + o, b);
+}
+
+// Tokens go in pieces, so that a launch has fewer than 2^24 workgroups (2^32 threads are
+// the limit).
+template <typename Launch>
+hipError_t in_pieces(const KvCacheArgs& c, int tokens, Launch launch) {
+  const int gl = c.dim_pad <= 64 ? 8 : 16;
+  const int hb_shift = c.heads % 4 == 0 ? 2 : c.heads % 2 == 0 ? 1 : 0;
+  const int per = (NT / gl) >> hb_shift, tiles = c.heads >> hb_shift;
+  const int piece = max(1, (1 << 23) / tiles) * per;
+  for (int first = 0; first < tokens; first += piece) {
+    const int n = min(piece, tokens - first);
+    launch(gl, hb_shift, (unsigned)((n + per - 1) / per * tiles), first, n);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
@@ -158,24 +204,21 @@ hipError_t launch_kv_append(const KvCacheArgs& c, const uint16_t* k, long long k
                             const uint16_t* v, long long v_stride, int tokens,
                             const int64_t* slots, const RopeArgs& rope, const int* positions,
                             hipStream_t s) {
-  const int gl = c.dim_pad <= 64 ? 8 : 16;
-  const long long pairs = (long long)tokens * c.heads;
-  const unsigned grid = (unsigned)((pairs + NT / gl - 1) / (NT / gl));
-  if (gl == 8)
-    kv_append_kernel<8><<<grid, NT, 0, s>>>(c, k, k_stride, v, v_stride, tokens, slots, rope, positions);
-  else
-    kv_append_kernel<16><<<grid, NT, 0, s>>>(c, k, k_stride, v, v_stride, tokens, slots, rope, positions);
-  return hipGetLastError();
+  return in_pieces(c, tokens, [&](int gl, int hb_shift, unsigned grid, int first, int n) {
+    auto* kernel = gl == 8 ? &kv_append_kernel<8> : &kv_append_kernel<16>;
+    kernel<<<grid, NT, 0, s>>>(c, hb_shift, k + first * k_stride, k_stride, v + first * v_stride,
+                               v_stride, n, slots + first, rope,
+                               positions == nullptr ? nullptr : positions + first);
+  });
 }
 
 hipError_t launch_kv_read(const KvCacheArgs& c, const int64_t* slots, int tokens, uint16_t* k,
                           uint16_t* v, hipStream_t s) {
-  const int gl = c.dim_pad <= 64 ? 8 : 16;
-  const long long pairs = (long long)tokens * c.heads;
-  const unsigned grid = (unsigned)((pairs + NT / gl - 1) / (NT / gl));
-  if (gl == 8) kv_read_kernel<8><<<grid, NT, 0, s>>>(c, slots, tokens, k, v);
-  else kv_read_kernel<16><<<grid, NT, 0, s>>>(c, slots, tokens, k, v);
-  return hipGetLastError();
+  return in_pieces(c, tokens, [&](int gl, int hb_shift, unsigned grid, int first, int n) {
+    const long long o = (long long)first * c.heads * c.head_dim;
+    auto* kernel = gl == 8 ? &kv_read_kernel<8> : &kv_read_kernel<16>;
+    kernel<<<grid, NT, 0, s>>>(c, hb_shift, slots + first, n, k + o, v + o);
+  });
 }
 
 }  // namespace tabit

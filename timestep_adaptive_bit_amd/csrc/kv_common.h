@@ -27,10 +27,13 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack8(uint4 a, float (&v)[8]) {
   v[0] = bf_lo(a.x); v[1] = bf_hi(a.x); v[2] = bf_lo(a.y); v[3] = bf_hi(a.y);
   v[4] = bf_lo(a.z); v[5] = bf_hi(a.z); v[6] = bf_lo(a.w); v[7] = bf_hi(a.w);
+}
+
+__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
+  unpack8(*reinterpret_cast<const uint4*>(p), v);
 }
 
 __device__ __forceinline__ bool finite_f32(float f) {
@@ -71,15 +74,14 @@ __device__ __forceinline__ void fwht8(float (&v)[8]) {
 }
 
 // One cross-lane butterfly: the lane with MASK clear keeps first + second, its
-// partner first - second.
+// partner first - second, as partner + (+-own): the sign bit is turned in the lanes
+// that subtract, which rounds alike.
 template <int MASK>
 __device__ __forceinline__ void fwht_cross8(float (&v)[8], int lane) {
-  const bool second = (lane & MASK) != 0;
+  const uint32_t sign = (lane & MASK) ? 0x80000000u : 0u;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float o = lane_xor<MASK>(v[e]);
-    v[e] = second ? (o - v[e]) : (v[e] + o);
-  }
+  for (int e = 0; e < 8; ++e)
+    v[e] = lane_xor<MASK>(v[e]) + __uint_as_float(__float_as_uint(v[e]) ^ sign);
 }
 
 // Block-32 transform over four consecutive lanes of eight elements each
@@ -136,13 +138,19 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   b = y;
 }
 
-// Eight elements [e0, e0 + 8) of a head vector of `dim` elements at p, rotated to
-// position row `pos` of the tables.  rope_dim is a multiple of 16, so in either
-// pairing the eight lie on one side of the rotated region and their partners are
-// eight consecutive elements (or the same eight).
-__device__ __forceinline__ void load8_turned(const uint16_t* p, int e0, const RopeArgs& rope, int pos,
-                                             float (&v)[8]) {
-  load8(p + e0, v);
+// Elements [e0, e0 + 8) of a head vector, rotated to position row `pos` of the tables.
+// rope_dim is a multiple of 16, so in either pairing the eight lie on one side of the
+// rotated region and their partners are the eight consecutive elements from
+// turn_partner(e0) on (the same eight where pairs are neighbours).
+__device__ __forceinline__ int turn_partner(int e0, const RopeArgs& rope) {
+  const int half = rope.rope_dim >> 1;
+  if (rope.interleaved || e0 >= rope.rope_dim) return e0;
+  return e0 >= half ? e0 - half : e0 + half;
+}
+
+__device__ __forceinline__ void turned8(uint4 own, uint4 partner, int e0, const RopeArgs& rope, int pos,
+                                        float (&v)[8]) {
+  unpack8(own, v);
   if (e0 >= rope.rope_dim) return;
   const int half = rope.rope_dim >> 1;
   const size_t row = (size_t)pos * half;
@@ -157,17 +165,26 @@ __device__ __forceinline__ void load8_turned(const uint16_t* p, int e0, const Ro
   }
   const bool second = e0 >= half;
   const int i0 = second ? e0 - half : e0;
-  float o[8];
-  load8(p + (second ? i0 : i0 + half), o);
   const float4 c0 = *reinterpret_cast<const float4*>(rope.cos + row + i0);
   const float4 c1 = *reinterpret_cast<const float4*>(rope.cos + row + i0 + 4);
   const float4 s0 = *reinterpret_cast<const float4*>(rope.sin + row + i0);
   const float4 s1 = *reinterpret_cast<const float4*>(rope.sin + row + i0 + 4);
   const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
   const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+  // the first of a pair takes -o s: the partner's sign bits are turned
+  const uint32_t sign = second ? 0u : 0x80008000u;
+  float o[8];
+  unpack8(make_uint4(partner.x ^ sign, partner.y ^ sign, partner.z ^ sign, partner.w ^ sign), o);
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    v[e] = second ? v[e] * c[e] + o[e] * s[e] : v[e] * c[e] - o[e] * s[e];
+  for (int e = 0; e < 8; ++e) v[e] = v[e] * c[e] + o[e] * s[e];
+}
+
+// The same with the elements read at p, a vector of the head.
+__device__ __forceinline__ void load8_turned(const uint16_t* p, int e0, const RopeArgs& rope, int pos,
+                                             float (&v)[8]) {
+  const uint4 own = *reinterpret_cast<const uint4*>(p + e0);
+  const uint4 partner = *reinterpret_cast<const uint4*>(p + turn_partner(e0, rope));
+  turned8(own, partner, e0, rope, pos, v);
 }
 
 }  // namespace kv
