@@ -188,7 +188,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # the handle itself: building a Stream object to ask for it takes longer than a small launch
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _dev(t: torch.Tensor, dtype, name: str, shape=None) -> None:
@@ -222,6 +223,9 @@ def _rows(t: torch.Tensor, name: str, tail, device) -> int:
 
 
 def _on(t: torch.Tensor, dtype, name: str, shape, device) -> None:
+    if (isinstance(t, torch.Tensor) and t.device == device and t.dtype == dtype and t.shape == shape
+            and t.is_contiguous()):
+        return
     _dev(t, dtype, name, shape)
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
@@ -857,17 +861,17 @@ class Context:
         if x_out is not None:
             _on(x_out, torch.bfloat16, "x_out", (M, H), dev)
         elif want_x:
-            x_out = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
+            x_out = torch.empty_like(x)
         h = hs = None
         if want_h:
             if fmt == FMT_INT8:
-                h = torch.empty((M, H), dtype=torch.int8, device=dev)
+                h = torch.empty_like(x, dtype=torch.int8)
                 hs = torch.empty((M,), dtype=torch.float32, device=dev)
             elif fmt == FMT_MXFP4:
                 h = torch.empty((M, H // 2), dtype=torch.uint8, device=dev)
                 hs = torch.empty((M, H // 32), dtype=torch.uint8, device=dev)
             else:
-                h = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
+                h = torch.empty_like(x)
         if M == 0:
             return x_out, h, hs
         a = _BlockNormArgs(x.data_ptr(), _ptr(y), M, H, post, pre, _ptr(post_weight), _ptr(pre_weight),

@@ -13,7 +13,13 @@
 // 32 is four lanes, so the transform's last two stages and the block maximum are
 // DPP moves inside a quad.  Every rotation, butterfly and scaling is one rounded
 // fp32 operation in a fixed order, so the stored codes are a function of the
-// inputs alone.  The kernel moves each byte once and is bound by memory.
+// inputs alone.
+//
+// Each byte moves once.  Measured at 17776 tokens x 30 heads x 64, rotated in neighbour
+// pairs, had_block 32: append 52 us (3.4 TB/s; 26 us for its loads alone, and the table
+// rows, the transform and the stores add 6 to 9 us each: the vector units are 75% busy
+// and the memory system is not full), read 34 us (5.0 TB/s, what a large copy reaches).
+// Two heads a lane sharing a table row took 50 us, in four more kernels; not kept.
 #include "kv_common.h"
 
 namespace tabit {
@@ -53,7 +59,14 @@ __device__ __forceinline__ Place place(int heads, int hb_shift) {
           (int)(th << hb_shift) + (g & ((1 << hb_shift) - 1))};
 }
 
-// 0 when a is finite everywhere, NaN or infinity otherwise: infinities stand out in the
+// Byte offset of a valid slot's scales; its codes are at 16 times that.
+__device__ __forceinline__ uint64_t scale_at(const KvCacheArgs& c, int64_t slot, int h) {
+  const uint32_t page = (uint32_t)(slot >> c.page_shift), in = (uint32_t)slot & ((1u << c.page_shift) - 1);
+  const uint64_t row = (((uint64_t)page * (uint32_t)c.heads + (uint32_t)h) << c.page_shift) | in;
+  return row * (uint32_t)(c.dim_pad >> 5);
+}
+
+// Whether any of v is NaN or infinite: infinities stand out in the
 // largest magnitude m, NaN in a sum (which may also overflow, and then is infinite).
 __device__ __forceinline__ bool any_bad(const float (&v)[8], float m) {
   float s = v[0];
@@ -73,7 +86,6 @@ kv_append_kernel(KvCacheArgs c, int hb_shift, const uint16_t* __restrict__ k, lo
   const auto [t, h] = place<GL>(c.heads, hb_shift);
   if (t >= tokens) return;                       // whole groups leave together
   const int e0 = gl * 8;
-  const int blocks = c.dim_pad / 32;
   // everything but the tables' rows is asked for at once
   const int64_t slot = slots[t];
   int pos = rope.rope_dim > 0 ? positions[t] : 0;
@@ -117,13 +129,12 @@ kv_append_kernel(KvCacheArgs c, int hb_shift, const uint16_t* __restrict__ k, lo
     vs = 127u;
   }
   if (e0 >= c.dim_pad) return;
-  const long long page = slot >> c.page_shift;
-  const long long row = ((page * c.heads + h) << c.page_shift) + (slot & ((1 << c.page_shift) - 1));
-  reinterpret_cast<uint32_t*>(c.k_codes)[row * (c.dim_pad / 8) + gl] = kc;
-  reinterpret_cast<uint32_t*>(c.v_codes)[row * (c.dim_pad / 8) + gl] = vc;
+  const uint64_t at = scale_at(c, slot, h);
+  *reinterpret_cast<uint32_t*>(c.k_codes + at * 16 + gl * 4) = kc;
+  *reinterpret_cast<uint32_t*>(c.v_codes + at * 16 + gl * 4) = vc;
   if ((gl & 3) == 0) {
-    c.k_scales[row * blocks + (gl >> 2)] = (uint8_t)ks;
-    c.v_scales[row * blocks + (gl >> 2)] = (uint8_t)vs;
+    c.k_scales[at + (gl >> 2)] = (uint8_t)ks;
+    c.v_scales[at + (gl >> 2)] = (uint8_t)vs;
   }
 }
 
@@ -159,13 +170,9 @@ kv_read_kernel(KvCacheArgs c, int hb_shift, const int64_t* __restrict__ slots, i
   const int e0 = gl * 8;
   float a[8] = {}, b[8] = {};
   if (slot >= 0 && slot < (long long)c.num_pages << c.page_shift && e0 < c.dim_pad) {
-    const long long page = slot >> c.page_shift;
-    const long long row = ((page * c.heads + h) << c.page_shift) + (slot & ((1 << c.page_shift) - 1));
-    const int blocks = c.dim_pad / 32;
-    mx_decode(reinterpret_cast<const uint32_t*>(c.k_codes)[row * (c.dim_pad / 8) + gl],
-              c.k_scales[row * blocks + (gl >> 2)], a);
-    mx_decode(reinterpret_cast<const uint32_t*>(c.v_codes)[row * (c.dim_pad / 8) + gl],
-              c.v_scales[row * blocks + (gl >> 2)], b);
+    const uint64_t at = scale_at(c, slot, h);
+    mx_decode(*reinterpret_cast<const uint32_t*>(c.k_codes + at * 16 + gl * 4), c.k_scales[at + (gl >> 2)], a);
+    mx_decode(*reinterpret_cast<const uint32_t*>(c.v_codes + at * 16 + gl * 4), c.v_scales[at + (gl >> 2)], b);
   }
   if (c.had) {
     fwht32_lanes(a, lane);

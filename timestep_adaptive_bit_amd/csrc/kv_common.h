@@ -48,12 +48,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 // Value of the lane whose index differs in bit MASK (1, 2: inside a quad by DPP;
-// 4, 8, 16: ds_swizzle inside 32 lanes).
+// 4, 8, 16: ds_swizzle inside 32 lanes).  With the bound bit set the compiler folds the
+// move into the instruction that uses it.
 template <int MASK>
 __device__ __forceinline__ float lane_xor(float v) {
   int i = __float_as_int(v);
-  if constexpr (MASK == 1) i = __builtin_amdgcn_mov_dpp(i, 0xB1, 0xF, 0xF, false);
-  else if constexpr (MASK == 2) i = __builtin_amdgcn_mov_dpp(i, 0x4E, 0xF, 0xF, false);
+  if constexpr (MASK == 1) i = __builtin_amdgcn_update_dpp(0, i, 0xB1, 0xF, 0xF, true);
+  else if constexpr (MASK == 2) i = __builtin_amdgcn_update_dpp(0, i, 0x4E, 0xF, 0xF, true);
   else i = __builtin_amdgcn_ds_swizzle(i, (MASK << 10) | 0x1F);
   return __int_as_float(i);
 }
