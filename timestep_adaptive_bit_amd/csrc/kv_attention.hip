@@ -59,12 +59,6 @@ __device__ __forceinline__ int v_off(int key, int c, int half) {
   return key * RS + ((c ^ x) << 5) + ((half ^ ((key >> 3) & 1)) << 4);
 }
 
-// Keys and MX blocks of the units that consecutive lanes bring in: 16 keys, block by block.
-template <int NB>
-__device__ __forceinline__ int unit_key(int unit) { return unit / (16 * NB) * 16 + unit % 16; }
-template <int NB>
-__device__ __forceinline__ int unit_block(int unit) { return unit % (16 * NB) / 16; }
-
 // Factor of the products q'.k' that gives scores in base 2.
 __device__ __forceinline__ float base2_scale(const KvAttnArgs& a) {
   return a.scale * 1.4426950408889634f / (a.cache.had ? 32.0f : 1.0f);
@@ -122,6 +116,8 @@ __device__ __forceinline__ bool load_q_block(const KvAttnArgs& a, int token, int
         const bool second = e0 >= half;
         const int at = e0 < R ? (second ? e0 - half : e0) : 0;
         other[i] = *reinterpret_cast<const uint4*>(p + (e0 < R ? (second ? e0 - half : e0 + half) : 0));
+        const uint32_t sign = second ? 0u : 0x80008000u;   // the first of a pair takes -other sin
+        other[i] = make_uint4(other[i].x ^ sign, other[i].y ^ sign, other[i].z ^ sign, other[i].w ^ sign);
         c[2 * i] = *reinterpret_cast<const float4*>(cos + at);
         c[2 * i + 1] = *reinterpret_cast<const float4*>(cos + at + 4);
         s[2 * i] = *reinterpret_cast<const float4*>(sin + at);
@@ -140,7 +136,7 @@ __device__ __forceinline__ bool load_q_block(const KvAttnArgs& a, int token, int
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float u = x[8 * i + e] * cc[e], w = y[e] * ss[e];
-          x[8 * i + e] = e0 >= R ? x[8 * i + e] : e0 >= half ? u + w : u - w;
+          x[8 * i + e] = e0 >= R ? x[8 * i + e] : u + w;
         }
       }
     }
@@ -156,19 +152,23 @@ __device__ __forceinline__ bool load_q_block(const KvAttnArgs& a, int token, int
     }
   if (a.cache.had) fwht32_lane(x);
 #pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    x[e] *= factor;
-    ok = ok && finite_f32(x[e]);
-  }
+  for (int e = 0; e < 32; ++e) x[e] *= factor;
   return ok;
 }
 
 // Three FP6 terms of a block of 32 with their E8M0 bytes (bytes 0..2 of `scales`).
-// A block that is not finite gets scale 255: its row answers NaN.
+// A block that is not `ok` or not finite gets scale 255 (not a number) for whatever its
+// codes are: its row answers NaN.  An infinity shows in the largest magnitude, NaN in
+// the sum (an overflow of the sum itself is an infinity and counts for nothing).
 __device__ __forceinline__ void q_terms(float (&x)[32], bool ok, v8i (&q)[3], uint32_t& scales) {
-  float top = 0.0f;
+  float top = 0.0f, even = 0.0f, odd = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(x[e]));
+  for (int e = 0; e < 32; e += 2) {
+    top = fmaxf(top, fmaxf(fabsf(x[e]), fabsf(x[e + 1])));
+    even += x[e];
+    odd += x[e + 1];
+  }
+  ok = ok && finite_f32(top) && even == even && odd == odd;
   const int ex = max(mx_exponent(top), -119);
   scales = 0u;
 #pragma unroll
@@ -178,13 +178,15 @@ __device__ __forceinline__ void q_terms(float (&x)[32], bool ok, v8i (&q)[3], ui
     v16f lo, hi;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      lo[e] = ok ? x[2 * e] : 0.0f;
-      hi[e] = ok ? x[2 * e + 1] : 0.0f;
+      lo[e] = x[2 * e];
+      hi[e] = x[2 * e + 1];
     }
     const v6u w = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(lo, hi, s);
-    const v32f d = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(w, s);
+    if (t < 2) {
+      const v32f d = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(w, s);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) x[e] -= d[e];
+      for (int e = 0; e < 32; ++e) x[e] -= d[e];
+    }
     q[t] = v8i{(int)w[0], (int)w[1], (int)w[2], (int)w[3], (int)w[4], (int)w[5], 0, 0};
     scales |= (uint32_t)(ok ? E : 255) << (8 * t);
   }
@@ -391,17 +393,13 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   for (int t = 0; t < 3; ++t) q[t] = v8i{0, 0, 0, 0, 0, 0, 0, 0};
   if (has) {
     float x[32];
-    bool ok = true;
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
       const v4f y = *reinterpret_cast<const v4f*>(qs + row * QROW + g * 32 + e);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[e + k] = y[k];
-        ok = ok && finite_f32(y[k]);
-      }
+      for (int k = 0; k < 4; ++k) x[e + k] = y[k];
     }
-    q_terms(x, ok, q, q_scales);
+    q_terms(x, true, q, q_scales);
   }
   __syncthreads();
 
