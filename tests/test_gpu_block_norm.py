@@ -236,6 +236,39 @@ def test_in_place_empty_and_odd_rows(ctx):
         assert none is None and only.shape == (M, 320)
 
 
+@pytest.mark.parametrize("M,H,samples", [
+    (9000, 512, 3), (7000, 1024, 7), (5000, 1536, 5), (5000, 2048, 4), (1700, 4096, 17), (1100, 8192, 11),
+    (40, 16384, 2), (9, 32768, 3),
+])
+def test_a_row_does_not_depend_on_the_others(ctx, M, H, samples):
+    """Enough rows for runs that end inside a sample: each sample by itself gives the same bits."""
+    print("block_norm runs", M, H, samples, flush=True)
+    t = _inputs(M, H, samples, H)
+    x, y, m = t["x"].to(DEV), t["y"].to(DEV), t["mod"].to(DEV)
+    w, n = t["post_weight"].to(DEV), M // samples
+    use = dict(post=T.NORM_RMS, post_weight=w, pre=T.NORM_LAYER, fmt=T.FMT_INT8, had_block=32)
+    a, h, s = ctx.block_norm(x, y, gate=m[:, 0], scale=m[:, 1], shift=m[:, 2], **use)
+    for i in range(samples):
+        for r in (slice(i * n, i * n + n // 2), slice(i * n + n // 2, i * n + n)):
+            a1, h1, s1 = ctx.block_norm(x[r], y[r], gate=m[i:i + 1, 0], scale=m[i:i + 1, 1],
+                                        shift=m[i:i + 1, 2], **use)
+            assert torch.equal(a[r], a1) and torch.equal(h[r], h1) and torch.equal(s[r], s1), (i, r)
+
+
+@pytest.mark.parametrize("H", [64, 1536, 4096, 16384])
+def test_not_a_number_stays_in_its_row(ctx, H):
+    t = _inputs(12, H, 1, 3)
+    x, y = t["x"].to(DEV), t["y"].to(DEV)
+    use = dict(post=T.NORM_RMS, pre=T.NORM_LAYER)
+    a, h, _ = ctx.block_norm(x, y, **use)
+    x[5, 3], y[7, H - 1] = float("nan"), float("inf")
+    b, g, _ = ctx.block_norm(x, y, **use)
+    good = [i for i in range(12) if i not in (5, 7)]
+    assert torch.equal(a[good], b[good]) and torch.equal(h[good], g[good])
+    assert torch.isnan(g[5]).all() and torch.isnan(g[7]).all()
+    assert torch.isnan(b[5]).sum() == 1 and torch.isnan(b[7]).any()
+
+
 def test_binding_refusals(ctx):
     x = torch.zeros(6, 64, dtype=torch.bfloat16, device=DEV)
     m = torch.zeros(2, 64, dtype=torch.bfloat16, device=DEV)

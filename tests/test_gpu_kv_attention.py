@@ -184,6 +184,42 @@ def test_not_a_number_reaches_only_the_rows_that_see_it(ctx):
         assert np.array_equal(nan, want) and np.array_equal(some, want), (n, D)
 
 
+@pytest.mark.parametrize("n,hk,D", [(4, 1, 128), (8, 2, 64), (40, 2, 64), (150, 2, 96), (3, 1, 32), (64, 4, 128)])
+def test_value_scales_beyond_bf16(ctx, n, hk, D):
+    """A key whose value scale is NaN (255) or too large for bf16 (253, 254): rows that see it
+    answer NaN, rows that do not are as without it."""
+    for byte in (253, 255):
+        p = _problem(12, [n + 30], [n], 4, hk, D, 16, 32)
+        cache, q, cu, table, lens, kw = _on_gpu(p)
+        a = ctx.kv_attention(cache, q, cu, table, lens, n, n + 30, causal=True)
+        j = 30 + n // 2
+        cache.v_scales[int(p["table"][0, j // 16]), hk - 1, j % 16, D // 32 - 1] = byte
+        b = ctx.kv_attention(cache, q, cu, table, lens, n, n + 30, causal=True)
+        sees = torch.zeros((n, 4), dtype=torch.bool, device=DEV)
+        sees[n // 2:, 4 // hk * (hk - 1):] = True
+        assert torch.isnan(b[sees]).all() and torch.equal(a[~sees], b[~sees]), (byte, n, D)
+
+
+@pytest.mark.parametrize("n,hq,hk,D", [(4, 4, 1, 128), (16, 2, 2, 64), (17, 2, 2, 64), (2, 17, 1, 96),
+                                       (1, 16, 1, 40), (1, 17, 1, 40), (31, 8, 2, 72)])
+@pytest.mark.parametrize("keys", [5, 64, 700])
+def test_around_sixteen_rows_a_key_head(ctx, n, hq, hk, D, keys):
+    """Both sides of the change of kernel, with as few keys as queries and many."""
+    print("attention rows", n * hq // hk, "keys", keys, flush=True)
+    p = _problem(n + keys, [keys, 1], [n, 1], hq, hk, D, 16, 32, "half")
+    _check(_run(ctx, p, True, D ** -0.5), _want(p, True, D ** -0.5), keys)
+
+
+def test_reference_rises_late(ctx):
+    """Scores near nothing for the first tiles, then one of hundreds: what was summed so far has
+    to be scaled away, in the tile where the reference rises and in the join of the ranges."""
+    for n, D in ((1, 64), (3, 128), (70, 64), (130, 96)):
+        p = _problem(13, [900], [n], 2, 1, D, 16, 0)
+        for j, x in ((500, 127 + 6), (700, 127 + 8)):
+            p["arr"]["k_scales"][p["table"][0, j // 16], :, j % 16] = x
+        _check(_run(ctx, p, False, 0.5), _want(p, False, 0.5), 900)
+
+
 def test_same_bits_every_time_and_other_streams(ctx):
     for qs in ([1, 1], [100, 30]):
         p = _problem(10, [900, 400], qs, 8, 2, 128, 16, 32, "half")

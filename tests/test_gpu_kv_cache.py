@@ -107,6 +107,42 @@ def _block_sum(codes, e8):
     return np.broadcast_to(a, e8.shape + (32,)).reshape(codes.shape[:-1] + (-1,))
 
 
+@pytest.mark.parametrize("heads", [1, 2, 3, 4, 6, 8, 12])
+@pytest.mark.parametrize("D", [64, 96])
+def test_head_tiles(ctx, heads, D):
+    """Head counts of every kind of tile, tokens that end inside one; all ranges of exponents."""
+    rng = np.random.default_rng(heads * 100 + D)
+    tokens = 67
+    bits = rng.integers(0, 1 << 16, (tokens, 2, heads, D), dtype=np.uint16)
+    top = rng.integers(0, 255, (tokens, 2, heads, 1), dtype=np.uint16)      # a vector's exponents
+    ex = np.maximum(top.astype(np.int64) - rng.integers(0, 9, bits.shape), 0).astype(np.uint16)
+    ex = np.minimum(ex, 240)                                                # room for the sums of 32
+    bits = (bits & 0x807F) | (ex << 7)
+    t = torch.from_numpy(bits.view(np.int16)).view(torch.bfloat16)
+    f = O.bf16_to_f32(bits)
+    for had in (0, 32):
+        cache = _filled(6, 16, heads, D, had)
+        slots = rng.permutation(96)[:tokens].astype(np.int64)
+        want = _arrays(cache)
+        ctx.kv_append(cache, t[:, 0].contiguous().to(DEV), t[:, 1].contiguous().to(DEV),
+                      torch.from_numpy(slots).to(DEV))
+        kc, ks = B.mx_rows(f[:, 0], had)
+        vc, vs = B.mx_rows(f[:, 1], had)
+        for i in range(tokens):
+            _put(want, slots[i], 16, {"k_codes": kc[i], "k_scales": ks[i], "v_codes": vc[i], "v_scales": vs[i]})
+        got = _arrays(cache)
+        for n in want:
+            assert np.array_equal(got[n], want[n]), (n, had)
+        rk, rv = ctx.kv_read(cache, torch.from_numpy(slots).to(DEV))
+        for r, c, e in ((rk, kc, ks), (rv, vc, vs)):
+            val = B.unrotated(B.mx_values(c, e), had)[..., :D]
+            room = np.abs(val) * 2.0 ** -8
+            if had:
+                room = room + 5 * 2.0 ** -24 * _block_sum(c, e)[..., :D] / 32
+            r = r.float().cpu().numpy().astype(np.float64)
+            assert np.all(np.abs(r - val) <= room + 1e-38)
+
+
 def test_append_marks_what_is_not_finite(ctx):
     heads, D, ps = 2, 64, 16
     g = torch.Generator().manual_seed(3)

@@ -18,8 +18,12 @@
 //           2^(e-8) per block of 32: what is left of an element is below 2^-13 of
 //           the block's largest one, less than bf16 would lose, at 3/4 of the
 //           matrix time of one bf16 product.
-//   softmax every lane holds one row (l%16) and 16 of the 64 keys, in fp32, base 2,
-//           with a running maximum and sum.
+//   softmax every lane holds one row (l%16) and 16 of the 64 keys, in fp32, base 2.
+//           Weights are 2^(s - ref) and their sum runs beside the values'.  Any ref that
+//           neither over- nor underflows gives the same relative precision, so it is 0
+//           until a row's first visible tile has a largest score beyond +-40 or a tile's
+//           weights pass 2^40; then it is raised to the largest score, and what is
+//           summed so far is scaled by 2^(old - new).
 //   values  O^T += V^T P^T with the 16x16x32 bf16 MFMA.  The order of the summed
 //           keys is free, so it is chosen as the lanes already hold them: P needs
 //           no exchange, only its rounding to bf16 (2^-9 a weight: the sums stay in
@@ -232,8 +236,14 @@ __device__ __forceinline__ int seen_keys(const KvAttnArgs& a, int len, int n, in
 // sequence over one range of its keys; the range's tiles go to the waves in runs and
 // every wave works by itself until the end.  Bound by the cache's bytes: a wave asks
 // for the next tile's codes and scales (8.7 KB at 128 elements) as soon as this one's
-// are in LDS or in the matrix core, and four workgroups fit a CU (8.4 KB of LDS a
-// wave: values are staged 32 keys at a time).
+// are in LDS or in the matrix core; the values of 32 keys are staged at a time (8 KB of
+// LDS a wave), and registers allow three workgroups a CU.
+//
+// Measured at 32 heads over 8, 128 elements: 64 rows of up to 8192 keys 97 us (371 MB,
+// 3.8 TB/s; large copies reach 5.2, reads alone 6), one row of 131072 keys 44 us with
+// the join (143 MB, 3.3 TB/s), one row of 1000 keys 15 us.  A workgroup's start costs
+// 6 us (bounds, pages, then codes and tables: three loads that depend on each other),
+// which is what short caches take.
 template <int NB>
 __global__ void __launch_bounds__(256, 3)
 kv_attention_rows16_kernel(KvAttnArgs a) {
@@ -446,9 +456,9 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
     // weights: as in the kernel for 128 rows, 2^(s - ref) with a reference only where needed
     float sum;
     uint32_t p[8];
-    bool exact = any_fresh && __any(fresh && j0 < seen);
-    for (;;) {
-      if (exact) {
+    bool over = false;
+    for (int pass = 0; pass < 2; ++pass) {
+      if (pass == 1 || (any_fresh && __any(fresh && j0 < seen))) {
         float top = kNegInf;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -459,7 +469,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
         const bool first = fresh && top > kNegInf;
         fresh = fresh && !first;
         any_fresh = __any(fresh);
-        const bool up = first ? fabsf(top) > 40.0f : !fresh && top > ref;
+        const bool up = first ? fabsf(top) > 40.0f : over && top > ref;
         const float by = up ? top - ref : 0.0f;
         const float alpha = first ? 1.0f : exp2_fast(-by);
         ref += by;
@@ -476,8 +486,10 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
         p[2 * k] = pack_bf16(w0_, w1_);
         p[2 * k + 1] = pack_bf16(w2_, w3_);
       }
-      if (exact || !__any(!(sum < 0x1p40f))) break;
-      exact = true;
+      unsigned long long m = __ballot(!(sum < 0x1p40f));
+      if (m == 0) break;
+      m |= m >> 32;
+      over = ((m | m >> 16) >> row) & 1;             // in any of the row's four lanes
     }
     l += sum;
     // values, 32 keys at a time through the wave's own staging (LDS serves a wave in order)
@@ -600,19 +612,22 @@ __device__ __forceinline__ v16f score_term(v4i x, const v8i& q, v16f s, int byte
 
 // One workgroup: 32 NW rows of one key head of one sequence, 32 a wave, over one range
 // of its keys.  The 64 keys of a tile are brought in once for all rows: codes and
-// scales through registers (loaded a tile ahead, their pages two ahead) into one of
-// three LDS stages, the values already as bf16, one barrier a tile; the scores of a
-// tile are computed beside the weights of the one before.  A wave uses the
-// 32x32 forms of the same products: scores with 32x32x64 (lane l: one row, l%32, and
-// 32 of the 64 keys), values with 32x32x16, P staying in its lanes.
+// scales through registers (loaded a tile ahead, their pages two ahead) into one of two
+// LDS stages, the values already as bf16, one barrier a tile.  A wave uses the 32x32
+// forms of the same products: scores with 32x32x64 (lane l: one row, l%32, and 32 of
+// the 64 keys), values with 32x32x16, P staying in its lanes.
 //
-// The vector units, not the matrix cores, bound this kernel, so a tile costs them one
-// exponential a score, half a rounding to bf16 and half an addition: exp2(s - ref) has
-// the same relative precision for any reference that neither over- nor underflows, so
-// the maximum is taken for the first tile a row sees (`exact`), and again only for a
-// tile in which a sum of exponentials passes 2^40; the matrix core subtracts ref by
-// starting its sums at -ref; the sum of the weights is a dot product of the rounded
-// weights with ones, two an instruction.
+// Vector instructions and matrix products share a wave's issue and about balance, so a
+// tile costs the vector units one exponential a score, half a rounding to bf16 and one
+// addition; without a reference (see the top) the scores go to the exponential as they
+// leave the matrix core.
+//
+// Measured: 2700 rows x 17776 keys x 30 heads x 64 in 460 us (800 TFLOP/s counted as
+// 4 flops a key, row and element; a library bf16 product of 8192^3 reaches 1207), causal
+// turns of 32 heads over 8 at 128 elements in 495 us (650 TFLOP/s counting visible keys),
+// 2 x 4096 rows x 300 keys x 16 heads x 72 in 32 us.  The matrix cores are busy for half
+// of the cycles.  Level or slower: scores of a tile beside the weights of the one before,
+// eight waves a workgroup, 32 keys a step, three stages, heads as the fastest index.
 template <int NB>
 __global__ void __launch_bounds__(256, NB <= 2 ? 3 : 2)
 kv_attention_rows128_kernel(KvAttnArgs a) {
@@ -748,8 +763,7 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     else return key * (DP / 2) + (blk << 4);
   };
 
-  // scores come out of the matrix core relative to `ref` (the accumulators start at
-  // -ref); `fresh`: the row has seen no key yet
+  // weights are 2^(s - ref); `fresh`: the row has seen no key yet
   float ref = 0.0f, l = 0.0f;
   bool fresh = true;
   v16f o[ND];
@@ -810,11 +824,12 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
           sc[kb] = score_term(x[kb], q[ds][t], sc[kb], kb * 2 + ds, ksw, t, (int)q_scales[ds]);
     }
   };
-  // Raises the reference to the largest score where a row needs it; what is summed so far is
-  // to be scaled by alpha.
+  // Sets the reference of rows that see their first key, raises it to the largest score in
+  // rows that are `over`; what is summed so far is to be scaled by alpha (1 in the first
+  // pass over a tile, where only fresh rows move).
   float alpha = 1.0f;
   bool any_fresh = true, any_ref = false, any_alpha = false;     // over the wave
-  auto raise = [&](const v16f (&sc)[2]) {
+  auto raise = [&](const v16f (&sc)[2], bool over) {
     float top = kNegInf;
 #pragma unroll
     for (int r = 0; r < 16; ++r) top = fmaxf(fmaxf(top, sc[0][r]), sc[1][r]);
@@ -825,7 +840,7 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     fresh = fresh && !first;
     any_fresh = __any(fresh);
     // 2^s is as exact as 2^(s - ref): a reference is needed only for large scores
-    const bool up = first ? fabsf(top) > 40.0f : !fresh && top > ref;
+    const bool up = first ? fabsf(top) > 40.0f : over && top > ref;
     const float by = up ? top - ref : 0.0f;
     alpha = first ? 1.0f : exp2_fast(-by);           // a fresh row's sums are zero
     ref += by;
@@ -906,12 +921,15 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
               if (kb * 32 + (r >> 2) * 8 + (r & 3) >= mine) sc[kb][r] = kNegInf;
           }
       }
-      bool exact = any_fresh && __any(fresh && j0 < seen);
-      for (;;) {
-        if (exact) raise(sc);
+      // first pass: rows that see their first key; second: rows whose weights are large
+      // (rows apart, so that none depends on its neighbours)
+      bool over = false;
+      for (int pass = 0; pass < 2; ++pass) {
+        if (pass == 1 || (any_fresh && __any(fresh && j0 < seen))) raise(sc, over);
         if (any_ref) weights(sc, ref); else weights(sc, 0.0f);
-        if (exact || !__any(!(sum < 0x1p40f))) break;
-        exact = true;
+        const unsigned long long m = __ballot(!(sum < 0x1p40f));
+        if (m == 0) break;
+        over = ((m | m >> 32) >> row) & 1;           // in either of the row's lanes
       }
       l += sum;
       if (any_alpha) {
@@ -1086,7 +1104,10 @@ kv_attention_join_kernel(KvAttnArgs a) {
 }
 
 // Rows of a (sequence, key head) that one workgroup takes: 16 (the keys split over its
-// waves) while they fit, else 128.
+// waves) while they fit, else 128.  Measured for up to 16 rows, by 16 and by 128: 64 rows
+// of up to 8192 keys 97 and 193 us, one row of 131072 keys 44 and 65, of 1000 keys 15 and
+// 19.  At 32 rows the two take the same time within 10% either way; at 16 sequences of 64
+// rows x 8192 keys 91 and 71 us.
 inline bool few_rows(int max_q, int group) { return (long long)max_q * group <= 16; }
 
 template <int NB>
@@ -1100,6 +1121,9 @@ hipError_t launch_nb(const KvAttnArgs& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const long long rows = (long long)a.max_q * a.q_heads;
+  // A workgroup a row where there are many splits, 32 / NB rows a workgroup where there
+  // are few: always wide costs the video shape (3 splits, 81000 rows) 534 us for 461, always
+  // narrow one sequence of 32 rows x 8192 keys 35 us for 18.
   if (a.splits > 8) {
     kv_attention_join_kernel<NB, true><<<dim3((unsigned)rows, (unsigned)a.seqs), 256, 0, s>>>(a);
   } else {
