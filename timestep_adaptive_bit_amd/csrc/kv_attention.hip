@@ -285,42 +285,36 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
 
   const int* table = a.table + (long long)b * a.table_stride;
   const int in_page = (1 << c.page_shift) - 1;
-  const long long page_rows = (long long)c.heads << c.page_shift, head_row = (long long)hk << c.page_shift;
   // lane: key l%16 and block l/16 of each group of 16 keys, which lie in one page
   const bool has = g < NB;
   const unsigned c_at = row * (DP / 2) + (has ? g * 16 : 0), s_at = row * NB + (has ? g : 0);
-  v4i kc[4], vc[4];
-  uint32_t ks[4], vs[4];
-  int page[4];
+  v4i kc[4] = {}, vc[4] = {};
+  uint32_t ks[4] = {127u, 127u, 127u, 127u}, vs[4] = {127u, 127u, 127u, 127u};
+  // Lane: the page of key group lane % 4 of tile t, -1 past the keys.
+  int page;
   auto pages = [&](int t) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int j = t * TILE + 16 * k;
-      page[k] = t < w1 && j < len ? table[min(j >> c.page_shift, a.table_stride - 1)] : -1;
-    }
+    const int j = t * TILE + 16 * (lane & 3);
+    page = t < w1 && j < len ? table[min(j >> c.page_shift, a.table_stride - 1)] : -1;
   };
+  // Codes and scales of tile t.  Where a group has no page, or a key lies past the end, some
+  // row of the cache is read all the same and taken out when the tile is used: every group
+  // costs four loads at uniform bases and no branch.
   auto fetch = [&](int t) {
+    if (t >= w1 || c.num_pages == 0) return;
+    const uint32_t pg = (unsigned)page < (unsigned)c.num_pages ? (uint32_t)page : 0u;
+    const uint32_t in = (uint32_t)(t * TILE + 16 * (lane & 3)) & (uint32_t)in_page;
+    const uint64_t at = ((((uint64_t)pg * (uint32_t)c.heads + (uint32_t)hk) << c.page_shift) | in) * NB;
+    // (kept 32 bits wide here, so that the loads take them beside a scalar base)
+    uint32_t ca = c_at, sa = s_at;
+    asm("" : "+v"(ca), "+v"(sa));
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int pg = __builtin_amdgcn_readfirstlane(page[k]);
-      const int j = t * TILE + 16 * k;
-      const bool there = (unsigned)pg < (unsigned)c.num_pages;
-      const long long r = pg * page_rows + head_row + (j & in_page);
-      if (there && j + 16 <= len) {
-        kc[k] = *reinterpret_cast<const v4i*>(c.k_codes + r * (DP / 2) + c_at);
-        vc[k] = *reinterpret_cast<const v4i*>(c.v_codes + r * (DP / 2) + c_at);
-        ks[k] = (c.k_scales + r * NB)[s_at];
-        vs[k] = (c.v_scales + r * NB)[s_at];
-      } else {
-        kc[k] = vc[k] = v4i{0, 0, 0, 0};
-        ks[k] = vs[k] = 127u;
-        if (there && row < len - j) {
-          kc[k] = *reinterpret_cast<const v4i*>(c.k_codes + r * (DP / 2) + c_at);
-          vc[k] = *reinterpret_cast<const v4i*>(c.v_codes + r * (DP / 2) + c_at);
-          ks[k] = (c.k_scales + r * NB)[s_at];
-          vs[k] = (c.v_scales + r * NB)[s_at];
-        }
-      }
+      const uint64_t base = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(at >> 32), k) << 32 |
+                            (uint32_t)__builtin_amdgcn_readlane((int)at, k);
+      kc[k] = *reinterpret_cast<const v4i*>((c.k_codes + base * 16) + ca);
+      vc[k] = *reinterpret_cast<const v4i*>((c.v_codes + base * 16) + ca);
+      ks[k] = (c.k_scales + base)[sa];
+      vs[k] = (c.v_scales + base)[sa];
     }
   };
   // The start is a chain of dependent loads, so each link asks for all it can: what
@@ -423,15 +417,31 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   for (int t = w0; t < w1; ++t) {
     const int j0 = t * TILE;
     v4f s[4];
+    if (j0 + TILE > len || holes) {                  // values of rows that were not asked for: zeros
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int j = j0 + 16 * k, pi = j >> c.page_shift;
+        const bool there = !holes || (pi < a.table_stride && (unsigned)table[pi] < (unsigned)c.num_pages);
+        if (!there || row >= len - j) {
+          vs[k] = 127u;
+          vc[k] = v4i{0, 0, 0, 0};
+        }
+      }
+    }
+    // a value scale beyond bf16 (or NaN): the key's scores become NaN, its values zero
+    if (__any(has && max(max(vs[0], vs[1]), max(vs[2], vs[3])) > kMaxValueScale)) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const unsigned long long bad = __ballot(has && vs[k] > kMaxValueScale);
+        if (((bad >> row) & 0x0001000100010001ull) != 0) {
+          ks[k] = 255u;
+          vs[k] = 127u;
+          vc[k] = v4i{0, 0, 0, 0};
+        }
+      }
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      // a value scale beyond bf16 (or NaN): the key's scores become NaN, its values zero
-      const unsigned long long bad = __ballot(has && vs[k] > kMaxValueScale);
-      if (bad != 0 && ((bad >> row) & 0x0001000100010001ull) != 0) {
-        ks[k] = 255u;
-        vs[k] = 127u;
-        vc[k] = v4i{0, 0, 0, 0};
-      }
       // blocks that do not exist (lanes past NB) are zeros on the side of q
       const v8i ka = {kc[k][0], kc[k][1], kc[k][2], kc[k][3], 0, 0, 0, 0};
       const int kw = has ? (int)ks[k] : 127;
@@ -513,7 +523,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
         }
       }
       if (h == 1) {                                    // the tile's registers are free
-        fetch(t + 1);                                  // past the range: no page, no loads
+        fetch(t + 1);                                  // past the range: no loads
         pages(t + 2);
       }
       __builtin_amdgcn_wave_barrier();
