@@ -724,41 +724,37 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     const int j = t * TILE + wave * KPW;
     page = t < t1 && j < len ? table[min(j >> c.page_shift, a.table_stride - 1)] : -1;
   };
-  const long long page_rows = (long long)c.heads << c.page_shift, head_row = (long long)hk << c.page_shift;
-  v4i kc, vc;
-  uint32_t ks, vs;
-  // Codes and scales of tile t through the page at hand.  Keys of no page, and values past
-  // the sequence's end, are zeros.
+  v4i kc = {}, vc = {};
+  uint32_t ks = 127u, vs = 127u;
+  int got = 0;                   // keys of the wave's 16 that are in the cache and the sequence
+  // Codes and scales of tile t through the page at hand: four loads at uniform bases and no
+  // branch.  Without a page, or past the sequence's end, some row of the cache is read all the
+  // same and its values are zeroed when they are stored.
   auto fetch = [&](int t) {
+    if (t >= t1 || c.num_pages == 0) return;
     const int pg = __builtin_amdgcn_readfirstlane(page);
     const int j = t * TILE + wave * KPW;
     const bool there = (unsigned)pg < (unsigned)c.num_pages;
-    const long long r = pg * page_rows + head_row + (j & in_page);
-    if (there && j + KPW <= len) {
-      kc = *reinterpret_cast<const v4i*>(c.k_codes + r * (DP / 2) + k_at);
-      const uint8_t* vp = c.v_codes + r * (DP / 2) + v_at;
-      if constexpr (VW == 4) {
-        vc = *reinterpret_cast<const v4i*>(vp);
-      } else if constexpr (VW == 2) {
-        const int2 w = *reinterpret_cast<const int2*>(vp);
-        vc[0] = w.x;
-        vc[1] = w.y;
-      } else {
-        vc[0] = *reinterpret_cast<const int*>(vp);
-      }
-      ks = (c.k_scales + r * NB)[ks_at];
-      vs = (c.v_scales + r * NB)[vs_at];
+    got = there ? len - j : 0;
+    const uint64_t row = ((uint64_t)(there ? (uint32_t)pg : 0u) * (uint32_t)c.heads + (uint32_t)hk) << c.page_shift |
+                         (uint32_t)(j & in_page);
+    const uint64_t base = row * NB;
+    // (kept 32 bits wide here, so that the loads take them beside a scalar base)
+    uint32_t ka = k_at, va = v_at, ksa = ks_at, vsa = vs_at;
+    asm("" : "+v"(ka), "+v"(va), "+v"(ksa), "+v"(vsa));
+    kc = *reinterpret_cast<const v4i*>((c.k_codes + base * 16) + ka);
+    const uint8_t* vp = (c.v_codes + base * 16) + va;
+    if constexpr (VW == 4) {
+      vc = *reinterpret_cast<const v4i*>(vp);
+    } else if constexpr (VW == 2) {
+      const int2 w = *reinterpret_cast<const int2*>(vp);
+      vc[0] = w.x;
+      vc[1] = w.y;
     } else {
-      kc = vc = v4i{0, 0, 0, 0};
-      ks = vs = 127u;
-      if (there && lkey < len - j) {
-        kc = *reinterpret_cast<const v4i*>(c.k_codes + r * (DP / 2) + k_at);
-        ks = (c.k_scales + r * NB)[ks_at];
-#pragma unroll
-        for (int w = 0; w < VW; ++w) vc[w] = *reinterpret_cast<const int*>(c.v_codes + r * (DP / 2) + v_at + 4 * w);
-        vs = (c.v_scales + r * NB)[vs_at];
-      }
+      vc[0] = *reinterpret_cast<const int*>(vp);
     }
+    ks = (c.k_scales + base)[ksa];
+    vs = (c.v_scales + base)[vsa];
   };
   // Whether a page of the range is not in the cache: its keys are then hidden tile by tile.
   bool holes = false;
@@ -784,6 +780,10 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   // A value scale beyond bf16 (or NaN): the key's scores become NaN and its values zero,
   // so that rows that do not see the key (weight 0) are not touched by it.
   auto settle = [&]() {
+    if (got < KPW && lkey >= got) {
+      vs = 127u;
+      vc = v4i{0, 0, 0, 0};
+    }
     const unsigned long long bad = __ballot(vs > kMaxValueScale);
     if (bad != 0 && ((bad >> lkey) & 0x0001000100010001ull) != 0) {   // lanes of the same key
       ks = 255u;
@@ -909,7 +909,7 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     auto bring = [&]() {
       settle();
       store(st[(t + 1 - t0) & 1]);
-      fetch(t + 2);              // past the range: no page, no loads
+      fetch(t + 2);              // past the range: no loads
       next_page(t + 3);
     };
     if (j0 >= seen_hi) {         // no row of the wave sees the tile, nor a later one
