@@ -470,6 +470,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
     for (int pass = 0; pass < 2; ++pass) {
       if (pass == 1 || (any_fresh && __any(fresh && j0 < seen))) {
         float top = kNegInf;
+        asm volatile("" : "+v"(top));                // (else the compiler takes the maximum of every tile)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -841,6 +842,7 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   bool any_fresh = true, any_ref = false, any_alpha = false;     // over the wave
   auto raise = [&](const v16f (&sc)[2], bool over) {
     float top = kNegInf;
+    asm volatile("" : "+v"(top));    // (else the compiler takes the maximum of every tile)
 #pragma unroll
     for (int r = 0; r < 16; ++r) top = fmaxf(fmaxf(top, sc[0][r]), sc[1][r]);
     float tl, th;
@@ -903,18 +905,8 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   for (int t = t0; t < t1; ++t) {
     const Stage& s = st[(t - t0) & 1];
     const int j0 = t * TILE;
-    // The next tile goes to the other stage, whose readers were done before the last
-    // barrier, between this tile's weights and values: the loads have had a tile's time to
-    // arrive, the writes have the value products to land.
-    auto bring = [&]() {
-      settle();
-      store(st[(t + 1 - t0) & 1]);
-      fetch(t + 2);              // past the range: no loads
-      next_page(t + 3);
-    };
-    if (j0 >= seen_hi) {         // no row of the wave sees the tile, nor a later one
-      bring();
-    } else {
+    const bool work = j0 < seen_hi;   // else no row of the wave sees the tile, nor a later one
+    if (work) {
       v16f sc[2];
       scores(s, sc);
       if (j0 + TILE > seen_lo || holes) {
@@ -947,9 +939,16 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
         for (int d = 0; d < ND; ++d) o[d] *= alpha;
         any_alpha = false;
       }
-      bring();
-      values(s);
     }
+    // The next tile goes to the other stage, whose readers were done before the last barrier,
+    // between this tile's weights and values: the loads have had a tile's time to arrive, the
+    // writes have the value products to land.  (One place for both kinds of wave: with two, the
+    // loads on their way are waited for where the paths meet.)
+    settle();
+    store(st[(t + 1 - t0) & 1]);
+    fetch(t + 2);                // past the range: no loads
+    next_page(t + 3);
+    if (work) values(s);
     tile::lds_barrier();
   }
   {
