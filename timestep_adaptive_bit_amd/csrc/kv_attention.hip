@@ -720,26 +720,33 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   const unsigned v_at = lkey * (DP / 2) + (has_v ? vblk * 16 + vpart * VW * 4 : 0);
   const unsigned ks_at = lkey * NB + (has_k ? kblk : 0), vs_at = lkey * NB + (has_v ? vblk : 0);
   const int* table = a.table + (long long)b * a.table_stride;
-  int page;
-  auto next_page = [&](int t) {
-    const int j = t * TILE + wave * KPW;
-    page = t < t1 && j < len ? table[min(j >> c.page_shift, a.table_stride - 1)] : -1;
+  // Where the wave's 16 keys of 64 tiles lie, a lane a tile: 32 (row / 16) + how many of them
+  // are in the cache and the sequence.  One lane-wide computation for 64 tiles (waited for at
+  // once: a load whose wait is left to a later tile makes every tile wait) leaves a tile two
+  // lane reads and the additions of its bases.
+  uint32_t at_lo = 0u, at_hi = 0u;
+  auto place = [&](int from) {
+    const int j = min(from + lane, t1 - 1) * TILE + wave * KPW;
+    const int page = table[min(j >> c.page_shift, a.table_stride - 1)];
+    const bool there = (unsigned)page < (unsigned)c.num_pages;
+    const uint64_t row = (((uint64_t)(there ? (uint32_t)page : 0u) * (uint32_t)c.heads + (uint32_t)hk) << c.page_shift) |
+                         (uint32_t)(j & in_page);
+    const uint64_t at = row * 2 + (there ? (uint32_t)min(max(len - j, 0), KPW) : 0u);
+    at_lo = (uint32_t)at;
+    at_hi = (uint32_t)(at >> 32);
   };
   v4i kc = {}, vc = {};
   uint32_t ks = 127u, vs = 127u;
   int got = 0;                   // keys of the wave's 16 that are in the cache and the sequence
-  // Codes and scales of tile t through the page at hand: four loads at uniform bases and no
+  // Codes and scales of tile t: four loads at uniform bases and no
   // branch.  Without a page, or past the sequence's end, some row of the cache is read all the
   // same and its values are zeroed when they are stored.
   auto fetch = [&](int t) {
     if (t >= t1 || c.num_pages == 0) return;
-    const int pg = __builtin_amdgcn_readfirstlane(page);
-    const int j = t * TILE + wave * KPW;
-    const bool there = (unsigned)pg < (unsigned)c.num_pages;
-    got = there ? len - j : 0;
-    const uint64_t row = ((uint64_t)(there ? (uint32_t)pg : 0u) * (uint32_t)c.heads + (uint32_t)hk) << c.page_shift |
-                         (uint32_t)(j & in_page);
-    const uint64_t base = row * NB;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)at_lo, (t - t0) & 63);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)at_hi, (t - t0) & 63);
+    got = (int)(lo & 31u);
+    const uint64_t base = ((uint64_t)hi << 32 | (lo & ~31u)) * NB >> 1;      // row * NB
     // (kept 32 bits wide here, so that the loads take them beside a scalar base)
     uint32_t ka = k_at, va = v_at, ksa = ks_at, vsa = vs_at;
     asm("" : "+v"(ka), "+v"(va), "+v"(ksa), "+v"(vsa));
@@ -889,9 +896,8 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     }
   };
 
-  next_page(t0);
+  if (t0 < t1) place(t0);
   fetch(t0);
-  next_page(t0 + 1);
   if constexpr (NB % 2 != 0) {   // scale bytes of blocks that do not exist: any finite scale
     for (int i = tid; i < 2 * 64; i += NW * 64)
       reinterpret_cast<uint32_t*>(st[i / 64].ks)[i % 64] = 0x7F7F7F7Fu;
@@ -900,7 +906,6 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   settle();
   store(st[0]);
   fetch(t0 + 1);
-  next_page(t0 + 2);
   tile::lds_barrier();
   for (int t = t0; t < t1; ++t) {
     const Stage& s = st[(t - t0) & 1];
@@ -946,8 +951,8 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     // loads on their way are waited for where the paths meet.)
     settle();
     store(st[(t + 1 - t0) & 1]);
+    if (((t + 2 - t0) & 63) == 0) place(t + 2);
     fetch(t + 2);                // past the range: no loads
-    next_page(t + 3);
     if (work) values(s);
     tile::lds_barrier();
   }
