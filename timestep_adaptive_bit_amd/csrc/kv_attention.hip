@@ -26,8 +26,7 @@
 //           summed so far is scaled by 2^(old - new).
 //   values  O^T += V^T P^T with the 16x16x32 bf16 MFMA.  The order of the summed
 //           keys is free, so it is chosen as the lanes already hold them: P needs
-//           no exchange, only its rounding to bf16 (2^-9 a weight: the sums stay in
-//           fp32).  V becomes bf16 exactly (a code has 2 bits) through LDS, and is
+//           no exchange, only its rounding to bf16 (2^-9 a weight; sums stay in fp32).  V becomes bf16 exactly (a code has 2 bits) through LDS, and is
 //           read transposed by ds_read_b64_tr_b16.
 //
 // Long caches are split over workgroups (`splits` ranges of whole 64-key tiles of
@@ -52,6 +51,14 @@ constexpr int kMaxSplits = 128;
 constexpr int kNarrow = 8;    // splits that one lane joins by itself
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// sum + both bf16 weights of a pair, in fp32.  The rounded weights are summed, not the exact
+// ones: what a row's values are multiplied with then adds up to one, and a row that sees one
+// key answers that key's value exactly.
+__device__ __forceinline__ float add_pair(uint32_t pair, float sum) {
+  const v2bf one = {(__bf16)1.0f, (__bf16)1.0f};
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf, pair), one, sum, false);
+}
 
 // Byte offset of 16-byte piece `half` of 16-element run `c` of key row `key` in the
 // bf16 value tile: rows of RS bytes.  Runs are XORed with bits of the key so that what
@@ -240,11 +247,13 @@ __device__ __forceinline__ int seen_keys(const KvAttnArgs& a, int len, int n, in
 // are in LDS or in the matrix core; the values of 32 keys are staged at a time (8 KB of
 // LDS a wave), and registers allow three workgroups a CU.
 //
-// Measured at 32 heads over 8, 128 elements: 64 rows of up to 8192 keys 97 us (371 MB,
-// 3.8 TB/s; large copies reach 5.2, reads alone 6), one row of 131072 keys 44 us with
-// the join (143 MB, 3.3 TB/s), one row of 1000 keys 15 us.  A workgroup's start costs
-// 6 us (bounds, pages, then codes and tables: three loads that depend on each other),
-// which is what short caches take.
+// Measured at 32 heads over 8, 128 elements: 64 rows of up to 8192 keys 87 us (371 MB,
+// 4.3 TB/s; 64 of 8192 each 108 us, 5.3 TB/s, what a large copy reaches: the rest is the
+// longest sequences, a lone workgroup passing 256 keys in 1.25 us), one row of 131072
+// keys 39 us with the join (143 MB, 3.7 TB/s), one row of 1000 keys 13 - 16 us.  A
+// workgroup's start costs 6 us (bounds, pages, then codes and tables: three loads that
+// depend on each other), which is what short caches take.  Six, eight or twelve waves a
+// workgroup level out ragged batches but fill the chip less: 99 to 112 us for 97 then.
 template <int NB>
 __global__ void __launch_bounds__(256, 3)
 kv_attention_rows16_kernel(KvAttnArgs a) {
@@ -494,9 +503,9 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
       for (int k = 0; k < 4; ++k) {
         const float w0_ = exp2_fast(s[k][0] - ref), w1_ = exp2_fast(s[k][1] - ref);
         const float w2_ = exp2_fast(s[k][2] - ref), w3_ = exp2_fast(s[k][3] - ref);
-        sum += (w0_ + w1_) + (w2_ + w3_);
         p[2 * k] = pack_bf16(w0_, w1_);
         p[2 * k + 1] = pack_bf16(w2_, w3_);
+        sum = add_pair(p[2 * k + 1], add_pair(p[2 * k], sum));
       }
       unsigned long long m = __ballot(!(sum < 0x1p40f));
       if (m == 0) break;
@@ -630,16 +639,18 @@ __device__ __forceinline__ v16f score_term(v4i x, const v8i& q, v16f s, int byte
 // the 64 keys), values with 32x32x16, P staying in its lanes.
 //
 // Vector instructions and matrix products share a wave's issue and about balance, so a
-// tile costs the vector units one exponential a score, half a rounding to bf16 and one
-// addition; without a reference (see the top) the scores go to the exponential as they
-// leave the matrix core.
+// tile costs the vector units one exponential a score, half a rounding to bf16 and half a
+// dot product that sums; without a reference (see the top) the scores go to the exponential
+// as they leave the matrix core, and what a tile's addresses need is prepared for 64 tiles
+// at once.
 //
-// Measured: 2700 rows x 17776 keys x 30 heads x 64 in 460 us (800 TFLOP/s counted as
-// 4 flops a key, row and element; a library bf16 product of 8192^3 reaches 1207), causal
-// turns of 32 heads over 8 at 128 elements in 495 us (650 TFLOP/s counting visible keys),
-// 2 x 4096 rows x 300 keys x 16 heads x 72 in 32 us.  The matrix cores are busy for half
-// of the cycles.  Level or slower: scores of a tile beside the weights of the one before,
-// eight waves a workgroup, 32 keys a step, three stages, heads as the fastest index.
+// Measured: 2700 rows x 17776 keys x 30 heads x 64 in 424 us with the join (870 TFLOP/s at
+// 4 flops a key, row and element; a library bf16 product of 8192^3 reaches 1207), four
+// causal turns (1024 to 2048 queries behind caches of up to 6144 keys, 32 heads over 8, 128
+// elements) in 470 us (940 TFLOP/s of visible keys), 2 x 4096 rows x 300 keys x 16 heads x
+// 72 in 31 us.  Level or slower: scores of a tile beside the weights of the one before,
+// eight waves a workgroup, 32 keys a step, three stages, heads or sequences as the fastest
+// index (causal turns 527 us for 466).
 template <int NB>
 __global__ void __launch_bounds__(256, NB <= 2 ? 3 : 2)
 kv_attention_rows128_kernel(KvAttnArgs a) {
@@ -875,9 +886,9 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float x = exp2_fast(sc[i >> 3][2 * (i & 7)] - from), y = exp2_fast(sc[i >> 3][2 * (i & 7) + 1] - from);
-      even += x;
-      odd += y;
       p[i] = pack_bf16(x, y);
+      if (i & 1) odd = add_pair(p[i], odd);
+      else even = add_pair(p[i], even);
     }
     sum = even + odd;
   };
@@ -1129,9 +1140,9 @@ kv_attention_join_kernel(KvAttnArgs a) {
 
 // Rows of a (sequence, key head) that one workgroup takes: 16 (the keys split over its
 // waves) while they fit, else 128.  Measured for up to 16 rows, by 16 and by 128: 64 rows
-// of up to 8192 keys 97 and 193 us, one row of 131072 keys 44 and 65, of 1000 keys 15 and
-// 19.  At 32 rows the two take the same time within 10% either way; at 16 sequences of 64
-// rows x 8192 keys 91 and 71 us.
+// of up to 8192 keys 87 and 158 us, one row of 131072 keys 40 and 55, of 1000 keys 15 and
+// 18.  At 32 rows neither form is ahead: 64 sequences x 4096 keys 92 and 84 us, one of 131072
+// keys 43 and 51; at 16 sequences of 64 rows x 8192 keys 89 and 68 us.
 inline bool few_rows(int max_q, int group) { return (long long)max_q * group <= 16; }
 
 template <int NB>
@@ -1146,8 +1157,8 @@ hipError_t launch_nb(const KvAttnArgs& a, hipStream_t s) {
   if (e != hipSuccess || a.splits == 1) return e;
   const long long rows = (long long)a.max_q * a.q_heads;
   // A workgroup a row where there are many splits, 32 / NB rows a workgroup where there
-  // are few: always wide costs the video shape (3 splits, 81000 rows) 534 us for 461, always
-  // narrow one sequence of 32 rows x 8192 keys 35 us for 18.
+  // are few: always wide costs the video shape (3 splits, 81000 rows) 804 us for 420, narrow up
+  // to 32 splits one sequence of 32 rows x 8192 keys 34 us for 17.
   if (a.splits > kNarrow) {
     kv_attention_join_kernel<NB, true><<<dim3((unsigned)rows, (unsigned)a.seqs), 256, 0, s>>>(a);
   } else {
@@ -1169,8 +1180,8 @@ int kv_attention_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_
   if (few) {
     // Two workgroups a CU, of at least four tiles (one a wave) each: a workgroup spends
     // about 8 us on its start and end, so more of them cost more than they balance (one
-    // row of 131072 keys: 64 splits 44 us, 96 45, 128 52; 64 rows of up to 8192 keys:
-    // 98 us unsplit, 105 in halves, 94 in thirds).
+    // row of 131072 keys: 64 splits 44 us, 96 45, 128 52 then; 64 rows of 5000 keys: 73 us
+    // unsplit, 81 in halves, 79 in thirds; of 1 to 10000 keys: 86, 92 and 81).
     long long want = (2ll * NUM_CUS + base - 1) / base;
     const long long most = (tiles + 3) / 4;
     want = want < most ? want : most;
