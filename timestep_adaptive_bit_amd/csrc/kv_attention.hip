@@ -855,11 +855,11 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     }
   };
   // Sets the reference of rows that see their first key, raises it to the largest score in
-  // rows that are `over`; what is summed so far is to be scaled by alpha (1 in the first
-  // pass over a tile, where only fresh rows move).
+  // rows that are `over`; the scores, relative to it, move along, and what is summed so far
+  // is to be scaled by alpha (1 in the first pass over a tile, where only fresh rows move).
   float alpha = 1.0f;
   bool any_fresh = true, any_ref = false, any_alpha = false;     // over the wave
-  auto raise = [&](const v16f (&sc)[2], bool over) {
+  auto raise = [&](v16f (&sc)[2], bool over) {
     float top = kNegInf;
     asm volatile("" : "+v"(top));    // (else the compiler takes the maximum of every tile)
 #pragma unroll
@@ -871,21 +871,25 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     fresh = fresh && !first;
     any_fresh = __any(fresh);
     // 2^s is as exact as 2^(s - ref): a reference is needed only for large scores
-    const bool up = first ? fabsf(top) > 40.0f : over && top > ref;
-    const float by = up ? top - ref : 0.0f;
+    const bool up = first ? fabsf(top) > 40.0f : over && top > 0.0f;
+    const float by = up ? top : 0.0f;
     alpha = first ? 1.0f : exp2_fast(-by);           // a fresh row's sums are zero
     ref += by;
     l *= alpha;
     any_ref = __any(ref != 0.0f);
     any_alpha = __any(alpha != 1.0f);
+    if (__any(by != 0.0f)) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) sc[kb] -= by;
+    }
   };
   uint32_t p[16];                // pairs of weights, in the order of the value products
   float sum;
-  auto weights = [&](const v16f (&sc)[2], float from) __attribute__((always_inline)) {
+  auto weights = [&](const v16f (&sc)[2]) __attribute__((always_inline)) {
     float even = 0.0f, odd = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float x = exp2_fast(sc[i >> 3][2 * (i & 7)] - from), y = exp2_fast(sc[i >> 3][2 * (i & 7) + 1] - from);
+      const float x = exp2_fast(sc[i >> 3][2 * (i & 7)]), y = exp2_fast(sc[i >> 3][2 * (i & 7) + 1]);
       p[i] = pack_bf16(x, y);
       if (i & 1) odd = add_pair(p[i], odd);
       else even = add_pair(p[i], even);
@@ -940,12 +944,16 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
               if (kb * 32 + (r >> 2) * 8 + (r & 3) >= mine) sc[kb][r] = kNegInf;
           }
       }
+      if (any_ref) {
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) sc[kb] -= ref;
+      }
       // first pass: rows that see their first key; second: rows whose weights are large
       // (rows apart, so that none depends on its neighbours)
       bool over = false;
       for (int pass = 0; pass < 2; ++pass) {
         if (pass == 1 || (any_fresh && __any(fresh && j0 < seen))) raise(sc, over);
-        if (any_ref) weights(sc, ref); else weights(sc, 0.0f);
+        weights(sc);
         const unsigned long long m = __ballot(!(sum < 0x1p40f));
         if (m == 0) break;
         over = ((m | m >> 32) >> row) & 1;           // in either of the row's lanes
