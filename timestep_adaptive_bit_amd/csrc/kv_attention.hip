@@ -800,12 +800,14 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   // A value scale beyond bf16 (or NaN): the key's scores become NaN and its values zero,
   // so that rows that do not see the key (weight 0) are not touched by it.
   auto settle = [&]() {
-    if (got < KPW && lkey >= got) {
+    if (got >= KPW && !__any(vs > kMaxValueScale)) return;
+    asm volatile("");                                // a branch, not selects in every tile
+    if (lkey >= got) {                               // rows that were not asked for
       vs = 127u;
       vc = v4i{0, 0, 0, 0};
     }
     const unsigned long long bad = __ballot(vs > kMaxValueScale);
-    if (bad != 0 && ((bad >> lkey) & 0x0001000100010001ull) != 0) {   // lanes of the same key
+    if (((bad >> lkey) & 0x0001000100010001ull) != 0) {            // lanes of the same key
       ks = 255u;
       vs = 127u;
       vc = v4i{0, 0, 0, 0};
@@ -896,16 +898,24 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     }
     sum = even + odd;
   };
-  auto values = [&](const Stage& s) {
-    const int key0 = 4 * half + ((lane & 15) >> 2), run0 = (lane >> 4) & 1, piece = (lane >> 1) & 1;
+  // Places of the lane's transposed reads: of key 16 u + key0 (+ 8), run 2 d + run0, beside
+  // u keys of 16 rows.  (Opaque, or the compiler forms them from their parts in every tile.)
+  uint32_t v_at0[ND], v_at8[ND];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {                    // 16 keys each
+  for (int d = 0; d < ND; ++d) {
+    const int key0 = 4 * half + ((lane & 15) >> 2), run = 2 * d + ((lane >> 4) & 1), piece = (lane >> 1) & 1;
+    v_at0[d] = v_off<RS>(key0, run, piece) + (lane & 1) * 8;
+    v_at8[d] = v_off<RS>(key0 + 8, run, piece) + (lane & 1) * 8;
+    asm volatile("" : "+v"(v_at0[d]), "+v"(v_at8[d]));
+  }
+  auto values = [&](const Stage& s) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {                    // 16 keys each: the same bits of the XOR
       const v8bf w = __builtin_bit_cast(v8bf, make_uint4(p[4 * u], p[4 * u + 1], p[4 * u + 2], p[4 * u + 3]));
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
-        const int key = key0 + 16 * u, run = 2 * d + run0;
-        const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(s.v + v_off<RS>(key, run, piece) + (lane & 1) * 8));
-        const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(s.v + v_off<RS>(key + 8, run, piece) + (lane & 1) * 8));
+        const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(s.v + v_at0[d] + u * 16 * RS));
+        const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(s.v + v_at8[d] + u * 16 * RS));
         const v8bf v = __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
         o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w, o[d], 0, 0, 0);
       }
