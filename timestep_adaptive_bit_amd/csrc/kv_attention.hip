@@ -418,7 +418,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   __syncthreads();
 
   float ref = 0.0f, l = 0.0f;
-  bool fresh = true, any_fresh = true;
+  bool fresh = true, any_fresh = true, any_ref = false;      // any: over the wave
   v4f o[ND];
 #pragma unroll
   for (int d = 0; d < ND; ++d) o[d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
@@ -477,6 +477,10 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
     float sum;
     uint32_t p[8];
     bool over = false;
+    if (any_ref) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] -= ref;
+    }
     for (int pass = 0; pass < 2; ++pass) {
       if (pass == 1 || (any_fresh && __any(fresh && j0 < seen))) {
         float top = kNegInf;
@@ -490,19 +494,24 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
         const bool first = fresh && top > kNegInf;
         fresh = fresh && !first;
         any_fresh = __any(fresh);
-        const bool up = first ? fabsf(top) > 40.0f : over && top > ref;
-        const float by = up ? top - ref : 0.0f;
-        const float alpha = first ? 1.0f : exp2_fast(-by);
+        const bool up = first ? fabsf(top) > 40.0f : over && top > 0.0f;
+        const float by = up ? top : 0.0f;
         ref += by;
-        l *= alpha;
+        any_ref = __any(ref != 0.0f);
+        if (__any(by != 0.0f)) {
+          const float alpha = first ? 1.0f : exp2_fast(-by);
+          l *= alpha;
 #pragma unroll
-        for (int d = 0; d < ND; ++d) o[d] *= alpha;
+          for (int d = 0; d < ND; ++d) o[d] *= alpha;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[k] -= by;
+        }
       }
       sum = 0.0f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float w0_ = exp2_fast(s[k][0] - ref), w1_ = exp2_fast(s[k][1] - ref);
-        const float w2_ = exp2_fast(s[k][2] - ref), w3_ = exp2_fast(s[k][3] - ref);
+        const float w0_ = exp2_fast(s[k][0]), w1_ = exp2_fast(s[k][1]);
+        const float w2_ = exp2_fast(s[k][2]), w3_ = exp2_fast(s[k][3]);
         p[2 * k] = pack_bf16(w0_, w1_);
         p[2 * k + 1] = pack_bf16(w2_, w3_);
         sum = add_pair(p[2 * k + 1], add_pair(p[2 * k], sum));
