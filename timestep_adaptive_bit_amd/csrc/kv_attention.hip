@@ -247,7 +247,7 @@ __device__ __forceinline__ int seen_keys(const KvAttnArgs& a, int len, int n, in
 // are in LDS or in the matrix core; the values of 32 keys are staged at a time (8 KB of
 // LDS a wave), and registers allow three workgroups a CU.
 //
-// Measured at 32 heads over 8, 128 elements: 64 rows of up to 8192 keys 87 us (371 MB,
+// Measured at 32 heads over 8, 128 elements: 64 rows of up to 8192 keys 84 - 87 us (371 MB,
 // 4.3 TB/s; 64 of 8192 each 108 us, 5.3 TB/s, what a large copy reaches: the rest is the
 // longest sequences, a lone workgroup passing 256 keys in 1.25 us), one row of 131072
 // keys 39 us with the join (143 MB, 3.7 TB/s), one row of 1000 keys 13 - 16 us.  A
@@ -653,13 +653,16 @@ __device__ __forceinline__ v16f score_term(v4i x, const v8i& q, v16f s, int byte
 // as they leave the matrix core, and what a tile's addresses need is prepared for 64 tiles
 // at once.
 //
-// Measured: 2700 rows x 17776 keys x 30 heads x 64 in 424 us with the join (870 TFLOP/s at
-// 4 flops a key, row and element; a library bf16 product of 8192^3 reaches 1207), four
-// causal turns (1024 to 2048 queries behind caches of up to 6144 keys, 32 heads over 8, 128
-// elements) in 470 us (940 TFLOP/s of visible keys), 2 x 4096 rows x 300 keys x 16 heads x
-// 72 in 31 us.  Level or slower: scores of a tile beside the weights of the one before,
+// Measured: 2700 rows x 17776 keys x 30 heads x 64 in 395 - 409 us with the join (900 - 930
+// TFLOP/s at 4 flops a key, row and element; a library bf16 product of 8192^3 reaches
+// 1207), four causal turns (1024 to 2048 queries behind caches of up to 6144 keys, 32 heads
+// over 8, 128 elements) at 950 TFLOP/s of visible keys, 2 x 4096 rows x 300 keys x 16 heads
+// x 72 in 31 us.  Matrix cores are busy for a third of the cycles, LDS for 30%; a wave
+// waits for its turn to issue most of the time.  Level or slower: scores of a tile beside the weights of the one before,
 // eight waves a workgroup, 32 keys a step, three stages, heads or sequences as the fastest
-// index (causal turns 527 us for 466).
+// index (causal turns 527 us for 466).  Up to 64 elements three workgroups fit a CU (four
+// would spill: 485 us for 409); 96 and 128 elements take 196 and 226 registers, two
+// workgroups (three spill: 38 us for 30 at 72 elements).
 template <int NB>
 __global__ void __launch_bounds__(256, NB <= 2 ? 3 : 2)
 kv_attention_rows128_kernel(KvAttnArgs a) {
