@@ -210,6 +210,30 @@ def test_around_sixteen_rows_a_key_head(ctx, n, hq, hk, D, keys):
     _check(_run(ctx, p, True, D ** -0.5), _want(p, True, D ** -0.5), keys)
 
 
+def test_ranges_of_many_tiles(ctx):
+    """A workgroup that passes more tiles than it places at once, some of their pages missing:
+    512 key heads, so that the 4500 keys stay one range; three heads against fp64."""
+    rng = np.random.default_rng(21)
+    n, hk, D, ps, keys = 20, 512, 16, 16, 4500
+    pages = (keys + ps - 1) // ps
+    arr = {"k_codes": rng.integers(0, 256, (pages, hk, ps, 16), dtype=np.uint8),
+           "v_codes": rng.integers(0, 256, (pages, hk, ps, 16), dtype=np.uint8),
+           "k_scales": rng.integers(122, 126, (pages, hk, ps, 1), dtype=np.uint8),
+           "v_scales": rng.integers(124, 128, (pages, hk, ps, 1), dtype=np.uint8)}
+    for name in ("k_codes", "v_codes"):
+        arr[name][..., D // 2:] = 0            # past the head's elements
+    table = rng.permutation(pages).astype(np.int32)[None]
+    table[0, [70, 256, 270]] = -1, pages, -5
+    wide = torch.from_numpy(rng.standard_normal((n, hk * D)).astype(np.float32)).bfloat16()
+    p = dict(arr=arr, table=table, cu=np.array([0, n], np.int32), lens=np.array([keys], np.int32), wide=wide,
+             rope=None, D=D, hq=hk, hk=hk, had=0, max_q=n, max_kv=keys, ps=ps)
+    out, lse = _run(ctx, p, True, 0.25)
+    pick = [0, 255, 511]
+    part = dict(p, arr={k: np.ascontiguousarray(v[:, pick]) for k, v in arr.items()},
+                q=O.bf16_to_f32(S.bf16_bits(wide)).reshape(n, hk, D)[:, pick])
+    _check((out[:, pick], lse[:, pick]), _want(part, True, 0.25), keys)
+
+
 def test_reference_rises_late(ctx):
     """Scores near nothing for the first tiles, then one of hundreds: what was summed so far has
     to be scaled away, in the tile where the reference rises and in the join of the ranges."""
