@@ -575,7 +575,8 @@ int tabit_kv_read(tabit_ctx* ctx, const tabit_kv_cache* cache, const int64_t* sl
  * table; with `causal` query i of the sequence's n sees j <= kv_lens[b] - n + i.
  * Query head h reads key head h / (num_q_heads / num_kv_heads).  A query that sees
  * no key answers zeros (lse -inf).  Scores, softmax and sums are fp32; a query
- * keeps 13 bits below its block's largest element, a weight is rounded to bf16.
+ * keeps 13 bits below its block's largest element, a weight is rounded to bf16 and
+ * summed as rounded.
  *   q            device bf16, token t's [num_q_heads][head_dim] at t * q_stride
  *                elements (multiple of 8), 16-byte aligned
  *   cu_q         device int32 [num_seqs + 1]: sequence b's rows are
@@ -590,7 +591,8 @@ int tabit_kv_read(tabit_ctx* ctx, const tabit_kv_cache* cache, const int64_t* sl
  *                finite, answers NaN
  *   out          device bf16 [num_tokens][num_q_heads][head_dim], 16-byte aligned
  *   lse          device fp32 [num_tokens][num_q_heads] or NULL: natural logarithm
- *                of the row's sum of exp(score)
+ *                of the row's sum of exp(score), each rounded to bf16 (2^-9 of the
+ *                sum at most, so exp(lse) * out joins ranges of keys without loss)
  *   ws           device workspace of tabit_kv_attention_workspace_bytes bytes,
  *                16-byte aligned (NULL when that is 0)
  * num_seqs and num_kv_heads at most 65535.  The result does not depend on timing:
