@@ -1,0 +1,58 @@
+"""The cache, the attention and the norms at the far ends of what their entry points accept:
+counts near 2^31, grids past 2^32 threads, bounds far beyond the lengths."""
+import pytest
+import torch
+
+import timestep_adaptive_bit_amd as T
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    c = T.Context()
+    yield c
+    c.close()
+
+
+@pytest.fixture
+def room():
+    """room(gib): skips where the card has less free memory; all of it is given back after."""
+    def need(gib):
+        torch.cuda.empty_cache()
+        if torch.cuda.mem_get_info()[0] < gib << 30:
+            pytest.skip(f"needs {gib} GiB of free device memory")
+    yield need
+    torch.cuda.empty_cache()
+
+
+def test_append_and_read_of_more_tokens_than_seven_pieces(ctx, room):
+    """One head of 64 elements or less goes in pieces of 2^28 tokens: the eighth begins at 7 * 2^28
+    and its end is past 2^31."""
+    room(100)
+    n, D = 7 * (1 << 28) + 37, 8
+    print("append", n, "tokens", flush=True)
+    cache = T.KVCache.empty(1, 16, 1, D, 0, DEV)
+    x = torch.zeros((n, 1, D), dtype=torch.bfloat16, device=DEV)
+    slots = torch.full((n,), -1, dtype=torch.int64, device=DEV)
+    at = [0, (1 << 28) - 1, 1 << 28, 7 * (1 << 28) - 1, 7 * (1 << 28), n - 1]
+    vals = torch.tensor([1.0, -2.0, 0.5, 3.0, 6.0, -1.5], dtype=torch.bfloat16, device=DEV)
+    for i, t in enumerate(at):
+        x[t], slots[t] = vals[i], 2 * i
+    ctx.kv_append(cache, x, x, slots)
+    rk, rv = ctx.kv_read(cache, torch.arange(16, device=DEV))
+    want = torch.zeros(16, dtype=torch.bfloat16, device=DEV)
+    want[0:12:2] = vals
+    assert torch.equal(rk, want[:, None, None].expand(16, 1, D)) and torch.equal(rk, rv)
+    print("read", n, "tokens", flush=True)
+    v = torch.ones_like(x)
+    x.fill_(1.0)
+    ctx.kv_read(cache, slots, k=x, v=v)
+    for i, t in enumerate(at):
+        for r in (x, v):
+            assert bool((r[t] == vals[i]).all()), t
+            r[t] = 0
+    for r in (x, v):                       # slots outside the cache: zeros, up to the last token
+        for part in r.view(-1).split(1 << 30):
+            assert not bool(part.any())

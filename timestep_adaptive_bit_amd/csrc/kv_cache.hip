@@ -197,8 +197,8 @@ hipError_t in_pieces(const KvCacheArgs& c, int tokens, Launch launch) {
   const int hb_shift = c.heads % 4 == 0 ? 2 : c.heads % 2 == 0 ? 1 : 0;
   const int per = (NT / gl) >> hb_shift, tiles = c.heads >> hb_shift;
   const int piece = max(1, (1 << 23) / tiles) * per;
-  for (int first = 0; first < tokens; first += piece) {
-    const int n = min(piece, tokens - first);
+  for (long long first = 0; first < tokens; first += piece) {   // first + piece may pass 2^31
+    const int n = (int)min((long long)piece, tokens - first);
     launch(gl, hb_shift, (unsigned)((n + per - 1) / per * tiles), first, n);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
@@ -211,7 +211,7 @@ hipError_t launch_kv_append(const KvCacheArgs& c, const uint16_t* k, long long k
                             const uint16_t* v, long long v_stride, int tokens,
                             const int64_t* slots, const RopeArgs& rope, const int* positions,
                             hipStream_t s) {
-  return in_pieces(c, tokens, [&](int gl, int hb_shift, unsigned grid, int first, int n) {
+  return in_pieces(c, tokens, [&](int gl, int hb_shift, unsigned grid, long long first, int n) {
     auto* kernel = gl == 8 ? &kv_append_kernel<8> : &kv_append_kernel<16>;
     kernel<<<grid, NT, 0, s>>>(c, hb_shift, k + first * k_stride, k_stride, v + first * v_stride,
                                v_stride, n, slots + first, rope,
@@ -221,8 +221,8 @@ hipError_t launch_kv_append(const KvCacheArgs& c, const uint16_t* k, long long k
 
 hipError_t launch_kv_read(const KvCacheArgs& c, const int64_t* slots, int tokens, uint16_t* k,
                           uint16_t* v, hipStream_t s) {
-  return in_pieces(c, tokens, [&](int gl, int hb_shift, unsigned grid, int first, int n) {
-    const long long o = (long long)first * c.heads * c.head_dim;
+  return in_pieces(c, tokens, [&](int gl, int hb_shift, unsigned grid, long long first, int n) {
+    const long long o = first * c.heads * c.head_dim;
     auto* kernel = gl == 8 ? &kv_read_kernel<8> : &kv_read_kernel<16>;
     kernel<<<grid, NT, 0, s>>>(c, hb_shift, slots + first, n, k + o, v + o);
   });
