@@ -56,3 +56,20 @@ def test_append_and_read_of_more_tokens_than_seven_pieces(ctx, room):
     for r in (x, v):                       # slots outside the cache: zeros, up to the last token
         for part in r.view(-1).split(1 << 30):
             assert not bool(part.any())
+
+
+@pytest.mark.parametrize("rows,width", [((1 << 31) - 5, 32), ((1 << 22) + 3, 16384)])
+def test_norm_of_rows_past_the_counts_of_one_launch(ctx, room, rows, width):
+    """Rows whose share, rounded up, passes 2^31 rows; rows of a workgroup each past 2^32 threads."""
+    room(132)
+    print("block_norm", rows, width, flush=True)
+    x = torch.ones((rows, width), dtype=torch.bfloat16, device=DEV)
+    for r in (0, rows // 2, rows - 1):
+        x[r] = 3.0
+    ctx.block_norm(x, x_out=x, res_scale=2.0, want_h=False)
+    for r in (0, rows // 2, rows - 1):
+        assert bool((x[r] == 6).all()), r
+        x[r] = 2.0
+    step = (1 << 31) // width
+    for part in x.split(step):
+        assert not bool(part.ne(2.0).any())

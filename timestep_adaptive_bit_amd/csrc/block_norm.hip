@@ -164,16 +164,17 @@ __device__ __forceinline__ void pre_factors(const BlockNormArgs& a, size_t mod, 
 
 template <int TPR, int S>
 __global__ void __launch_bounds__(TPR > 256 ? TPR : 256, TPR > 256 ? 4 : 2)
-block_norm_kernel(BlockNormArgs a, int rows_per) {
+block_norm_kernel(BlockNormArgs a, int rows_per, int unit0) {
   constexpr int NT = TPR > 256 ? TPR : 256;
   static_assert(TPR == 64 || TPR == NT, "a row is one wave's or one workgroup's");
   __shared__ float buf[TPR > 64 ? 10 : 1][16];
   const int li = TPR == NT ? threadIdx.x : threadIdx.x & 63;
   const int lane = threadIdx.x & 63;
   // this wave's (workgroup's) rows
-  const int unit = TPR == NT ? blockIdx.x
-                             : (int)(blockIdx.x * (NT / 64)) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row0 = min((long long)unit * rows_per, (long long)a.rows), row1 = min(row0 + rows_per, a.rows);
+  const int unit = unit0 + (TPR == NT ? (int)blockIdx.x
+                                      : (int)(blockIdx.x * (NT / 64)) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+  const int row0 = min((long long)unit * rows_per, (long long)a.rows);
+  const int row1 = row0 + min(rows_per, a.rows - row0);     // (the sum of the two may pass 2^31)
   const int chunks = a.width >> 3;
 
   // the longest rows leave no registers for the shared factors or the next row: a
@@ -326,10 +327,16 @@ hipError_t launch(const BlockNormArgs& a, hipStream_t s) {
   // is a run of its own.
   constexpr int kWavesPerSimd = S == 1 ? 8 : S == 2 ? 3 : 2;
   constexpr int kUnits = 256 * 4 * kWavesPerSimd * 64 / TPR;
-  const int rows_per = TPR > 256 ? 1 : (a.rows + kUnits - 1) / kUnits;
-  const int units = (a.rows + rows_per - 1) / rows_per;
-  block_norm_kernel<TPR, S><<<(units + RPW - 1) / RPW, NT, 0, s>>>(a, rows_per);
-  return hipGetLastError();
+  const int rows_per = TPR > 256 ? 1 : (a.rows - 1) / kUnits + 1;
+  const int units = (a.rows - 1) / rows_per + 1;
+  // a launch is limited to 2^32 threads, which rows of the longest kind can pass
+  constexpr int kMost = 1 << 21;
+  for (int first = 0;; first += kMost) {
+    const int n = min(kMost, units - first);
+    block_norm_kernel<TPR, S><<<(n + RPW - 1) / RPW, NT, 0, s>>>(a, rows_per, first);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || units - first <= kMost) return e;
+  }
 }
 
 }  // namespace
