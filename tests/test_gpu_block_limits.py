@@ -73,3 +73,33 @@ def test_norm_of_rows_past_the_counts_of_one_launch(ctx, room, rows, width):
     step = (1 << 31) // width
     for part in x.split(step):
         assert not bool(part.ne(2.0).any())
+
+
+def _one_page(heads, D, seed, pages=1, page=16):
+    """A full cache of ordinary codes and scales."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    dp = (D + 31) // 32 * 32
+    codes = [torch.randint(0, 256, (pages, heads, page, dp // 2), generator=g, device=DEV).byte() for _ in range(2)]
+    for c in codes:
+        c[..., D // 2:] = 0
+    scales = [torch.randint(124, 128, (pages, heads, page, dp // 32), generator=g, device=DEV).byte() for _ in range(2)]
+    return T.KVCache(codes[0], scales[0], codes[1], scales[1], head_dim=D)
+
+
+def test_attention_of_more_workgroups_than_one_launch(ctx):
+    """65535 sequences x 257 heads of 17 rows are more than 2^32 threads; rows in three of them."""
+    seqs, heads, D, n = 65535, 257, 8, 17
+    print("attention", seqs, "sequences", heads, "heads", flush=True)
+    cache = _one_page(heads, D, 1)
+    some = [0, 40000, seqs - 1]
+    rows = torch.zeros(seqs + 1, dtype=torch.int32)
+    rows[[i + 1 for i in some]] = n
+    q = torch.randn(n * len(some), heads, D, generator=torch.Generator().manual_seed(2)).bfloat16().to(DEV)
+    lens = torch.full((seqs,), 16, dtype=torch.int32)
+    lens[some[1]] = 5
+    table = torch.zeros((seqs, 1), dtype=torch.int32, device=DEV)
+    out = torch.full_like(q, 9.0)
+    ctx.kv_attention(cache, q, rows.cumsum(0).int().to(DEV), table, lens.to(DEV), n, 16, out=out)
+    cu = torch.arange(0, n * len(some) + 1, n, dtype=torch.int32, device=DEV)
+    want = ctx.kv_attention(cache, q, cu, table[:3].contiguous(), lens[some].to(DEV), n, 16)
+    assert torch.equal(out, want) and not bool((out == 9).any())

@@ -1180,10 +1180,25 @@ hipError_t launch_nb(const KvAttnArgs& a, hipStream_t s) {
   const bool few = few_rows(a.max_q, a.group);
   const int per = few ? 16 : 128;
   const int row_tiles = (int)(((long long)a.max_q * a.group + per - 1) / per);
-  const dim3 grid((unsigned)((long long)row_tiles * a.splits), (unsigned)a.cache.heads, (unsigned)a.seqs);
-  if (few) kv_attention_rows16_kernel<NB><<<grid, 256, 0, s>>>(a);
-  else kv_attention_rows128_kernel<NB><<<grid.x * grid.y * grid.z, 256, 0, s>>>(a);
-  hipError_t e = hipGetLastError();
+  const unsigned per_head = (unsigned)((long long)row_tiles * a.splits);
+  hipError_t e = hipSuccess;
+  if (few) {
+    kv_attention_rows16_kernel<NB><<<dim3(per_head, (unsigned)a.cache.heads, (unsigned)a.seqs), 256, 0, s>>>(a);
+    e = hipGetLastError();
+  } else {
+    // one axis, which is limited to 2^32 threads: as many sequences a launch as fit
+    const long long per_seq = (long long)per_head * a.cache.heads;
+    const int most = (int)min(max(((1ll << 24) - 1) / per_seq, 1ll), (long long)a.seqs);
+    for (int first = 0; first < a.seqs && e == hipSuccess; first += most) {
+      KvAttnArgs part = a;
+      part.seqs = min(most, a.seqs - first);
+      part.cu_q += first;
+      part.kv_lens += first;
+      part.table += (long long)first * a.table_stride;
+      kv_attention_rows128_kernel<NB><<<(unsigned)(per_seq * part.seqs), 256, 0, s>>>(part);
+      e = hipGetLastError();
+    }
+  }
   if (e != hipSuccess || a.splits == 1) return e;
   const long long rows = (long long)a.max_q * a.q_heads;
   // A workgroup a row where there are many splits, 32 / NB rows a workgroup where there
