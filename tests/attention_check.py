@@ -1,0 +1,118 @@
+"""Bounds of the cached attention's error for queries that it holds exactly (test support).
+
+A query of small whole numbers with a scale of 2^-k / log2(e) (times 32 for a cache that is
+transformed) becomes, rotated by nothing and transformed or not, whole numbers of at most seven
+bits times 2^-k: the three FP6 terms of the kernel hold them but for the last bit of the scale's
+product with log2(e).  Then only this is left of its error:
+
+  scores    fp32: 2^-21 of the absolute sum of a score's products, at most
+  weights   2^s by the hardware's exponential (2^-21 relative) and rounded to bf16: 2^-8 at most.
+            The rounded weights are summed, so a weight's error e moves the output by e (v - o),
+            and all of them by 2^-8 sum_j p_j |v_j - o| at most; a transformed cache's output is
+            1/32 of the sum over a block of such terms
+  sums      fp32: 2^-22 a summed key
+  output    bf16: 2^-8 of itself, and half of the smallest step, 2^-134
+  lse       the logarithm of what the weights' rounding and the sums move: 2^-8 + 2^-21, and 2^-22
+            a key, and its own rounding
+"""
+import math
+
+import numpy as np
+
+from oracle import block_oracle as B
+
+LOG2E = np.float32(1.4426950408889634)
+
+
+def exact_scale(k: int, had: int) -> float:
+    """A scale whose product with log2(e) (over 32 for a transformed cache) is 2^-k."""
+    return float(np.float32(2.0 ** -k * (32.0 if had else 1.0) / float(LOG2E)))
+
+
+def whole_queries(rng, tokens: int, heads: int, dim: int, most: int = 2) -> np.ndarray:
+    return rng.integers(-most, most + 1, (tokens, heads, dim)).astype(np.float32)
+
+
+def gathered(arr, table_row, n: int):
+    """fp64 keys and values [hk][n][Dp] of one sequence, and which of them are in the cache."""
+    kc, ks, vc, vs = (arr[x] for x in ("k_codes", "k_scales", "v_codes", "v_scales"))
+    ps, j = kc.shape[2], np.arange(n)
+    page = np.asarray(table_row)[j // ps] if n else np.zeros(0, int)
+    there = (page >= 0) & (page < kc.shape[0])
+    page = np.where(there, page, 0)
+    k = B.mx_values(kc[page, :, j % ps], ks[page, :, j % ps]).transpose(1, 0, 2)
+    v = B.mx_values(vc[page, :, j % ps], vs[page, :, j % ps]).transpose(1, 0, 2)
+    return k, v, there
+
+
+def scores(q, k, scale: float, had: int):
+    """fp64 scores in base e of q [..][D] with k [n][Dp], and their absolute sums."""
+    x = B.padded(np.asarray(q, np.float64))
+    if had:
+        x = B.hadamard_blocks(x)
+    c = scale / (32.0 if had else 1.0)
+    return x @ k.T * c, np.abs(x) @ np.abs(k).T * abs(c)
+
+
+def joined(w, v, had: int, dim: int):
+    """Outputs [rows][dim] of weights [rows][n] that add up to one."""
+    o = w @ v
+    return B.unrotated(o, had)[:, :dim]
+
+
+def want(q, arr, table, lens, cu, scale: float, causal: bool, dim: int, had: int):
+    """fp64 out [T][hq][dim], lse [T][hq] and the bounds of their errors."""
+    T, hq, _ = q.shape
+    hk = arr["k_codes"].shape[1]
+    group = hq // hk
+    out, room = np.zeros((T, hq, dim)), np.zeros((T, hq, dim))
+    lse, lroom = np.full((T, hq), -np.inf), np.zeros((T, hq))
+    for b in range(len(lens)):
+        n, ln = int(cu[b + 1] - cu[b]), int(lens[b])
+        if n == 0 or ln == 0:
+            continue
+        ks, vs, there = gathered(arr, table[b], ln)
+        for h in range(hk):
+            k, v = ks[h], vs[h]
+            rows = q[cu[b]:cu[b + 1], h * group:(h + 1) * group].reshape(n * group, -1)
+            s, spread = scores(rows, k, scale, had)
+            i = np.arange(n).repeat(group)
+            seen = there[None] & ((np.arange(ln)[None] <= (ln - n + i)[:, None]) | (not causal))
+            k0 = seen.sum(1)
+            s = np.where(seen, s, -np.inf)
+            m = s.max(1, keepdims=True)
+            m[np.isinf(m)] = 0.0
+            p = np.exp(s - m)
+            l = p.sum(1, keepdims=True)
+            p = np.divide(p, l, out=np.zeros_like(p), where=l > 0)
+            o = p @ v
+            eps = 2.0 ** -8 + 2.0 ** -20 + np.expm1((np.where(seen, spread, 0) * 2.0 ** -20).max(1))
+            off = np.empty_like(o)
+            for r in range(len(o)):       # sum_j p_j |v_j - o|
+                off[r] = p[r] @ np.abs(v - o[r])
+            e = off * eps[:, None] * 1.01 + (p @ np.abs(v)) * ((k0 + 64) * 2.0 ** -22)[:, None]
+            if had:
+                e = np.repeat(e.reshape(len(e), -1, 32).sum(2) / 32.0, 32, 1)
+            res = B.unrotated(o, had)[:, :dim]
+            e = e[:, :dim] + np.abs(res) * 2.0 ** -8 + 2.0 ** -134
+            at = slice(cu[b], cu[b + 1]), slice(h * group, (h + 1) * group)
+            out[at], room[at] = res.reshape(n, group, dim), e.reshape(n, group, dim)
+            with np.errstate(divide="ignore"):
+                ls = np.where(l[:, 0] > 0, m[:, 0] + np.log(l[:, 0]), -np.inf)
+            lr = eps * 1.01 + (k0 + 64) * 2.0 ** -22 + np.abs(np.where(k0 > 0, ls, 0)) * 2.0 ** -21
+            lse[at], lroom[at] = ls.reshape(n, group), lr.reshape(n, group)
+    return out, lse, room, lroom
+
+
+def outside(got, ref, room) -> float:
+    """The share of elements that are farther from the reference than their room."""
+    with np.errstate(invalid="ignore"):
+        bad = ~(np.abs(got - ref) <= room) & ~((got == ref) & np.isinf(ref))
+    return float(bad.mean())
+
+
+def check(out, lse, w) -> None:
+    ref, rlse, room, lroom = w
+    assert outside(out, ref, room) == 0.0, (outside(out, ref, room), np.nanmax(np.abs(out - ref)))
+    assert outside(lse, rlse, lroom) == 0.0, (outside(lse, rlse, lroom), lse.ravel()[:8], rlse.ravel()[:8])
+    assert math.isfinite(float(np.abs(ref).max()))

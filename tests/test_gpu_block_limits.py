@@ -1,8 +1,10 @@
 """The cache, the attention and the norms at the far ends of what their entry points accept:
 counts near 2^31, grids past 2^32 threads, bounds far beyond the lengths."""
+import numpy as np
 import pytest
 import torch
 
+from tests import attention_check as A
 import timestep_adaptive_bit_amd as T
 
 pytestmark = pytest.mark.gpu
@@ -103,3 +105,54 @@ def test_attention_of_more_workgroups_than_one_launch(ctx):
     cu = torch.arange(0, n * len(some) + 1, n, dtype=torch.int32, device=DEV)
     want = ctx.kv_attention(cache, q, cu, table[:3].contiguous(), lens[some].to(DEV), n, 16)
     assert torch.equal(out, want) and not bool((out == 9).any())
+
+
+@pytest.mark.parametrize("rows", [1, 16, 17, 140])
+@pytest.mark.parametrize("most", [(1 << 31) - 1, (1 << 31) - 63, (1 << 31) - 64, 1 << 30])
+def test_a_bound_far_beyond_the_lengths(ctx, rows, most):
+    """max_kv near 2^31 (a table of 2048 pages of 2^20 holds it) with some keys: all are seen."""
+    D, ps = 8, 1 << 20
+    rng = np.random.default_rng(3)
+    cache = _one_page(1, D, 5, page=ps)
+    cache.v_scales[:, :, 30000:] = 129            # later values are larger, and none is negative:
+    cache.v_codes.bitwise_and_(0x77)              # what is left out shows
+    for n in (1, 64, 40000):
+        print("attention", rows, "rows", n, "keys, bound", most, flush=True)
+        q = A.whole_queries(rng, rows, 1, D)
+        arr = {x: getattr(cache, x)[:, :, :n].contiguous().cpu().numpy()
+               for x in ("k_codes", "k_scales", "v_codes", "v_scales")}
+        scale = A.exact_scale(3, 0)
+        w = A.want(q, arr, np.zeros((1, 1), int), [n], [0, rows], scale, False, D, 0)
+        lse = torch.empty(rows, 1, device=DEV)
+        i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)      # noqa: E731
+        out = ctx.kv_attention(cache, torch.from_numpy(q).bfloat16().to(DEV), i32(0, rows),
+                               torch.zeros((1, 2048), dtype=torch.int32, device=DEV), i32(n), rows, most,
+                               scale=scale, lse=lse)
+        A.check(out.double().cpu().numpy(), lse.double().cpu().numpy(), w)
+
+
+@pytest.mark.parametrize("rows", [1, 17])
+def test_as_many_keys_as_an_int_counts(ctx, rows):
+    """2^31 - 1 keys: one page of 2^20 keys 2048 times (but for the last), so the softmax is that of
+    the page, and the sum 2048 times its."""
+    D, ps, n = 8, 1 << 20, (1 << 31) - 1
+    print("attention", rows, "rows", n, "keys", flush=True)
+    rng = np.random.default_rng(4)
+    cache = _one_page(1, D, 6, page=ps)
+    cache.v_scales[:, :, ps // 2:] = 129
+    cache.v_codes.bitwise_and_(0x77)
+    q = A.whole_queries(rng, rows, 1, D)
+    arr = {x: getattr(cache, x).cpu().numpy() for x in ("k_codes", "k_scales", "v_codes", "v_scales")}
+    scale = A.exact_scale(3, 0)
+    ref, rlse, room, lroom = A.want(q, arr, np.zeros((1, 1), int), [ps], [0, rows], scale, False, D, 0)
+    lse = torch.empty(rows, 1, device=DEV)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)      # noqa: E731
+    out = ctx.kv_attention(cache, torch.from_numpy(q).bfloat16().to(DEV), i32(0, rows),
+                           torch.zeros((1, 2048), dtype=torch.int32, device=DEV), i32(n), rows, n,
+                           scale=scale, lse=lse)
+    # the page's room has 2^-22 for each of its 2^20 keys: a quarter.  A lane's sum has at most 2^19
+    # tiles of a rounding of 2^-24; a sum of values has some roundings a tile of either sign.  A lost
+    # half of the keys moves lse by log 2
+    assert A.outside(out.double().cpu().numpy(), ref, room) == 0.0
+    assert A.outside(lse.double().cpu().numpy(), rlse + np.log(2048.0), lroom) == 0.0
+    assert bool((np.abs(ref[..., :D]) > room).all())       # zeros would not pass

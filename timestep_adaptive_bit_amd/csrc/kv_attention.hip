@@ -204,11 +204,16 @@ __device__ __forceinline__ void q_terms(float (&x)[32], bool ok, v8i (&q)[3], ui
   }
 }
 
+// Tiles of n keys, and the first n = TILE t keys cut at len: n and TILE t may be within TILE of
+// 2^31, or 2^31 itself.
+__device__ __forceinline__ int tiles_of(int n) { return (int)(((unsigned)n + (TILE - 1)) / TILE); }
+__device__ __forceinline__ int keys_to(int t, int len) { return (int)min((unsigned)t * TILE, (unsigned)len); }
+
 // The range of tiles [t0, t1) of split `sp`, of `tiles` tiles in all.  A sequence has as
 // many splits as its length needs at the share of the longest one there may be, alike in
 // length: the workgroups of a ragged batch cost about the same.
 __device__ __forceinline__ void split_range(const KvAttnArgs& a, int tiles, int sp, int& t0, int& t1) {
-  const int most = (a.max_kv + TILE - 1) / TILE, share = max((most + a.splits - 1) / a.splits, 1);
+  const int most = tiles_of(a.max_kv), share = max((most + a.splits - 1) / a.splits, 1);
   const int parts = max((tiles + share - 1) / share, 1), per = (tiles + parts - 1) / parts;
   t0 = min(sp * per, tiles);
   t1 = min(t0 + per, tiles);
@@ -284,7 +289,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   const int seen = row_ok ? seen_keys(a, len, n, qi) : seen_hi;     // idle rows hide nothing
 
   int t0, t1;
-  split_range(a, (seen_hi + TILE - 1) / TILE, sp, t0, t1);
+  split_range(a, tiles_of(seen_hi), sp, t0, t1);
   if (a.splits > 1 && t0 >= t1) {
     if (threadIdx.x < 16 && row_ok)
       *part_stats(a, sp, (long long)(q0 + qi) * a.q_heads + qh) = make_float2(kNegInf, 0.0f);
@@ -303,7 +308,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   // Lane: the page of key group lane % 4 of tile t, -1 past the keys.
   int page;
   auto pages = [&](int t) {
-    const int j = t * TILE + 16 * (lane & 3);
+    const int j = (int)((unsigned)t * TILE + 16 * (lane & 3));     // (t may be past the range)
     page = t < w1 && j < len ? table[min(j >> c.page_shift, a.table_stride - 1)] : -1;
   };
   // Codes and scales of tile t.  Where a group has no page, or a key lies past the end, some
@@ -331,7 +336,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   // depends on the sequence's bounds alone (pages, positions, query rows), then the table
   // rows and the first tile, which arrives while the queries are turned.
   pages(w0);
-  const int hole0 = (w0 * TILE) >> c.page_shift, hole1 = min(((min(w1 * TILE, len) - 1) >> c.page_shift) + 1, a.table_stride);
+  const int hole0 = (int)((unsigned)w0 * TILE >> c.page_shift), hole1 = min(((keys_to(w1, len) - 1) >> c.page_shift) + 1, a.table_stride);
   const int probe = hole0 + lane < hole1 ? table[hole0 + lane] : 0;
   // q': eight elements a thread, through LDS to the B operand (row l%16, block l/16)
   float* qs = reinterpret_cast<float*>(smem);
@@ -427,7 +432,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   for (int t = w0; t < w1; ++t) {
     const int j0 = t * TILE;
     v4f s[4];
-    if (j0 + TILE > len || holes) {                  // values of rows that were not asked for: zeros
+    if (len - j0 < TILE || holes) {                  // values of rows that were not asked for: zeros
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int j = j0 + 16 * k, pi = j >> c.page_shift;
@@ -461,7 +466,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
       s[k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ka, q[2], s[k], 4, 2, 0, kw, 2, (int)q_scales);
     }
     // lane: keys 16 k + 4 g + r of its row
-    if (j0 + TILE > seen_lo || holes) {
+    if (seen_lo - j0 < TILE || holes) {
       const int left = seen - j0 - 4 * g;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -705,7 +710,7 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   const int seen_hi = first < rows ? seen_keys(a, len, n, min(first + 31, rows - 1) / a.group) : 0;
 
   int t0, t1;
-  split_range(a, (seen_all + TILE - 1) / TILE, sp, t0, t1);
+  split_range(a, tiles_of(seen_all), sp, t0, t1);
   const long long out_row = (long long)(q0 + qi) * a.q_heads + qh;
   if (a.splits > 1 && t0 >= t1) {
     if (half == 0 && row_ok) *part_stats(a, sp, out_row) = make_float2(kNegInf, 0.0f);
@@ -790,7 +795,7 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   };
   // Whether a page of the range is not in the cache: its keys are then hidden tile by tile.
   bool holes = false;
-  for (int i = (t0 * TILE >> c.page_shift) + lane; i < a.table_stride && i <= (min(t1 * TILE, len) - 1) >> c.page_shift; i += 64)
+  for (int i = (int)((unsigned)t0 * TILE >> c.page_shift) + lane; i < a.table_stride && i <= (keys_to(t1, len) - 1) >> c.page_shift; i += 64)
     holes = holes || (unsigned)table[i] >= (unsigned)c.num_pages;
   holes = __any(holes);
   // 16-byte block `blk` of key row `key`: rows share a 256-byte bank window, the XOR
@@ -952,7 +957,7 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     if (work) {
       v16f sc[2];
       scores(s, sc);
-      if (j0 + TILE > seen_lo || holes) {
+      if (seen_lo - j0 < TILE || holes) {
         const int left = seen - j0 - half * 4;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
