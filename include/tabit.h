@@ -581,7 +581,8 @@ int tabit_kv_read(tabit_ctx* ctx, const tabit_kv_cache* cache, const int64_t* sl
  *                elements (multiple of 8), 16-byte aligned
  *   cu_q         device int32 [num_seqs + 1]: sequence b's rows are
  *                [cu_q[b], cu_q[b+1]) of q and out, at most max_q of them (further
- *                ones are not computed); rows of no sequence are left as they are
+ *                ones count for the mask but are not computed); rows of no sequence
+ *                are left as they are
  *   block_table  device int32 [num_seqs][table_stride] page numbers; tokens of a
  *                page outside the cache are not seen
  *   kv_lens      device int32 [num_seqs], taken as at most max_kv

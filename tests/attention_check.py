@@ -33,6 +33,28 @@ def whole_queries(rng, tokens: int, heads: int, dim: int, most: int = 2) -> np.n
     return rng.integers(-most, most + 1, (tokens, heads, dim)).astype(np.float32)
 
 
+def problem(seed: int, lens, qs, hq: int, hk: int, dim: int, ps: int, had: int, k: int = 3, most: int = 2,
+            causal: bool = True) -> dict:
+    """Keys and values of a normal distribution in pages of any order, whole queries, scale 2^-k."""
+    rng = np.random.default_rng(seed)
+    need = [(n + ps - 1) // ps for n in lens]
+    table = np.full((len(lens), max(need + [1])), -1, np.int32)
+    order, at = rng.permutation(sum(need) + 2), 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    x = rng.standard_normal((2, len(order) * ps, hk, dim)).astype(np.float32)
+    arr = {}
+    for name, y in zip("kv", x):
+        codes, scales = B.mx_rows(y, had)
+        for part, z in (("codes", codes), ("scales", scales)):
+            arr[f"{name}_{part}"] = np.ascontiguousarray(
+                z.reshape(len(order), ps, hk, -1).transpose(0, 2, 1, 3))
+    cu = np.concatenate([[0], np.cumsum(qs)]).astype(np.int32)
+    return dict(arr=arr, table=table, lens=list(lens), cu=cu, q=whole_queries(rng, int(cu[-1]), hq, dim, most),
+                scale=exact_scale(k, had), causal=causal, D=dim, had=had)
+
+
 def gathered(arr, table_row, n: int):
     """fp64 keys and values [hk][n][Dp] of one sequence, and which of them are in the cache."""
     kc, ks, vc, vs = (arr[x] for x in ("k_codes", "k_scales", "v_codes", "v_scales"))

@@ -230,19 +230,21 @@ __device__ __forceinline__ float2* part_stats(const KvAttnArgs& a, int sp, long 
   return reinterpret_cast<float2*>(a.part + (long long)a.splits * rows * a.cache.dim_pad) + sp * rows + row;
 }
 
-// First query row and number of queries of sequence b, inside [0, tokens].
-__device__ __forceinline__ void seq_rows(const KvAttnArgs& a, int b, int& q0, int& n) {
+// First query row of sequence b, its queries, inside [0, tokens], and how many of them are
+// computed.
+__device__ __forceinline__ void seq_rows(const KvAttnArgs& a, int b, int& q0, int& all, int& n) {
   q0 = min(max(a.cu_q[b], 0), a.tokens);
-  n = min(max(a.cu_q[b + 1] - q0, 0), min(a.max_q, a.tokens - q0));
+  all = max(min(a.cu_q[b + 1], a.tokens) - q0, 0);
+  n = min(all, a.max_q);
 }
 
 __device__ __forceinline__ int seq_keys(const KvAttnArgs& a, int b) {
   return min(max(a.kv_lens[b], 0), a.max_kv);
 }
 
-// Keys that query i of n sees, of `len`.
-__device__ __forceinline__ int seen_keys(const KvAttnArgs& a, int len, int n, int i) {
-  return a.causal ? min(max(len - n + i + 1, 0), len) : len;
+// Keys that query i of `all` sees, of `len`.
+__device__ __forceinline__ int seen_keys(const KvAttnArgs& a, int len, int all, int i) {
+  return a.causal ? min(max(len - all + i + 1, 0), len) : len;
 }
 
 // One workgroup: 16 rows (queries x heads of the group) of one key head of one
@@ -277,16 +279,16 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   const int sp = blockIdx.x % a.splits, row_tile = blockIdx.x / a.splits;
   const KvCacheArgs& c = a.cache;
 
-  int q0, n;
-  seq_rows(a, b, q0, n);
+  int q0, all, n;
+  seq_rows(a, b, q0, all, n);
   const int r0 = row_tile * 16;
   if (r0 >= n * a.group) return;
   const int len = seq_keys(a, b);
   const int qi = (r0 + row) / a.group, qh = hk * a.group + (r0 + row) % a.group;
   const bool row_ok = qi < n;
   const int last = (min(r0 + 16, n * a.group) - 1) / a.group;
-  const int seen_hi = seen_keys(a, len, n, last), seen_lo = seen_keys(a, len, n, r0 / a.group);
-  const int seen = row_ok ? seen_keys(a, len, n, qi) : seen_hi;     // idle rows hide nothing
+  const int seen_hi = seen_keys(a, len, all, last), seen_lo = seen_keys(a, len, all, r0 / a.group);
+  const int seen = row_ok ? seen_keys(a, len, all, qi) : seen_hi;     // idle rows hide nothing
 
   int t0, t1;
   split_range(a, tiles_of(seen_hi), sp, t0, t1);
@@ -692,8 +694,8 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   const int sp = at_y % a.splits, row_tile = at_y / a.splits;
   const KvCacheArgs& c = a.cache;
 
-  int q0, n;
-  seq_rows(a, b, q0, n);
+  int q0, all, n;
+  seq_rows(a, b, q0, all, n);
   const int rows = n * a.group;
   // the last rows of a causal sequence see most: they start first
   const int tiles_r = (rows + ROWS - 1) / ROWS;
@@ -703,11 +705,11 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   const int rr = r0 + wave * 32 + row;
   const bool row_ok = rr < rows;
   const int qi = rr / a.group, qh = hk * a.group + rr % a.group;
-  const int seen_all = seen_keys(a, len, n, (min(r0 + ROWS, rows) - 1) / a.group);
-  const int seen = row_ok ? seen_keys(a, len, n, qi) : seen_all;   // idle rows mask nothing
+  const int seen_all = seen_keys(a, len, all, (min(r0 + ROWS, rows) - 1) / a.group);
+  const int seen = row_ok ? seen_keys(a, len, all, qi) : seen_all;   // idle rows mask nothing
   const int first = r0 + wave * 32;
-  const int seen_lo = seen_keys(a, len, n, min(first, rows - 1) / a.group);
-  const int seen_hi = first < rows ? seen_keys(a, len, n, min(first + 31, rows - 1) / a.group) : 0;
+  const int seen_lo = seen_keys(a, len, all, min(first, rows - 1) / a.group);
+  const int seen_hi = first < rows ? seen_keys(a, len, all, min(first + 31, rows - 1) / a.group) : 0;
 
   int t0, t1;
   split_range(a, tiles_of(seen_all), sp, t0, t1);
@@ -1080,8 +1082,8 @@ kv_attention_join_kernel(KvAttnArgs a) {
   __shared__ float part[WIDE ? GROUPS : 1][DP], weight[WIDE ? 256 : 1], stats[8];
   static_assert(kMaxSplits <= 256, "one thread a split");
   const int b = blockIdx.y;
-  int q0, n;
-  seq_rows(a, b, q0, n);
+  int q0, all, n;
+  seq_rows(a, b, q0, all, n);
   const int gr = threadIdx.x / LPR, li = threadIdx.x % LPR, lane = threadIdx.x & 63;
   const int r = WIDE ? blockIdx.x : blockIdx.x * GROUPS + gr;
   if (WIDE && r >= n * a.q_heads) return;
