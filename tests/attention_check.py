@@ -138,3 +138,35 @@ def check(out, lse, w) -> None:
     assert outside(out, ref, room) == 0.0, (outside(out, ref, room), np.nanmax(np.abs(out - ref)))
     assert outside(lse, rlse, lroom) == 0.0, (outside(lse, rlse, lroom), lse.ravel()[:8], rlse.ravel()[:8])
     assert math.isfinite(float(np.abs(ref).max()))
+
+
+def steep_problem(seed: int, n: int, rows: int, heads: int, dim: int, had: int, v_bytes, top: int = 36,
+                  noise: int = 124, causal: bool = False, ps: int = 16) -> dict:
+    """Scores (base 2) of +top in even rows and -top in odd ones and, where there is more than one
+    block, a few tenths beside: the first block of each key is one code of 6 that a query of 3 (or
+    1.5 in every element, for a transformed cache) meets.  v_bytes(rng, shape): the values' scale
+    bytes [pages][heads][ps][blocks].  top is 36 times a power of two."""
+    rng = np.random.default_rng(seed)
+    dp = (dim + 31) // 32 * 32
+    pages = max((n + ps - 1) // ps, 1)
+    nib = lambda w: rng.integers(0, 256, (pages, heads, ps, w), dtype=np.uint8)    # noqa: E731
+    kc, vc = nib(dp // 2), nib(dp // 2)
+    vc = (vc & 0x77) | (rng.integers(0, 256, dp // 2, dtype=np.uint8) & 0x88)   # a sign for each element:
+    for c in (kc, vc):                                                          # sums of many stay large
+        if not had and dim % 32:
+            c[..., dim // 2:] = 0
+    kc[..., :16] = 0
+    kc[..., 0] = 7                                     # E2M1 code of 6, the other elements 0
+    ks = np.full((pages, heads, ps, dp // 32), noise, np.uint8)
+    ks[..., 0] = 127 + 4 + round(math.log2(top / 36))
+    vs = v_bytes(rng, (pages, heads, ps, dp // 32)).astype(np.uint8)
+    q = rng.integers(-1, 2, (rows, heads, dim)).astype(np.float32)
+    sign = (1.0 - 2.0 * (np.arange(rows) % 2))[:, None, None]
+    q[..., :32] = 0.0
+    if had:
+        q[..., :32] = 1.5 * sign
+    else:
+        q[..., :1] = 3.0 * sign
+    return dict(arr=dict(k_codes=kc, k_scales=ks, v_codes=vc, v_scales=vs),
+                table=rng.permutation(pages).astype(np.int32)[None], lens=[n], cu=np.array([0, rows], np.int32),
+                q=q, scale=exact_scale(7 if had else 3, had), causal=causal, D=dim, had=had)

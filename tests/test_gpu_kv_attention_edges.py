@@ -49,3 +49,61 @@ def test_rows_past_max_q_keep_the_mask(ctx, hq, hk, D, had):
         done = in_seq < m
         A.check(got[done], glse[done], (out[done], lse[done], room[done], lroom[done]))
         assert (got[~done] == 9).all() and (glse[~done] == 7).all()
+
+
+def _bytes(kind, b):
+    """Scale bytes of the values: all b; b in some keys; b in one key; b in the last block alone."""
+    def make(rng, shape):
+        x = rng.integers(125, 130, shape)
+        if kind == "all":
+            x[...] = b
+        elif kind == "some":
+            x[rng.random(shape[:3]) < 0.1] = b
+        elif kind == "one":
+            x[shape[0] // 2, :, 3] = b
+        else:
+            x[..., -1] = b
+        return x
+    return make
+
+
+@pytest.mark.parametrize("rows,heads,D", [(1, 2, 128), (16, 1, 64), (20, 2, 64), (140, 1, 128), (1, 3, 32),
+                                          (33, 1, 96)])
+@pytest.mark.parametrize("had", [0, 32])
+@pytest.mark.parametrize("kind", ["all", "some", "one", "block"])
+def test_values_of_any_finite_size(ctx, rows, heads, D, had, kind):
+    """Scores of about +-36 (base 2), where the weights need no reference, with values from 2^-126 to
+    2^127: the result is finite and as exact as that of ordinary values."""
+    for n in (1, 5, 64, 300, 2000):
+        for b in (1, 30, 60, 66, 67, 90, 177, 178, 210, 245, 252):
+            print("attention rows", rows, "heads", heads, "D", D, "had", had, kind, b, "keys", n, flush=True)
+            p = A.steep_problem(n + b, n, rows, heads, D, had, _bytes(kind, b))
+            w = _want(p)
+            A.check(*_run(ctx, p), w)
+            some = w[0] != 0
+            assert A.outside(0.0, w[0][some], w[2][some]) > 0.6          # zeros would not pass
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_far_values_do_not_reach_rows_that_do_not_see_them(ctx, D):
+    """Causal rows before a key of a far value are the same bits as with an ordinary one."""
+    for rows, n in ((40, 60), (8, 30), (150, 400)):
+        for b in (20, 240):
+            p = A.steep_problem(rows, n, rows, 2, D, 32, _bytes("all", 127), causal=True)
+            a = _run(ctx, p)
+            j = n - rows // 2                       # seen by rows // 2 rows
+            p["arr"]["v_scales"][p["table"][0, j // 16], :, j % 16, 1] = b
+            c = _run(ctx, p)
+            w = _want(p)
+            A.check(*c, w)
+            before = rows - rows // 2
+            assert np.array_equal(a[0][:before], c[0][:before]) and np.array_equal(a[1][:before], c[1][:before])
+
+
+def test_far_values_same_bits_every_time(ctx):
+    for rows in (1, 70):
+        p = A.steep_problem(3, 3000, rows, 2, 64, 32, _bytes("some", 230))
+        a = _run(ctx, p)
+        for _ in range(5):
+            b = _run(ctx, p)
+            assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])

@@ -23,7 +23,10 @@
 //           neither over- nor underflows gives the same relative precision, so it is 0
 //           until a row's first visible tile has a largest score beyond +-40 or a tile's
 //           weights pass 2^40; then it is raised to the largest score, and what is
-//           summed so far is scaled by 2^(old - new).
+//           summed so far is scaled by 2^(old - new).  Weights of 2^-40 to 2^40 times
+//           values could leave fp32 where the result does not, so in a row that sees a
+//           value scale far from one (kFarLow, kFarHigh) the reference follows what the
+//           row has seen: its largest score, or the logarithm of its sum.
 //   values  O^T += V^T P^T with the 16x16x32 bf16 MFMA.  The order of the summed
 //           keys is free, so it is chosen as the lanes already hold them: P needs
 //           no exchange, only its rounding to bf16 (2^-9 a weight; sums stay in fp32).  V becomes bf16 exactly (a code has 2 bits) through LDS, and is
@@ -45,12 +48,36 @@ typedef __attribute__((address_space(3))) v4s* lds_v4s;
 
 constexpr float kNegInf = -__builtin_inff();
 constexpr uint32_t kMaxValueScale = 252;   // 6 * 2^(252 - 127) is the largest finite value
+// Value scales up to 2^50: sums of weights to 2^67 (2^40 in each of 2^27 tiles), 2^3 for a code
+// and 2^5 for the transform stay below 2^128.  From 2^-60 on: the largest weight, 2^-40 or more,
+// times half of it is far above 2^-126, so a row's sums keep their bits.
+constexpr uint32_t kFarLow = 67, kFarHigh = 177;
+// A row with a value scale beyond them has weights of one at most, or of 2^-16 from a large scale
+// on: 2^16 of them times the largest finite value stay finite.
+constexpr float kFarRoom = 16.0f;
+constexpr int kNever = 0x7FFFFFFF;
 constexpr int TILE = 64;      // keys a wave takes at a time
 constexpr int NUM_CUS = 256;  // MI355X
 constexpr int kMaxSplits = 128;
 constexpr int kNarrow = 8;    // splits that one lane joins by itself
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ bool far_scale(uint32_t s) { return s - kFarLow > kFarHigh - kFarLow; }
+
+// Lowest of 16 keys that has one of a wave's bits (lane % 16: the key).
+__device__ __forceinline__ int lowest_key(unsigned long long m) {
+  m |= m >> 32;
+  m |= m >> 16;
+  return __builtin_ctz((unsigned)m & 0xFFFFu);
+}
+
+// What a part (reference, sum of weights) of a row is taken relative to when parts are joined: the
+// exponent of its sum, so that every part's sum of weights becomes less than one.  A part
+// without keys is (-inf, 0).
+__device__ __forceinline__ float part_top(float ref, float sum) {
+  return ref + (float)__builtin_amdgcn_frexp_expf(sum);
+}
 
 // sum + both bf16 weights of a pair, in fp32.  The rounded weights are summed, not the exact
 // ones: what a row's values are multiplied with then adds up to one, and a row that sees one
@@ -424,7 +451,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   }
   __syncthreads();
 
-  float ref = 0.0f, l = 0.0f;
+  float ref = 0.0f, l = 0.0f, far_room = 0.0f;
   bool fresh = true, any_fresh = true, any_ref = false;      // any: over the wave
   v4f o[ND];
 #pragma unroll
@@ -445,8 +472,10 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
         }
       }
     }
-    // a value scale beyond bf16 (or NaN): the key's scores become NaN, its values zero
-    if (__any(has && max(max(vs[0], vs[1]), max(vs[2], vs[3])) > kMaxValueScale)) {
+    // a value scale beyond bf16 (or NaN): the key's scores become NaN, its values zero; one far from
+    // one: the rows that see the first such key of the tile keep their reference near their scores
+    int far_from = kNever, high_from = kNever;
+    if (__any(has && max(max(vs[0] - kFarLow, vs[1] - kFarLow), max(vs[2] - kFarLow, vs[3] - kFarLow)) > kFarHigh - kFarLow)) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const unsigned long long bad = __ballot(has && vs[k] > kMaxValueScale);
@@ -455,6 +484,10 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
           vs[k] = 127u;
           vc[k] = v4i{0, 0, 0, 0};
         }
+        const unsigned long long far = __ballot(has && far_scale(vs[k]));
+        const unsigned long long high = __ballot(has && vs[k] > kFarHigh);
+        if (far != 0) far_from = min(far_from, j0 + 16 * k + lowest_key(far));
+        if (high != 0) high_from = min(high_from, j0 + 16 * k + lowest_key(high));
       }
     }
 #pragma unroll
@@ -489,7 +522,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
       for (int k = 0; k < 4; ++k) s[k] -= ref;
     }
     for (int pass = 0; pass < 2; ++pass) {
-      if (pass == 1 || (any_fresh && __any(fresh && j0 < seen))) {
+      if (pass == 1 || far_from != kNever || (any_fresh && __any(fresh && j0 < seen))) {
         float top = kNegInf;
         asm volatile("" : "+v"(top));                // (else the compiler takes the maximum of every tile)
 #pragma unroll
@@ -502,7 +535,14 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
         fresh = fresh && !first;
         any_fresh = __any(fresh);
         const bool up = first ? fabsf(top) > 40.0f : over && top > 0.0f;
-        const float by = up ? top : 0.0f;
+        float by = up ? top : 0.0f;
+        if (pass == 0 && far_from != kNever) {
+          float all = l + __shfl_xor(l, 16, 64);
+          all += __shfl_xor(all, 32, 64);
+          const float m = fmaxf(top, __builtin_amdgcn_logf(all));
+          far_room = seen > high_from ? kFarRoom : far_room;
+          if (seen > far_from && m > kNegInf) by = m + far_room;
+        }
         ref += by;
         any_ref = __any(ref != 0.0f);
         if (__any(by != 0.0f)) {
@@ -588,7 +628,8 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   if (fi >= n) return;
   float M = kNegInf;
 #pragma unroll
-  for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * 16 + fr) * 2]);
+  for (int w = 0; w < NW; ++w) M = fmaxf(M, part_top(ml[(w * 16 + fr) * 2], ml[(w * 16 + fr) * 2 + 1]));
+  M += 2.0f;                                          // four sums: less than one together
   const float base = M == kNegInf ? 0.0f : M;
   float x[32], L = 0.0f;
 #pragma unroll
@@ -614,14 +655,16 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
     return;
   }
   const float inv = L == 0.0f ? 0.0f : (c.had ? 0.03125f : 1.0f) / L;   // no visible key: 0
+#pragma unroll
+  for (int e = 0; e < 32; ++e) x[e] *= inv;          // (first: the transform adds 32 of them)
   if (c.had) fwht32_lane(x);
 #pragma unroll
   for (int e = 0; e < 32; e += 8) {
     const int d = fb * 32 + e;
     if (d < c.head_dim)
       *reinterpret_cast<uint4*>(a.out + out_row * c.head_dim + d) =
-          make_uint4(pack_bf16(x[e] * inv, x[e + 1] * inv), pack_bf16(x[e + 2] * inv, x[e + 3] * inv),
-                     pack_bf16(x[e + 4] * inv, x[e + 5] * inv), pack_bf16(x[e + 6] * inv, x[e + 7] * inv));
+          make_uint4(pack_bf16(x[e], x[e + 1]), pack_bf16(x[e + 2], x[e + 3]),
+                     pack_bf16(x[e + 4], x[e + 5]), pack_bf16(x[e + 6], x[e + 7]));
   }
   if (a.lse != nullptr && fb == 0)
     a.lse[out_row] = L == 0.0f ? kNegInf : (M + __builtin_log2f(L)) * 0.6931471805599453f;
@@ -682,9 +725,15 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   struct Stage {
     uint8_t v[TILE * RS];
     uint8_t k[KB];
-    uint8_t ks[2][32][4];                            // [block % 2][key % 32][key / 32 * 2 + block / 2]
+    // [block % 2][key % 32]: scale bytes of [key / 32 * 2 + block / 2], then as many marks of keys
+    // (of this tile or an earlier one of the stage) whose value scale is far from one
+    uint8_t ks[2][32][8];
   };
   __shared__ __attribute__((aligned(1024))) Stage st[2];
+  // by stage: the first key so far whose value scale is far from one, and that is far above it.
+  // Like the stage's marks written before the barrier that hands a tile over and read in that tile
+  // alone, so neither depends on timing.
+  __shared__ int2 far_at[2];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = lane & 31, half = lane >> 5;
@@ -818,8 +867,9 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   const int skey = wave * KPW + lkey;
   // A value scale beyond bf16 (or NaN): the key's scores become NaN and its values zero,
   // so that rows that do not see the key (weight 0) are not touched by it.
-  auto settle = [&]() {
-    if (got >= KPW && !__any(vs > kMaxValueScale)) return;
+  // One far from one is noted for the tile's readers.
+  auto settle = [&](int t) {
+    if (got >= KPW && !__any(far_scale(vs))) return;
     asm volatile("");                                // a branch, not selects in every tile
     if (lkey >= got) {                               // rows that were not asked for
       vs = 127u;
@@ -831,6 +881,12 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
       vs = 127u;
       vc = v4i{0, 0, 0, 0};
     }
+    const unsigned long long far = __ballot(far_scale(vs)), high = __ballot(vs > kFarHigh);
+    const int key = (int)((unsigned)t * TILE) + wave * KPW;
+    if (has_k && ((far >> lkey) & 0x0001000100010001ull) != 0)
+      st[(t - t0) & 1].ks[kblk & 1][skey & 31][4 + (skey >> 5) * 2 + (kblk >> 1)] = 1;
+    if (far != 0 && lane == 0) atomicMin(&far_at[(t - t0) & 1].x, key + lowest_key(far));
+    if (high != 0 && lane == 0) atomicMin(&far_at[(t - t0) & 1].y, key + lowest_key(high));
   };
   auto store_keys = [&](Stage& s) {
     if (has_k) {
@@ -857,8 +913,10 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     for (int w = 0; w < VW; ++w) store_values(s, w);
   };
   // Scores of a tile.  Lane: keys 32 kb + 8 (r / 4) + 4 half + r % 4 of its row.
+  // Returns the lane's marks.
   auto scores = [&](const Stage& s, v16f (&sc)[2]) {
-    const int ksw = *reinterpret_cast<const int*>(s.ks[half][row]);
+    const int2 ks_far = *reinterpret_cast<const int2*>(s.ks[half][row]);
+    const int ksw = ks_far.x;
     sc[0] = sc[1] = v16f{};
 #pragma unroll
     for (int ds = 0; ds < NS; ++ds) {
@@ -874,13 +932,15 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
         for (int kb = 0; kb < 2; ++kb)
           sc[kb] = score_term(x[kb], q[ds][t], sc[kb], kb * 2 + ds, ksw, t, (int)q_scales[ds]);
     }
+    return ks_far.y;
   };
   // Sets the reference of rows that see their first key, raises it to the largest score in
-  // rows that are `over`; the scores, relative to it, move along, and what is summed so far
-  // is to be scaled by alpha (1 in the first pass over a tile, where only fresh rows move).
+  // rows that are `over`, and in a row `far` puts it at its largest score or `least`; the scores,
+  // relative to it, move along, and what is summed so far is to be scaled by alpha.
   float alpha = 1.0f;
   bool any_fresh = true, any_ref = false, any_alpha = false;     // over the wave
-  auto raise = [&](v16f (&sc)[2], bool over) {
+  float far_room = 0.0f;
+  auto raise = [&](v16f (&sc)[2], bool over, bool far, float least) {
     float top = kNegInf;
     asm volatile("" : "+v"(top));    // (else the compiler takes the maximum of every tile)
 #pragma unroll
@@ -893,10 +953,13 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     any_fresh = __any(fresh);
     // 2^s is as exact as 2^(s - ref): a reference is needed only for large scores
     const bool up = first ? fabsf(top) > 40.0f : over && top > 0.0f;
-    const float by = up ? top : 0.0f;
-    alpha = first ? 1.0f : exp2_fast(-by);           // a fresh row's sums are zero
+    float by = up ? top : 0.0f;
+    const float m = fmaxf(top, least);
+    if (far && m > kNegInf) by = m + far_room;
+    const float f = first ? 1.0f : exp2_fast(-by);   // a fresh row's sums are zero
     ref += by;
-    l *= alpha;
+    alpha *= f;
+    l *= f;
     any_ref = __any(ref != 0.0f);
     any_alpha = __any(alpha != 1.0f);
     if (__any(by != 0.0f)) {
@@ -943,12 +1006,11 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
 
   if (t0 < t1) place(t0);
   fetch(t0);
-  if constexpr (NB % 2 != 0) {   // scale bytes of blocks that do not exist: any finite scale
-    for (int i = tid; i < 2 * 64; i += NW * 64)
-      reinterpret_cast<uint32_t*>(st[i / 64].ks)[i % 64] = 0x7F7F7F7Fu;
-    __syncthreads();
-  }
-  settle();
+  if (tid < 2 * 64)              // scale bytes of blocks that do not exist: any finite scale; no marks
+    reinterpret_cast<uint2*>(st[tid / 64].ks)[tid % 64] = make_uint2(0x7F7F7F7Fu, 0u);
+  if (tid < 2) far_at[tid] = make_int2(kNever, kNever);
+  __syncthreads();
+  settle(t0);
   store(st[0]);
   fetch(t0 + 1);
   tile::lds_barrier();
@@ -958,7 +1020,7 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     const bool work = j0 < seen_hi;   // else no row of the wave sees the tile, nor a later one
     if (work) {
       v16f sc[2];
-      scores(s, sc);
+      const bool any_far = __any(scores(s, sc) != 0);
       if (seen_lo - j0 < TILE || holes) {
         const int left = seen - j0 - half * 4;
 #pragma unroll
@@ -981,7 +1043,19 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
       // (rows apart, so that none depends on its neighbours)
       bool over = false;
       for (int pass = 0; pass < 2; ++pass) {
-        if (pass == 1 || (any_fresh && __any(fresh && j0 < seen))) raise(sc, over);
+        if (pass == 1 || (__builtin_expect(any_fresh | any_far, 0) && (any_far || __any(fresh && j0 < seen)))) {
+          float least = kNegInf;         // the logarithm of what a row has summed
+          bool far = false;
+          if (pass == 0 && any_far) {
+            const int2 from = far_at[(t - t0) & 1];
+            if (seen > from.y) far_room = kFarRoom;
+            float tl, th;
+            halves(l, tl, th);
+            least = __builtin_amdgcn_logf(tl + th);
+            far = seen > from.x;
+          }
+          raise(sc, over, far, least);
+        }
         weights(sc);
         const unsigned long long m = __ballot(!(sum < 0x1p40f));
         if (m == 0) break;
@@ -992,13 +1066,14 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
 #pragma unroll
         for (int d = 0; d < ND; ++d) o[d] *= alpha;
         any_alpha = false;
+        alpha = 1.0f;
       }
     }
     // The next tile goes to the other stage, whose readers were done before the last barrier,
     // between this tile's weights and values: the loads have had a tile's time to arrive, the
     // writes have the value products to land.  (One place for both kinds of wave: with two, the
     // loads on their way are waited for where the paths meet.)
-    settle();
+    settle(t + 1);
     store(st[(t + 1 - t0) & 1]);
     if (((t + 2 - t0) & 63) == 0) place(t + 2);
     fetch(t + 2);                // past the range: no loads
@@ -1026,6 +1101,7 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   const float inv = l == 0.0f ? 0.0f : (c.had ? 0.03125f : 1.0f) / l;
 #pragma unroll
   for (int d = 0; d < ND; ++d) {
+    o[d] *= inv;   // (first: the transform adds 32 of them)
     if (c.had) {   // element bits 0, 1 and 3, 4 are register bits, bit 2 is the lane half
 #pragma unroll
       for (int h = 1; h < 16; h <<= 1) {
@@ -1051,7 +1127,7 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     for (int g = 0; g < 4; ++g)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        w[g][e] = pack_bf16(o[d][4 * g + 2 * e] * inv, o[d][4 * g + 2 * e + 1] * inv);
+        w[g][e] = pack_bf16(o[d][4 * g + 2 * e], o[d][4 * g + 2 * e + 1]);
     // runs g and g + 1 of eight elements: the low half ends with run g, the high one with g + 1
 #pragma unroll
     for (int g = 0; g < 4; g += 2) {
@@ -1090,7 +1166,7 @@ kv_attention_join_kernel(KvAttnArgs a) {
   const bool ok = gr < GROUPS && r < n * a.q_heads;
   const KvCacheArgs& c = a.cache;
   const long long row = (long long)q0 * a.q_heads + (ok ? r : 0);
-  float M = kNegInf, L = 0.0f;
+  float M = kNegInf, L = 0.0f, inv = 0.0f;
   v4f x = {0.0f, 0.0f, 0.0f, 0.0f};
   if constexpr (WIDE) {
     // one thread a split: maxima and sums at once, the weights to LDS
@@ -1107,7 +1183,7 @@ kv_attention_join_kernel(KvAttnArgs a) {
       if (ok && gr + k * GROUPS < a.splits)
         y[k] = *reinterpret_cast<const v4f*>(part_sums(a, gr + k * GROUPS, row) + li * 4);
     const bool none = m == kNegInf && w == 0.0f;     // no keys: there are no sums to read
-    M = m;
+    M = part_top(m, w);
 #pragma unroll
     for (int k = 32; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor(M, k, 64));
     if (lane == 0) stats[threadIdx.x >> 6] = M;
@@ -1121,13 +1197,18 @@ kv_attention_join_kernel(KvAttnArgs a) {
     if (lane == 0) stats[4 + (threadIdx.x >> 6)] = w;
     __syncthreads();
     L = (stats[4] + stats[5]) + (stats[6] + stats[7]);
+    inv = L == 0.0f ? 0.0f : (c.had ? 0.03125f : 1.0f) / L;
 #pragma unroll
     for (int k = 0; k < MINE; ++k) {
       const int s = gr + k * GROUPS;
-      if (ok && s < a.splits && !(weight[s] < 0.0f)) x += weight[s] * y[k];
+      if (ok && s < a.splits && !(weight[s] < 0.0f)) x += weight[s] * inv * y[k];
     }
   } else if (ok) {
-    for (int s = 0; s < a.splits; ++s) M = fmaxf(M, part_stats(a, s, row)->x);
+    for (int s = 0; s < a.splits; ++s) {
+      const float2 st = *part_stats(a, s, row);
+      M = fmaxf(M, part_top(st.x, st.y));
+    }
+    M += 3.0f;                                         // up to eight sums: less than one together
     const float base = M == kNegInf ? 0.0f : M;
 #pragma unroll 4
     for (int s = 0; s < a.splits; ++s) {
@@ -1151,6 +1232,11 @@ kv_attention_join_kernel(KvAttnArgs a) {
       }
     }
   }
+  if constexpr (!WIDE) {                   // (first: the transform adds 32 of them)
+    static_assert(kNarrow <= 8, "the room of the narrow form");
+    inv = L == 0.0f ? 0.0f : (c.had ? 0.03125f : 1.0f) / L;
+    x *= inv;
+  }
   if (c.had) {
     float v[4] = {x[0], x[1], x[2], x[3]};
     const float a0 = v[0] + v[1], a1 = v[0] - v[1], a2 = v[2] + v[3], a3 = v[2] - v[3];
@@ -1167,10 +1253,9 @@ kv_attention_join_kernel(KvAttnArgs a) {
     x = v4f{v[0], v[1], v[2], v[3]};
   }
   if (!ok || (WIDE && gr != 0)) return;
-  const float inv = L == 0.0f ? 0.0f : (c.had ? 0.03125f : 1.0f) / L;
   if (li * 4 < c.head_dim)
     *reinterpret_cast<uint2*>(a.out + row * c.head_dim + li * 4) =
-        make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+        make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
   if (a.lse != nullptr && li == 0)
     a.lse[row] = L == 0.0f ? kNegInf : (M + __builtin_log2f(L)) * 0.6931471805599453f;
 }
