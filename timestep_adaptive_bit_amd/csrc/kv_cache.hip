@@ -175,13 +175,13 @@ kv_read_kernel(KvCacheArgs c, int hb_shift, const int64_t* __restrict__ slots, i
     mx_decode(*reinterpret_cast<const uint32_t*>(c.v_codes + at * 16 + gl * 4), c.v_scales[at + (gl >> 2)], b);
   }
   if (c.had) {
-    fwht32_lanes(a, lane);
-    fwht32_lanes(b, lane);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 8; ++e) {      // (first, and exactly: 32 of them could pass fp32)
       a[e] *= 0.03125f;
       b[e] *= 0.03125f;
     }
+    fwht32_lanes(a, lane);
+    fwht32_lanes(b, lane);
   }
   if (e0 >= c.head_dim) return;
   const long long o = ((long long)t * c.heads + h) * c.head_dim + e0;
