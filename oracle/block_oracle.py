@@ -129,6 +129,35 @@ def attention(q: np.ndarray, cache: Dict[str, np.ndarray], table: np.ndarray, le
     return out, lse, weight, spread
 
 
+_E2M3 = np.array([m / 8.0 for m in range(8)] + [(1 + m / 8.0) * 2.0 ** e for e in range(3) for m in range(8)])
+
+
+def e2m3(x: np.ndarray) -> np.ndarray:
+    """x rounded to FP6 E2M3 (0 to 7.5 in steps of 1/8 to 1/2), to nearest even, saturating."""
+    a = np.abs(np.asarray(x, np.float64))
+    hi = np.searchsorted(_E2M3, a).clip(1, len(_E2M3) - 1)
+    lo = hi - 1
+    dl, dh = a - _E2M3[lo], _E2M3[hi] - a
+    up = (dh < dl) | ((dh == dl) & (hi % 2 == 0))
+    return np.copysign(_E2M3[np.where(up, hi, lo)], x)
+
+
+def query_terms(x: np.ndarray):
+    """The three terms of blocks x [..][32] that the attention holds a query as, fp64 [3][..][32]:
+    each E2M3 times 2^e, 2^(e-4), 2^(e-8), e the exponent that puts the block's largest element in
+    [3.75, 7.5) of 2^e."""
+    x = np.asarray(x, np.float64)
+    top = np.abs(x).max(-1, keepdims=True)
+    unit = 2.0 ** np.ceil(np.log2(np.where(top > 0, top, 1.0) / 7.5))
+    unit = np.where(top >= 7.5 * unit, 2 * unit, unit)
+    left, terms = x.copy(), []
+    for t in range(3):
+        u = unit * 2.0 ** (-4 * t)
+        terms.append(e2m3(left / u) * u)
+        left = left - terms[-1]
+    return np.stack(terms)
+
+
 # ------------------------------------------------------------------ norms
 NONE, LAYER, RMS = 0, 1, 2
 

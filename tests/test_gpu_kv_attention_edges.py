@@ -107,3 +107,35 @@ def test_far_values_same_bits_every_time(ctx):
         for _ in range(5):
             b = _run(ctx, p)
             assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("rows", [1, 16, 40])
+@pytest.mark.parametrize("D", [32, 128])
+def test_queries_are_held_to_13_bits(ctx, rows, D):
+    """One key of one code and a score in the hundreds, which lse gives to fp32: an element of the
+    query, times the scale, with a mantissa anywhere, just below a power of two among them, is held
+    to 2^-13 of the largest of its block (and the score to 2^-21 of its absolute sum)."""
+    rng = np.random.default_rng(rows + D)
+    kc = np.zeros((1, 1, 16, D // 2), np.uint8)
+    kc[..., 0], kc[..., -1] = 7, 0x50                     # a code of 6, and one of 3 in the last block
+    ks = np.full((1, 1, 16, D // 32), 127 + 4, np.uint8)
+    arr = dict(k_codes=kc, k_scales=ks, v_codes=kc.copy(), v_scales=np.full_like(ks, 127))
+    mantissas = [1.0, 1.3, 1.87, 1.876, 1.93, 1.938, 1.99, 1.998, 1.9996, 1.99997, 1.9999995]
+    for m in mantissas + list(rng.uniform(1, 2, 8)):
+        scale = float(np.float32(m / float(A.LOG2E)))
+        q = np.zeros((rows, 1, D), np.float32)
+        q[:, 0, 0] = rng.choice([-1.0, 1.0], rows)        # times the scale and log2(e): the mantissa
+        q[:, 0, -1] = rng.choice([-1.0, 1.0, 0.5, 0.375], rows)
+        p = dict(arr=arr, table=np.zeros((1, 1), np.int32), lens=[1], cu=np.array([0, rows], np.int32), q=q,
+                 scale=scale, causal=False, D=D, had=0)
+        _, lse = _run(ctx, p)
+        k, _, _ = A.gathered(arr, [0], 1)
+        s, spread = A.scores(q[:, 0], k[0], scale, 0)
+        top = np.abs(q[:, 0]).reshape(rows, -1, 32).max(2)
+        kmag = np.abs(k[0, 0]).reshape(-1, 32).sum(1)
+        slip = (top * kmag).sum(1) * scale * 2.0 ** -13 + spread[:, 0] * 2.0 ** -21
+        off = np.abs(lse[:, 0] - s[:, 0])
+        # a score within 40 (base 2) has a weight that is rounded to bf16
+        small = np.abs(s[:, 0]) <= 40.5 * np.log(2)
+        assert (off <= slip + np.abs(s[:, 0]) * 2.0 ** -22 + np.where(small, 2.0 ** -8, 0)).all(), (m, off, slip)
+        assert small.mean() < 0.7

@@ -15,9 +15,11 @@
 //           memory into the matrix core as they are stored (lane l holds one MX
 //           block: key l%16, block l/16), scaled by their E8M0 bytes in the
 //           instruction.  q' is three FP6 (E2M3) terms with scales 2^e, 2^(e-4),
-//           2^(e-8) per block of 32: what is left of an element is below 2^-13 of
-//           the block's largest one, less than bf16 would lose, at 3/4 of the
-//           matrix time of one bf16 product.
+//           2^(e-8) per block of 32, e such that the block's largest element is 3.75 to
+//           7.5 of 2^e (7.5 is the largest E2M3): what is left of an element is at most
+//           2^-12 of 2^e, so below 2^-13 of the largest element.  That is less than bf16
+//           loses of elements down to 2^-5 of the largest, and more of smaller ones; it
+//           takes 3/4 of the matrix time of one bf16 product.
 //   softmax every lane holds one row (l%16) and 16 of the 64 keys, in fp32, base 2.
 //           Weights are 2^(s - ref) and their sum runs beside the values'.  Any ref that
 //           neither over- nor underflows gives the same relative precision, so it is 0
@@ -208,7 +210,8 @@ __device__ __forceinline__ void q_terms(float (&x)[32], bool ok, v8i (&q)[3], ui
     odd += x[e + 1];
   }
   ok = ok && finite_f32(top) && even == even && odd == odd;
-  const int ex = max(mx_exponent(top), -119);
+  // the exponent floor(log2 top) - 2, or one more above 7.5 of it: all terms end at 7.5
+  const int ex = max(mx_exponent(__uint_as_float(__float_as_uint(top) + 0x100000u)), -119);
   scales = 0u;
 #pragma unroll
   for (int t = 0; t < 3; ++t) {
