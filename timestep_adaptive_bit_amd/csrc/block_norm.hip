@@ -12,7 +12,8 @@
 // of the centred values, in registers, so a large common mean costs no bits.
 // h leaves as bf16, as INT8 codes with a per-token scale after a block Walsh-
 // Hadamard transform (the codes tabit_hadamard_quant_act defines, of the fp32 h),
-// or as MXFP4.
+// or as MXFP4.  What is not finite stays visible: maxima carry NaN, and a row (MXFP4: a
+// block) whose largest magnitude is NaN or infinite gets zero codes and a scale of NaN.
 //
 // A row is held in registers, eight elements a lane and slot, by a wave (or by a
 // workgroup for long rows); its sums are DPP butterflies (and one value per wave
@@ -39,8 +40,11 @@ using namespace kv;
 // v combined over the 64 lanes, in every lane: inside rows of 16 by DPP (after the
 // first two steps a quad agrees, so the mirrored lane stands for the other one), then
 // row and half exchanges.
+// The larger one, NaN if either is (fmaxf drops it).
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 template <bool MAX>
-__device__ __forceinline__ float both(float a, float b) { return MAX ? fmaxf(a, b) : a + b; }
+__device__ __forceinline__ float both(float a, float b) { return MAX ? larger(a, b) : a + b; }
 
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
@@ -117,7 +121,9 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 }
 
 // INT8 codes of four values: v * r is at most 127 (1 + 2^-24) for the row's largest, so
-// adding 1.5 * 2^23 rounds it to the nearest even whole number in the low byte.
+// adding 1.5 * 2^23 rounds it to the nearest even whole number in the low byte.  r is 0 in a
+// row that is not finite: zeros, and NaNs whose low byte is 0 (they are the hardware's or come
+// from a bf16, whose lower half is 0).
 __device__ __forceinline__ uint32_t i8x4(float a, float b, float c, float d, float r) {
   const uint32_t qa = __float_as_uint(a * r + 12582912.0f), qb = __float_as_uint(b * r + 12582912.0f);
   const uint32_t qc = __float_as_uint(c * r + 12582912.0f), qd = __float_as_uint(d * r + 12582912.0f);
@@ -282,10 +288,11 @@ block_norm_kernel(BlockNormArgs a, int rows_per, int unit0) {
 #pragma unroll
       for (int i = 0; i < S; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][e]));
+        for (int e = 0; e < 8; ++e) top = larger(top, fabsf(x[i][e]));
       top = row_all<TPR, true>(top, buf, par + 4);
-      const float q = top > 0.0f ? 127.0f / top : 0.0f;
-      if (li == 0) static_cast<float*>(a.h_scale)[row] = top / 127.0f;
+      const bool good = finite_f32(top);
+      const float q = good && top > 0.0f ? 127.0f / top : 0.0f;
+      if (li == 0) static_cast<float*>(a.h_scale)[row] = good ? top / 127.0f : __builtin_nanf("");
 #pragma unroll
       for (int i = 0; i < S; ++i) {
         const int ch = i * TPR + li;
@@ -301,16 +308,18 @@ block_norm_kernel(BlockNormArgs a, int rows_per, int unit0) {
       const int ch = i * TPR + li;
       float top = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][e]));
-      top = fmaxf(top, lane_xor<1>(top));
-      top = fmaxf(top, lane_xor<2>(top));
+      for (int e = 0; e < 8; e += 2)   // (as `larger`, which takes 22 registers more here)
+        asm("v_maximum3_f32 %0, %0, |%1|, |%2|" : "+v"(top) : "v"(x[i][e]), "v"(x[i][e + 1]));
+      top = larger(top, lane_xor<1>(top));
+      top = larger(top, lane_xor<2>(top));
+      const bool good = finite_f32(top);
       const int X = mx_exponent(top);
       const float inv = __uint_as_float((uint32_t)(127 - X) << 23);   // 2^-X: X is at most 125
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[i][e] *= inv;
       if (ch < chunks) {
-        reinterpret_cast<uint32_t*>(a.h)[at / 8 + ch] = e2m1x8(x[i]);
-        if ((ch & 3) == 0) static_cast<uint8_t*>(a.h_scale)[at / 32 + (ch >> 2)] = (uint8_t)(X + 127);
+        reinterpret_cast<uint32_t*>(a.h)[at / 8 + ch] = good ? e2m1x8(x[i]) : 0u;
+        if ((ch & 3) == 0) static_cast<uint8_t*>(a.h_scale)[at / 32 + (ch >> 2)] = (uint8_t)(good ? X + 127 : 255);
       }
     }
   }
