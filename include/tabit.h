@@ -644,7 +644,8 @@ enum tabit_norm { TABIT_NORM_NONE = 0, TABIT_NORM_LAYER = 1, TABIT_NORM_RMS = 2 
  *                bf16 [rows][width]; TABIT_FMT_INT8 int8 [rows][width] with h_scale
  *                fp32 [rows]; TABIT_FMT_MXFP4 codes [rows][width/2] with h_scale
  *                uint8 [rows][width/32]: the codes tabit_hadamard_quant_act defines,
- *                of the fp32 h, with its had_block choices.  Inputs need not be finite:
+ *                of the fp32 h, with its had_block choices (rows below 2^-121, where
+ *                127 / max|y| is past fp32, too).  Inputs need not be finite:
  *                an INT8 row whose transformed h holds a NaN or infinity has zero codes
  *                and a scale of NaN, an MXFP4 block zero codes and E8M0 255 (NaN), so
  *                that the products after it answer NaN for that row

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import tabit_oracle as O
 import timestep_adaptive_bit_amd as T
 
 pytestmark = pytest.mark.gpu
@@ -68,3 +69,31 @@ def test_what_is_not_finite_stays_so_in_mxfp4(ctx, H, pre):
         assert not g.view(14, H // 32, 16)[marked].any()
         good = [i for i in range(14) if i not in bad]
         assert torch.equal(h[good], g[good]) and torch.equal(s[good], t[good])
+
+
+@pytest.mark.parametrize("had", [0, 32, 128])
+@pytest.mark.parametrize("e", [80, 93, 94, 115, 120, 121, 126, 130])
+def test_int8_codes_of_very_small_rows(ctx, had, e):
+    """Whole numbers times 2^-e, whose transform is exact: codes are rint(127 y / max|y|) (two fp32
+    roundings of 2^-24 beside a tie) also where 127 / max|y| is past fp32, and nowhere clamped; scales
+    are max|y| / 127 to fp32, whose smallest step is 2^-149."""
+    for H in (128, 1536, 8192, 16384):
+        rng = np.random.default_rng(H + e)
+        c = rng.integers(-50, 51, (5, H)).astype(np.float64)
+        c[1, 1:] = 0
+        c[2] = 0
+        x = torch.from_numpy(np.ldexp(c, -e)).bfloat16().to(DEV)
+        assert np.array_equal(x.double().cpu().numpy(), np.ldexp(c, -e))
+        _, h, s = ctx.block_norm(x, fmt=T.FMT_INT8, had_block=had, want_x=False)
+        y = c
+        if had:
+            y = (c.reshape(5, -1, had) @ O.sylvester_hadamard(had).astype(np.float64)).reshape(5, H)
+        a = np.abs(y).max(1, keepdims=True)
+        v = np.divide(y * 127, a, out=np.zeros_like(y), where=a > 0)
+        code = h.cpu().numpy().astype(np.float64)
+        room = 127 * 2.0 ** -23
+        assert np.all(np.abs(code - v) <= 0.5 + room)
+        sure = np.abs(np.abs(v - np.floor(v)) - 0.5) > room
+        assert np.array_equal(code[sure], np.rint(v)[sure]) and sure.mean() > 0.9
+        want = np.ldexp(a[:, 0] / 127, -e)
+        assert np.all(np.abs(s.double().cpu().numpy() - want) <= want * 2.0 ** -24 + 2.0 ** -150)

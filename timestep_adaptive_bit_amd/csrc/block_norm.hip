@@ -291,8 +291,15 @@ block_norm_kernel(BlockNormArgs a, int rows_per, int unit0) {
         for (int e = 0; e < 8; ++e) top = larger(top, fabsf(x[i][e]));
       top = row_all<TPR, true>(top, buf, par + 4);
       const bool good = finite_f32(top);
-      const float q = good && top > 0.0f ? 127.0f / top : 0.0f;
+      float q = good && top > 0.0f ? 127.0f / top : 0.0f;
       if (li == 0) static_cast<float*>(a.h_scale)[row] = good ? top / 127.0f : __builtin_nanf("");
+      if (q > 0x1p100f) {          // (127 / top would be infinite below 2^-121: both by 2^64, exactly)
+        q = 127.0f / (top * 0x1p64f);
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[i][e] *= 0x1p64f;
+      }
 #pragma unroll
       for (int i = 0; i < S; ++i) {
         const int ch = i * TPR + li;
