@@ -248,7 +248,7 @@ int tabit_block_norm(tabit_ctx* ctx, const tabit_block_norm_args* a, void* strea
   k.scale = a->scale;
   k.shift = a->shift;
   k.mod_stride = mod ? a->mod_stride : 0;
-  k.rows_per_sample = mod ? a->rows_per_sample : 1;
+  k.rows_per_sample = mod ? a->rows_per_sample : a->rows;   // one sample: weights are read once a wave
   k.res_scale = a->res_scale;
   k.eps = a->eps;
   k.x_out = a->x_out;
