@@ -187,9 +187,15 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+# The handle itself, where this torch has that call (it is not a public one): building a Stream
+# object to ask for it takes longer than a small launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device: torch.device) -> int:
-    # the handle itself: building a Stream object to ask for it takes longer than a small launch
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    if _raw_stream is None or device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
 
 
 def _dev(t: torch.Tensor, dtype, name: str, shape=None) -> None:
