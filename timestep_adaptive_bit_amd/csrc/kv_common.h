@@ -180,13 +180,5 @@ __device__ __forceinline__ void turned8(uint4 own, uint4 partner, int e0, const 
   for (int e = 0; e < 8; ++e) v[e] = v[e] * c[e] + o[e] * s[e];
 }
 
-// The same with the elements read at p, a vector of the head.
-__device__ __forceinline__ void load8_turned(const uint16_t* p, int e0, const RopeArgs& rope, int pos,
-                                             float (&v)[8]) {
-  const uint4 own = *reinterpret_cast<const uint4*>(p + e0);
-  const uint4 partner = *reinterpret_cast<const uint4*>(p + turn_partner(e0, rope));
-  turned8(own, partner, e0, rope, pos, v);
-}
-
 }  // namespace kv
 }  // namespace tabit
