@@ -170,3 +170,129 @@ def steep_problem(seed: int, n: int, rows: int, heads: int, dim: int, had: int, 
     return dict(arr=dict(k_codes=kc, k_scales=ks, v_codes=vc, v_scales=vs),
                 table=rng.permutation(pages).astype(np.int32)[None], lens=[n], cu=np.array([0, rows], np.int32),
                 q=q, scale=exact_scale(7 if had else 3, had), causal=causal, D=dim, had=had)
+
+
+# ---------------------------------------------------------------- references that move
+_CODE = {6.0: 7, 4.0: 6, 3.0: 5, 2.0: 4, 1.5: 3, 1.0: 2, 0.5: 1}
+
+
+def _codes_of(target: int):
+    """E2M1 codes of sixteen elements whose values add up to target / 2, a whole number in [-96, 96]."""
+    left, out = abs(target) / 2.0, []
+    for _ in range(16):
+        c = next((c for c in _CODE if c <= left), 0.0)
+        out.append((_CODE[c] if c else 0) | (8 if c and target < 0 else 0))
+        left -= c
+    assert left == 0, target
+    return out
+
+
+CLIMBS = ("late", "straddle", "straddle low", "high", "low", "stairs", "falls", "levels")
+
+
+def climb(kind: str, n: int, rng) -> np.ndarray:
+    """Scores (base 2, whole numbers) of n keys that make a row's reference move between tiles of 64
+    while what was summed before still counts, or has to be scaled away."""
+    j = np.arange(n)
+    part = j / n
+    jitter = rng.integers(-2, 3, n)
+    if kind == "late":         # next to nothing, then 60
+        s = np.where(part < 0.6, 0, 60) + jitter
+    elif kind == "straddle":   # one key of 38 to 43 in each 64: raised past 40, after some that count
+        s = 20 + jitter
+        first = np.arange(0, n, 64)
+        at = np.minimum(first + rng.integers(0, 64, len(first)), n - 1)
+        s[at] = np.array([38, 39, 39, 41, 39, 43, 38])[np.arange(len(first)) % 7]
+    elif kind == "straddle low":   # the same above a first tile of -50: a reference of -46 or so, then -4
+        s = -50 + jitter
+        first = np.arange(0, n, 64)
+        at = np.minimum(first + rng.integers(0, 64, len(first)), n - 1)
+        s[at] = np.array([-46, -9, -8, -8, -5, -4, -46])[np.arange(len(first)) % 7]
+    elif kind == "high":       # a reference of 45 from the start, raised to 90
+        s = np.where(part < 0.5, 43, 88) + jitter
+        s[rng.choice(n // 2, max(n // 50, 2), replace=False)] = 87
+    elif kind == "low":        # -60, then -15, then -14
+        s = np.where(part < 0.4, -60, -16) + jitter
+    elif kind == "stairs":     # up by a few every 64 keys
+        s = -90 + np.minimum(9 * (j // 64), 180) + jitter
+    elif kind == "falls":      # 60 first, then 58 and less: what comes later counts less
+        s = 60 - np.minimum(2 * (j // 64), 60) + jitter
+    else:                      # a level for each 64 keys
+        s = rng.integers(-94, 95, n // 64 + 1)[j // 64] + jitter
+    return s.clip(-96, 96)
+
+
+def climb_problem(seed: int, kind: str, n: int, rows: int, heads: int, dim: int, had: int, copies: int = 1,
+                  ps: int = 16) -> dict:
+    """Keys whose scores are factor * climb(kind), the factor of a row one of +-1, +-1/2, 1/4; values
+    of a sign for each element, the other one after the keys' middle, so that sums of the wrong scale
+    show.  The
+    `heads` heads are repeated `copies` times."""
+    rng = np.random.default_rng(seed)
+    dp = (dim + 31) // 32 * 32
+    pages = (n + ps - 1) // ps
+    kc = np.zeros((pages * ps, heads, dp // 2), np.uint8)
+    vc = rng.integers(0, 128, (pages * ps, heads, dp // 2), dtype=np.uint8) & 0x77
+    vc |= rng.integers(0, 256, dp // 2, dtype=np.uint8) & 0x88
+    vc[n // 2:] ^= 0x88
+    for h in range(heads):
+        t = climb(kind, n, rng)
+        c = np.array([_codes_of(int(x)) for x in t], np.uint8)
+        kc[:n, h, :8] = c[:, 0::2] | c[:, 1::2] << 4
+    if dim % 32 and not had:
+        vc[..., dim // 2:] = 0
+    ks = np.full((pages * ps, heads, dp // 32), 128, np.uint8)           # codes times 2
+    vs = rng.integers(125, 129, (pages * ps, heads, dp // 32)).astype(np.uint8)
+    arr = {m: np.ascontiguousarray(np.tile(x.reshape(pages, ps, heads, -1).transpose(0, 2, 1, 3),
+                                           (1, copies, 1, 1)))
+           for m, x in (("k_codes", kc), ("k_scales", ks), ("v_codes", vc), ("v_scales", vs))}
+    pattern = np.zeros(dim)
+    pattern[:16] = 1.0
+    if had:                                                              # whose transform is the pattern
+        pattern[:32] = B.hadamard_blocks(pattern[None, :32])[0] / 32.0
+    factor = rng.choice([1.0, 1.0, -1.0, 0.5, -0.5, 0.25], (rows, heads))
+    factor[0] = 1.0
+    q = np.tile((factor[..., None] * pattern).astype(np.float32), (1, copies, 1))
+    return dict(arr=arr, table=np.arange(pages, dtype=np.int32)[None], lens=[n],
+                cu=np.array([0, rows], np.int32), q=q, scale=exact_scale(0, had), causal=False, D=dim,
+                had=had, heads=heads)
+
+
+def only_heads(p: dict, heads: int) -> dict:
+    return dict(p, arr={m: np.ascontiguousarray(x[:, :heads]) for m, x in p["arr"].items()},
+                q=np.ascontiguousarray(p["q"][:, :heads]))
+
+
+def summed(s, v, runs: int, mistake: str = ""):
+    """Out of one row by the kernel's rule (reference 0 until a first tile beyond +-40, or weights past
+    2^40), the keys in `runs` runs that are joined, with one mistake planted."""
+    tiles = (len(s) + 63) // 64
+    per = (tiles + runs - 1) // runs
+    parts = []
+    for r in range(runs):
+        ref, l, o, fresh = 0.0, 0.0, np.zeros(v.shape[1]), True
+        for t in range(r * per, min(r * per + per, tiles)):
+            x, y = s[t * 64:t * 64 + 64], v[t * 64:t * 64 + 64]
+            by = 0.0
+            if fresh and abs(x.max()) > 40:
+                by = x.max() - ref
+            elif not fresh and np.exp2(x - ref).sum() >= 2.0 ** 40:
+                by = x.max() - ref
+            alpha = 1.0 if fresh else 2.0 ** -by
+            fresh = False
+            ref += by
+            w = np.exp2(x - (ref - by if mistake == "weights of the old reference" else ref))
+            l = l * (1.0 if mistake == "sums of weights not scaled" else alpha) + w.sum()
+            o = o * (1.0 if mistake == "sums of values not scaled" else
+                     alpha * alpha if mistake == "sums of values scaled twice" else alpha) + w @ y
+        if not fresh:
+            parts.append((ref, l, o))
+    top = max(p[0] for p in parts)
+    f = [1.0 if mistake == "parts joined as they are" else 2.0 ** (p[0] - top) for p in parts]
+    if mistake == "one part lost":
+        f[len(f) // 2] = 0.0
+    return sum(a * p[2] for a, p in zip(f, parts)) / sum(a * p[1] for a, p in zip(f, parts))
+
+
+MISTAKES = ("weights of the old reference", "sums of weights not scaled", "sums of values not scaled",
+            "sums of values scaled twice", "parts joined as they are", "one part lost")

@@ -139,3 +139,49 @@ def test_queries_are_held_to_13_bits(ctx, rows, D):
         small = np.abs(s[:, 0]) <= 40.5 * np.log(2)
         assert (off <= slip + np.abs(s[:, 0]) * 2.0 ** -22 + np.where(small, 2.0 ** -8, 0)).all(), (m, off, slip)
         assert small.mean() < 0.7
+
+
+@pytest.mark.parametrize("kind", A.CLIMBS)
+@pytest.mark.parametrize("rows,copies,D,n", [
+    (1, 1, 64, 1300), (1, 1, 128, 9000), (7, 256, 64, 1300), (16, 128, 128, 1300), (1, 256, 32, 1300),
+    (20, 1, 64, 1300), (20, 1, 128, 9000), (20, 256, 64, 1300), (150, 64, 96, 1300), (33, 256, 32, 1300),
+])
+def test_references_that_move(ctx, kind, rows, copies, D, n):
+    """Scores that climb, fall or jump by tens while earlier sums still count, in ranges, in waves and
+    in one pass; test_attention_bounds shows which mistakes these rooms reject."""
+    for had in (0, 32):
+        print("attention", kind, "rows", rows, "heads", 2 * copies, "D", D, "keys", n, "had", had, flush=True)
+        p = A.climb_problem(n + D, kind, n, rows, 2, D, had, copies)
+        out, lse = _run(ctx, p)
+        w = _want(A.only_heads(p, 2))
+        A.check(out[:, :2], lse[:, :2], w)
+        assert A.outside(0.0, w[0], w[2]) > 0.4                       # zeros would not pass
+        assert np.array_equal(out, np.tile(out[:, :2], (1, copies, 1)))
+        assert np.array_equal(lse, np.tile(lse[:, :2], (1, copies)))
+
+
+ORDINARY = [
+    # lens, qs, hq, hk, D, page, had, causal
+    ([1], [1], 1, 1, 64, 16, 0, True), ([17], [1], 8, 1, 128, 16, 32, True),
+    ([64, 65, 63], [1, 1, 1], 8, 2, 128, 16, 32, True), ([1000, 1, 0, 333], [1, 1, 1, 1], 32, 8, 128, 16, 32, True),
+    ([129], [1], 16, 1, 96, 32, 0, True), ([200], [1], 20, 1, 112, 64, 32, True),
+    ([70, 300], [5, 1], 6, 2, 72, 16, 32, False), ([150, 40], [33, 40], 4, 4, 64, 64, 32, True),
+    ([10, 100], [30, 7], 4, 2, 64, 16, 32, True), ([257], [130], 3, 3, 40, 128, 0, True),
+    ([31, 300, 128], [64, 129, 1], 2, 2, 80, 16, 32, False), ([48], [17], 2, 1, 32, 16, 32, False),
+    ([48], [3], 2, 1, 8, 16, 32, True), ([700], [200], 4, 1, 128, 32, 32, True),
+    ([2100], [2], 4, 2, 64, 16, 0, False), ([3000, 5], [1, 1], 4, 1, 96, 16, 0, True),
+    ([640], [100], 5, 5, 24, 16, 0, False),
+]
+
+
+@pytest.mark.parametrize("lens,qs,hq,hk,D,ps,had,causal", ORDINARY)
+def test_ordinary_problems_closely(ctx, lens, qs, hq, hk, D, ps, had, causal):
+    """Masks, ragged lengths, groups and pages with queries held exactly: what is left is the weights'
+    rounding, so that most zeros would not pass."""
+    print("attention lens", lens, "qs", qs, "heads", hq, hk, "D", D, "page", ps, "had", had, flush=True)
+    for k in (3, 1):                                  # scores of a few units, and of tens
+        p = A.problem(sum(lens) + D + k, lens, qs, hq, hk, D, ps, had, k=k + (4 if had else 0), causal=causal)
+        w = _want(p)
+        A.check(*_run(ctx, p), w)
+        seen = np.isfinite(w[1])
+        assert A.outside(0.0, w[0][seen], w[2][seen]) > 0.75
