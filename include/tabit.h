@@ -553,9 +553,9 @@ typedef struct tabit_rope {
  *   slots           device int64 [num_tokens].  A slot outside the cache (-1 for
  *                   padding) writes nothing; slots of one call must be distinct.
  *   positions       device int32 [num_tokens], or NULL without rope.
- * A (token, head) whose key or value holds an infinity or NaN, or whose position
- * is outside the tables, is stored as not a number: queries that see it answer
- * NaN, no other query is touched by it.
+ * A (token, head) whose key or value holds an infinity or NaN, before or after its
+ * transform, or whose position is outside the tables, is stored as not a number:
+ * queries that see it answer NaN, no other query is touched by it.
  */
 int tabit_kv_append(tabit_ctx* ctx, const tabit_kv_cache* cache, const uint16_t* k_bf16,
                     int64_t k_stride, const uint16_t* v_bf16, int64_t v_stride, int num_tokens,
@@ -575,8 +575,10 @@ int tabit_kv_read(tabit_ctx* ctx, const tabit_kv_cache* cache, const int64_t* sl
  * table; with `causal` query i of the sequence's n sees j <= kv_lens[b] - n + i.
  * Query head h reads key head h / (num_q_heads / num_kv_heads).  A query that sees
  * no key answers zeros (lse -inf).  Scores, softmax and sums are fp32; a query
- * keeps 13 bits below its block's largest element, a weight is rounded to bf16 and
- * summed as rounded.
+ * keeps 13 bits below the largest element of its block of 32 (fewer bits of itself,
+ * then, than bf16 has in elements below 2^-5 of it), a weight is rounded to bf16
+ * and summed as rounded.  Values of any finite size give a finite result (up to 2^16
+ * keys of the largest weight and value).
  *   q            device bf16, token t's [num_q_heads][head_dim] at t * q_stride
  *                elements (multiple of 8), 16-byte aligned
  *   cu_q         device int32 [num_seqs + 1]: sequence b's rows are
@@ -592,7 +594,7 @@ int tabit_kv_read(tabit_ctx* ctx, const tabit_kv_cache* cache, const int64_t* sl
  *                finite, answers NaN
  *   out          device bf16 [num_tokens][num_q_heads][head_dim], 16-byte aligned
  *   lse          device fp32 [num_tokens][num_q_heads] or NULL: natural logarithm
- *                of the row's sum of exp(score), each rounded to bf16 (2^-9 of the
+ *                of the row's sum of exp(score), each rounded to bf16 (2^-8 of the
  *                sum at most, so exp(lse) * out joins ranges of keys without loss)
  *   ws           device workspace of tabit_kv_attention_workspace_bytes bytes,
  *                16-byte aligned (NULL when that is 0)
@@ -632,8 +634,9 @@ enum tabit_norm { TABIT_NORM_NONE = 0, TABIT_NORM_LAYER = 1, TABIT_NORM_RMS = 2 
  *   x' = res_scale * x + gate * N_post(y)      (x' = res_scale * x without y)
  *   h  = N_pre(x') * (1 + scale) + shift
  * N: identity, layer norm (v - mean) / sqrt(var + eps) or RMS norm
- * v / sqrt(mean(v^2) + eps), times its weight if given.  fp32 throughout; h is
- * computed from x' before x' is rounded.
+ * v / sqrt(mean(v^2) + eps), times its weight if given.  fp32 throughout (a row
+ * with elements above 2^56, whose squares may add up past it, is divided by
+ * infinity); h is computed from x' before x' is rounded.
  *   x, y         device bf16 [rows][width]; y may be NULL (then no post norm or gate)
  *   post_weight, pre_weight  device bf16 [width] or NULL (1)
  *   gate, scale, shift       device bf16, sample s's row of width elements at
