@@ -185,3 +185,20 @@ def test_ordinary_problems_closely(ctx, lens, qs, hq, hk, D, ps, had, causal):
         A.check(*_run(ctx, p), w)
         seen = np.isfinite(w[1])
         assert A.outside(0.0, w[0][seen], w[2][seen]) > 0.75
+
+
+def test_counts_past_32_bits_are_refused(ctx):
+    """A bound of 2^32 was cut to 0 on its way into the library, and every row answered zeros."""
+    p = A.problem(1, [20], [2], 4, 2, 64, 16, 0)
+    d = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(DEV)       # noqa: E731
+    cache = T.KVCache(*[d(p["arr"][x]) for x in ("k_codes", "k_scales", "v_codes", "v_scales")], head_dim=64)
+    q, cu, lens = d(p["q"]).bfloat16(), d(p["cu"]), d(np.asarray(p["lens"], np.int32))
+    for max_q, max_kv in ((2, 1 << 32), (1 << 32, 20), (2, (1 << 32) + 20), (2, 1 << 31)):
+        with pytest.raises(ValueError):
+            ctx.kv_attention(cache, q, cu, d(p["table"]), lens, max_q, max_kv)
+        with pytest.raises(ValueError):
+            ctx.kv_attention_workspace(cache, q, 1, max_q, max_kv)
+    with pytest.raises(T.TabitError) as e:
+        ctx.kv_attention(cache, q, cu, d(p["table"]), lens, 2, -1)
+    assert e.value.status == T.ESHAPE
+    assert torch.isfinite(ctx.kv_attention(cache, q, cu, d(p["table"]), lens, 2, 20)).all()

@@ -211,6 +211,13 @@ def _dev(t: torch.Tensor, dtype, name: str, shape=None) -> None:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _counts(*values) -> None:
+    """Refuses what a C int does not hold: ctypes would cut it without a word."""
+    for v in values:
+        if not -0x80000000 <= v <= 0x7FFFFFFF:
+            raise ValueError(f"a count of {v} does not fit the library's 32 bits")
+
+
 def _rows(t: torch.Tensor, name: str, tail, device) -> int:
     """bf16 [T][heads][head_dim] whose tokens may be apart (a slice of a fused output):
     the stride of a token in elements."""
@@ -754,6 +761,7 @@ class Context:
             raise ValueError("k and v disagree on the number of tokens")
         _on(slots, torch.int64, "slots", (n,), cache.device)
         r, pos = self._rope(cache, rope, positions, n)
+        _counts(n)
         if n == 0:
             return
         self._check(self._lib.tabit_kv_append(self._h, cache._ref, k.data_ptr(), ks, v.data_ptr(), vs,
@@ -764,6 +772,7 @@ class Context:
         """The keys and values held at `slots` as bf16 [T][kv_heads][head_dim] each."""
         n = slots.shape[0]
         _on(slots, torch.int64, "slots", (n,), cache.device)
+        _counts(n)
         shape = (n,) + tuple(cache._row)
         k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
         v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
@@ -777,6 +786,7 @@ class Context:
     def kv_attention_workspace(self, cache: KVCache, q: torch.Tensor, num_seqs: int, max_q: int,
                                max_kv: int) -> Optional[torch.Tensor]:
         """A workspace for such calls (None where none is needed)."""
+        _counts(q.shape[0], num_seqs, max_q, max_kv)
         n = int(self._lib.tabit_kv_attention_workspace_bytes(
             q.shape[0], q.shape[1], cache.num_kv_heads, cache.head_dim, num_seqs, max_q, max_kv))
         return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
@@ -799,6 +809,7 @@ class Context:
         T, hq = q.shape[0], q.shape[1]
         stride = _rows(q, "q", torch.Size((hq, cache.head_dim)), dev)
         B = kv_lens.shape[0]
+        _counts(T, B, max_q, max_kv)
         _on(kv_lens, torch.int32, "kv_lens", (B,), dev)
         _on(cu_q, torch.int32, "cu_q", (B + 1,), dev)
         _on(block_table, torch.int32, "block_table", (B, block_table.shape[1]), dev)
@@ -843,6 +854,7 @@ class Context:
             raise ValueError("x must be [M][H]")
         M, H = x.shape
         dev = x.device
+        _counts(M, H)
         if y is not None:
             _on(y, torch.bfloat16, "y", (M, H), dev)
         for w, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
