@@ -24,11 +24,12 @@
 // a SIMD alone do not keep enough bytes on the way.
 //
 // Memory bounds it: 4 bytes read and 2 + 2 (INT8 1, MXFP4 0.53) written per element.
-// Measured: 17776 x 1920, RMS post and layer pre norm, INT8 after a block of 32: 56 us
+// Measured: 17776 x 1920, RMS post and layer pre norm, INT8 after a block of 32: 53 - 56 us
 // (76 with the factors read for each row, 60 without the early loads), 4.3 TB/s where a
-// large copy reaches 5.2; 8192 x 1152 (two samples, layer norm, bf16): 17 us, 4.5 TB/s.
-// At 67 MB of x the widths 512 to 8192 reach 4.3 - 5.4 TB/s, 256 reaches 2.9 (half of the
-// lanes are past the row), 16384 reaches 3.8 and 32768 1.7, where registers spill.
+// large copy reaches 5.2, MXFP4 after a block of 32 55 us (4.0 TB/s); 8192 x 1152 (two samples,
+// layer norm, bf16): 17 us, 4.5 TB/s.  At 67 MB of x, INT8 and MXFP4, the widths 512 to 8192 reach
+// 4.3 - 5.6 TB/s with modulation or without, 256 reaches 3.0 (half of the lanes are past the row),
+// 16384 reaches 3.9 and 32768 1.7, where registers spill.
 #include "../../include/tabit.h"
 #include "kv_common.h"
 

@@ -98,7 +98,10 @@ __device__ __forceinline__ float add_pair(uint32_t pair, float sum) {
 // bf16 value tile: rows of RS bytes.  Runs are XORed with bits of the key so that what
 // one access touches fills a 256-byte bank window: the 4 keys x 2 runs (or 8 keys x 1
 // run) of 32 lanes of a transposed read, and, with the pieces of every other eight
-// keys swapped, the 16 keys that 16 lanes write at once.
+// keys swapped, the 16 keys that 16 lanes write at once.  By the counters that is not
+// the whole rule: 39 - 40% of the cycles LDS is active are conflicts in single rows of
+// 128 elements, 21 - 25% in chunks (which access has them was not taken apart; LDS is
+// active for about a quarter of the time).
 template <int RS>
 __device__ __forceinline__ int v_off(int key, int c, int half) {
   const int x = RS == 256 ? ((key & 3) << 1 | ((key >> 2) & 1)) : ((key & 2) | ((key >> 2) & 1));
@@ -711,16 +714,17 @@ __device__ __forceinline__ v16f score_term(v4i x, const v8i& q, v16f s, int byte
 // as they leave the matrix core, and what a tile's addresses need is prepared for 64 tiles
 // at once.
 //
-// Measured: 2700 rows x 17776 keys x 30 heads x 64 in 395 - 409 us with the join (900 - 930
-// TFLOP/s at 4 flops a key, row and element; a library bf16 product of 8192^3 reaches
-// 1207), four causal turns (1024 to 2048 queries behind caches of up to 6144 keys, 32 heads
-// over 8, 128 elements) at 950 TFLOP/s of visible keys, 2 x 4096 rows x 300 keys x 16 heads
-// x 72 in 31 us.  Matrix cores are busy for a third of the cycles, LDS for 30%; a wave
+// Measured, the clock settled: 2700 rows x 17776 keys x 30 heads x 64 in 407 - 424 us by the box,
+// 16 of it the join (870 - 905 TFLOP/s at 4 flops a key, row and element; a library bf16 product
+// of 8192^3 reaches 1207; 446 us in the first 20 calls on an idle card), four causal turns (1024
+// to 2048 queries behind caches of up to 6144 keys, 32 heads over 8, 128 elements) at 965
+// TFLOP/s of visible keys, 2 x 4096 rows x 300 keys x 16 heads x 72 in 30 - 31 us.  Matrix cores are busy for a third of the cycles, LDS for 30%; a wave
 // waits for its turn to issue most of the time.  Level or slower: scores of a tile beside the weights of the one before,
 // eight waves a workgroup, 32 keys a step, three stages, heads or sequences as the fastest
 // index (causal turns 527 us for 466).  Up to 64 elements three workgroups fit a CU (four
-// would spill: 485 us for 409); 96 and 128 elements take 196 and 226 registers, two
-// workgroups (three spill: 38 us for 30 at 72 elements).
+// would spill: 485 us for 409); 96 and 128 elements take 204 and 232 registers, two
+// workgroups (three spill: 38 us for 30 at 72 elements).  Seeing value scales far from one and
+// keeping sums in range for them costs the first 1.2%, short chunks 1.5%, causal turns nothing.
 template <int NB>
 __global__ void __launch_bounds__(256, NB <= 2 ? 3 : 2)
 kv_attention_rows128_kernel(KvAttnArgs a) {
@@ -1335,7 +1339,11 @@ int kv_attention_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_
   }
   // 128 rows: the splits whose rounds of workgroups over the chip's slots take least.  A
   // range costs its tiles and about six more to start; each split's partial sums cost the
-  // chip about one tile's time a row tile in two slots.
+  // chip about one tile's time a row tile in two slots.  Two slots a CU are counted for every
+  // head size: up to 64 elements a third workgroup fits, but the three share the vector units,
+  // so a round of three takes longer.  By two and by three (64 elements, us): 2700 rows x 17776
+  // keys x 30 heads 404 and 423, 17776 x 17776 x 6 504 and 527, 4096 x 4096 x 16 83 and 95, four of
+  // 256 x 2048 x 16 28 and 31; 512 x 8192 x 30 54 and 53, two of 1000 x 3000 x 20 58 and 55.
   const long long slots = 2ll * NUM_CUS;
   long long best = 0;
   int splits = 1;
