@@ -202,3 +202,37 @@ def test_counts_past_32_bits_are_refused(ctx):
         ctx.kv_attention(cache, q, cu, d(p["table"]), lens, 2, -1)
     assert e.value.status == T.ESHAPE
     assert torch.isfinite(ctx.kv_attention(cache, q, cu, d(p["table"]), lens, 2, 20)).all()
+
+
+@pytest.mark.parametrize("rows,n", [(1, 1), (16, 1), (17, 1), (140, 1), (1, 3000), (1, 400), (20, 3000)])
+@pytest.mark.parametrize("had", [0, 32])
+def test_one_visible_key_answers_its_value(ctx, rows, n, had):
+    """One key alone, or one with all the weight of fp32 (the others 200 below, base 2): its value,
+    rounded to bf16 (at a tie either way), and zero exactly where the value is zero."""
+    for D in (64, 128):
+        print("attention one key, rows", rows, "keys", n, "D", D, "had", had, flush=True)
+        p = A.climb_problem(rows + n, "late", n, rows, 2, D, had)
+        rng = np.random.default_rng(n + D)
+        # every score -100 times the factor but one key's, +100
+        codes = np.array([A._codes_of(-96), A._codes_of(96)], np.uint8)
+        codes = codes[:, 0::2] | codes[:, 1::2] << 4
+        kc = p["arr"]["k_codes"]
+        kc[:, :, :, :8] = codes[0]
+        at = n // 3
+        kc[at // 16, :, at % 16, :8] = codes[1]
+        if n > 1:
+            p["q"] = np.repeat(A.climb_problem(1, "late", 64, rows, 2, D, had)["q"][:1], rows, 0)
+        else:                                      # scores between -40 and 40, weights of any mantissa
+            p["q"] = 0.3 * rng.standard_normal(p["q"].shape).astype(np.float32) / (5 if had else 1)
+        for nib in range(3):                       # zeros among the values
+            p["arr"]["v_codes"][:, :, :, nib::5] = 0
+        out, _ = _run(ctx, p)
+        _, v, _ = A.gathered(p["arr"], p["table"][0], n)
+        want = A.joined(np.eye(n)[at:at + 1], v[0], had, D)[0], A.joined(np.eye(n)[at:at + 1], v[1], had, D)[0]
+        for h in range(2):
+            x = want[h]
+            step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(x), 1e-300))) - 7)
+            tie = np.abs(np.abs(x / step - np.floor(x / step)) - 0.5) < 1e-9
+            assert np.all(out[:, h][:, ~tie] == (np.rint(x / step) * step)[~tie])
+            assert np.all(np.abs(out[:, h] - x) <= step / 2 * (1 + 1e-9))
+            assert tie.mean() < 0.5

@@ -86,9 +86,21 @@ __device__ __forceinline__ float part_top(float ref, float sum) {
   return ref + (float)__builtin_amdgcn_frexp_expf(sum);
 }
 
+// 1 / sum (for a transformed cache 1 / (32 sum)) in two factors: a power of two, which is taken
+// before the transform adds 32 elements, so that their sum stays in range and what cancels does so
+// exactly, and the rest, which is taken after it.  0 for a row that sees no key.
+struct Shares {
+  float power, rest;
+};
+__device__ __forceinline__ Shares shares(float sum, bool had) {
+  const int e = __builtin_amdgcn_frexp_expf(sum);
+  return {__builtin_amdgcn_ldexpf(had ? 0.03125f : 1.0f, -e),
+          sum == 0.0f ? 0.0f : 1.0f / __builtin_amdgcn_ldexpf(sum, -e)};
+}
+
 // sum + both bf16 weights of a pair, in fp32.  The rounded weights are summed, not the exact
 // ones: what a row's values are multiplied with then adds up to one, and a row that sees one
-// key answers that key's value exactly.
+// key answers that key's value as it is (a tie of its rounding to bf16 may fall either way).
 __device__ __forceinline__ float add_pair(uint32_t pair, float sum) {
   const v2bf one = {(__bf16)1.0f, (__bf16)1.0f};
   return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf, pair), one, sum, false);
@@ -665,17 +677,17 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
     if (fb == 0) *part_stats(a, sp, out_row) = make_float2(M, L);
     return;
   }
-  const float inv = L == 0.0f ? 0.0f : (c.had ? 0.03125f : 1.0f) / L;   // no visible key: 0
+  const Shares inv = shares(L, c.had);
 #pragma unroll
-  for (int e = 0; e < 32; ++e) x[e] *= inv;          // (first: the transform adds 32 of them)
+  for (int e = 0; e < 32; ++e) x[e] *= inv.power;
   if (c.had) fwht32_lane(x);
 #pragma unroll
   for (int e = 0; e < 32; e += 8) {
     const int d = fb * 32 + e;
     if (d < c.head_dim)
       *reinterpret_cast<uint4*>(a.out + out_row * c.head_dim + d) =
-          make_uint4(pack_bf16(x[e], x[e + 1]), pack_bf16(x[e + 2], x[e + 3]),
-                     pack_bf16(x[e + 4], x[e + 5]), pack_bf16(x[e + 6], x[e + 7]));
+          make_uint4(pack_bf16(x[e] * inv.rest, x[e + 1] * inv.rest), pack_bf16(x[e + 2] * inv.rest, x[e + 3] * inv.rest),
+                     pack_bf16(x[e + 4] * inv.rest, x[e + 5] * inv.rest), pack_bf16(x[e + 6] * inv.rest, x[e + 7] * inv.rest));
   }
   if (a.lse != nullptr && fb == 0)
     a.lse[out_row] = L == 0.0f ? kNegInf : (M + __builtin_log2f(L)) * 0.6931471805599453f;
@@ -1110,10 +1122,10 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     if (half == 0) *part_stats(a, sp, out_row) = make_float2(fresh ? kNegInf : ref, l);
     return;
   }
-  const float inv = l == 0.0f ? 0.0f : (c.had ? 0.03125f : 1.0f) / l;
+  const Shares inv = shares(l, c.had);
 #pragma unroll
   for (int d = 0; d < ND; ++d) {
-    o[d] *= inv;   // (first: the transform adds 32 of them)
+    o[d] *= inv.power;
     if (c.had) {   // element bits 0, 1 and 3, 4 are register bits, bit 2 is the lane half
 #pragma unroll
       for (int h = 1; h < 16; h <<= 1) {
@@ -1139,7 +1151,7 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     for (int g = 0; g < 4; ++g)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        w[g][e] = pack_bf16(o[d][4 * g + 2 * e], o[d][4 * g + 2 * e + 1]);
+        w[g][e] = pack_bf16(o[d][4 * g + 2 * e] * inv.rest, o[d][4 * g + 2 * e + 1] * inv.rest);
     // runs g and g + 1 of eight elements: the low half ends with run g, the high one with g + 1
 #pragma unroll
     for (int g = 0; g < 4; g += 2) {
@@ -1178,7 +1190,8 @@ kv_attention_join_kernel(KvAttnArgs a) {
   const bool ok = gr < GROUPS && r < n * a.q_heads;
   const KvCacheArgs& c = a.cache;
   const long long row = (long long)q0 * a.q_heads + (ok ? r : 0);
-  float M = kNegInf, L = 0.0f, inv = 0.0f;
+  float M = kNegInf, L = 0.0f;
+  Shares inv;
   v4f x = {0.0f, 0.0f, 0.0f, 0.0f};
   if constexpr (WIDE) {
     // one thread a split: maxima and sums at once, the weights to LDS
@@ -1209,11 +1222,11 @@ kv_attention_join_kernel(KvAttnArgs a) {
     if (lane == 0) stats[4 + (threadIdx.x >> 6)] = w;
     __syncthreads();
     L = (stats[4] + stats[5]) + (stats[6] + stats[7]);
-    inv = L == 0.0f ? 0.0f : (c.had ? 0.03125f : 1.0f) / L;
+    inv = shares(L, c.had);
 #pragma unroll
     for (int k = 0; k < MINE; ++k) {
       const int s = gr + k * GROUPS;
-      if (ok && s < a.splits && !(weight[s] < 0.0f)) x += weight[s] * inv * y[k];
+      if (ok && s < a.splits && !(weight[s] < 0.0f)) x += weight[s] * inv.power * y[k];
     }
   } else if (ok) {
     for (int s = 0; s < a.splits; ++s) {
@@ -1244,10 +1257,10 @@ kv_attention_join_kernel(KvAttnArgs a) {
       }
     }
   }
-  if constexpr (!WIDE) {                   // (first: the transform adds 32 of them)
+  if constexpr (!WIDE) {
     static_assert(kNarrow <= 8, "the room of the narrow form");
-    inv = L == 0.0f ? 0.0f : (c.had ? 0.03125f : 1.0f) / L;
-    x *= inv;
+    inv = shares(L, c.had);
+    x *= inv.power;
   }
   if (c.had) {
     float v[4] = {x[0], x[1], x[2], x[3]};
@@ -1267,7 +1280,7 @@ kv_attention_join_kernel(KvAttnArgs a) {
   if (!ok || (WIDE && gr != 0)) return;
   if (li * 4 < c.head_dim)
     *reinterpret_cast<uint2*>(a.out + row * c.head_dim + li * 4) =
-        make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+        make_uint2(pack_bf16(x[0] * inv.rest, x[1] * inv.rest), pack_bf16(x[2] * inv.rest, x[3] * inv.rest));
   if (a.lse != nullptr && li == 0)
     a.lse[row] = L == 0.0f ? kNegInf : (M + __builtin_log2f(L)) * 0.6931471805599453f;
 }
