@@ -726,7 +726,7 @@ __device__ __forceinline__ v16f score_term(v4i x, const v8i& q, v16f s, int byte
 // as they leave the matrix core, and what a tile's addresses need is prepared for 64 tiles
 // at once.
 //
-// Measured, the clock settled: 2700 rows x 17776 keys x 30 heads x 64 in 407 - 424 us by the box,
+// Measured, the clock settled: 2700 rows x 17776 keys x 30 heads x 64 in 407 - 424 us by the card,
 // 16 of it the join (870 - 905 TFLOP/s at 4 flops a key, row and element; a library bf16 product
 // of 8192^3 reaches 1207; 446 us in the first 20 calls on an idle card), four causal turns (1024
 // to 2048 queries behind caches of up to 6144 keys, 32 heads over 8, 128 elements) at 965
