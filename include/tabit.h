@@ -627,6 +627,152 @@ int tabit_kv_attention(tabit_ctx* ctx, const tabit_kv_cache* cache, const tabit_
 size_t tabit_kv_attention_workspace_bytes(int num_tokens, int num_q_heads, int num_kv_heads,
                                           int head_dim, int num_seqs, int max_q, int max_kv);
 
+/*
+ * Attention of trees of drafted tokens: tabit_kv_attention's rows, arguments and result
+ * with a mask of their own.  The n = cu_q[b+1] - cu_q[b] rows of sequence b are the nodes of
+ * its tree (or several trees), whose keys and values are the last n of its kv_lens[b]
+ * tokens, in the order of the rows: row i sees every token before them, and node j iff bit
+ * j % 64 of word j / 64 of its row of the mask is set.
+ *   args        as tabit_kv_attention; args->causal must be 0, max_q at most 8192
+ *   mask        device uint64 [num_tokens][mask_words], 8-byte aligned;
+ *               mask_words at least ceil(max_q / 64); bits past n are not read.  Nodes past
+ *               the mask's words are not seen
+ * A row that sees no key answers zeros (lse -inf).  ws: of
+ * tabit_kv_tree_attention_workspace_bytes, arguments as the other's.
+ */
+int tabit_kv_tree_attention(tabit_ctx* ctx, const tabit_kv_cache* cache, const tabit_kv_attention_args* args,
+                            const uint64_t* mask, int mask_words, void* stream);
+size_t tabit_kv_tree_attention_workspace_bytes(int num_tokens, int num_q_heads, int num_kv_heads,
+                                               int head_dim, int num_seqs, int max_q, int max_kv);
+
+/*
+ * Masks and depths of such trees from each node's parent, once for all layers of a step.
+ *   parents     device int32 [num_tokens]: of row cu_q[b] + i the index of its parent among
+ *               the sequence's rows, less than i; anything else (-1): the node hangs on the
+ *               last token before the tree
+ *   mask        device uint64 [num_tokens][mask_words]: the node itself and its ancestors
+ *   depth       device int32 [num_tokens] or NULL: the number of ancestors, which added to
+ *               kv_len - n is the node's position
+ * cu_q, num_seqs, max_q as for the attention (at most max_q nodes of a sequence; rows of no
+ * sequence are left as they are); max_q at most 8192, mask_words at least ceil(max_q / 64).
+ */
+int tabit_tree_mask(tabit_ctx* ctx, const int32_t* parents, int num_tokens, const int32_t* cu_q, int num_seqs,
+                    int max_q, uint64_t* mask, int mask_words, int32_t* depth, void* stream);
+
+/*
+ * Accumulated attention weights, what eviction goes by.  Adds to the sum of every cached
+ * token and key head the weights that the query rows give it:
+ *   sums[page][h][slot] += sum over the rows i of sequence b and the heads of h's group of
+ *                          exp(s_ij) / sum_j exp(s_ij),   s_ij = scale (R q_i) . k_j
+ * with rows, masks and lengths as tabit_kv_attention.  With args->causal the last n tokens
+ * of a sequence (the queries' own) are set, not added to: a token's sum starts with the call
+ * that has its query.  Without, clear the sums of tokens when they are appended.
+ *   args    as tabit_kv_attention; out is not used and must be NULL; lse may be NULL, or
+ *           receives the logarithm of each row's sum of exp(score), here of exact weights
+ *   sums    device fp32 [num_pages][num_kv_heads][page_size], 16-byte aligned
+ *   ws      of tabit_kv_weigh_workspace_bytes bytes, 16-byte aligned
+ * Everything is held to fp32 (a query to 2^-21 of the largest element of its block of 32).
+ * A row whose own values, position or score with some key it sees is not a number (see
+ * tabit_kv_append) adds nothing, nor does a row that sees no key; the sum of a token that is
+ * not a number gets nothing.  Sums never become NaN by a call.  Pages of the sequences of a
+ * call must be distinct.  The result does not depend on timing.
+ */
+int tabit_kv_weigh(tabit_ctx* ctx, const tabit_kv_cache* cache, const tabit_kv_attention_args* args, float* sums,
+                   void* stream);
+size_t tabit_kv_weigh_workspace_bytes(int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                      int num_seqs, int max_q, int max_kv);
+
+/*
+ * Which tokens of its cache each key head keeps.  A sequence of at most `budget` tokens keeps
+ * them all; of a longer one each head keeps the first `sinks`, the last `recent`, and of those
+ * between the budget - sinks - recent with the largest sums, of equal sums the earlier
+ * token.  NaN, and a token whose page is not in the cache, come after every number.
+ *   cache        for its shape (the arrays are not read)
+ *   sums         device fp32 [num_pages][num_kv_heads][page_size], as tabit_kv_weigh keeps them
+ *   block_table, table_stride, kv_lens, max_kv, num_seqs   as tabit_kv_attention, max_kv at
+ *                most 2^30
+ *   keep         device int32 [num_seqs][num_kv_heads][budget] output: the kept tokens'
+ *                indexes in their order, then -1
+ *   new_lens     device int32 [num_seqs] output: min(kv_len, budget)
+ * sinks + recent at most budget.
+ */
+int tabit_kv_evict(tabit_ctx* ctx, const tabit_kv_cache* cache, const float* sums, const int32_t* block_table,
+                   int table_stride, const int32_t* kv_lens, int num_seqs, int max_kv, int budget, int sinks,
+                   int recent, int32_t* keep, int32_t* new_lens, void* stream);
+
+/*
+ * Moves tokens inside the cache, in place: of each sequence b and key head h, token
+ * starts[b] + j becomes what token keep[b][h][j] was, for j < counts[b] (codes and scales of
+ * key and value, and the sum where sums are given).  After tabit_kv_evict this is the
+ * eviction (keep and new_lens as they came); with one list for all heads and starts it keeps
+ * the accepted path of a drafted tree.
+ *   keep        device int32 [num_seqs][keep_heads][keep_stride], keep_heads 1 or
+ *               num_kv_heads.  In rising order, none before its place (keep[j] >= starts + j);
+ *               an index that is negative or outside the table's pages in the cache moves
+ *               nothing, and its place is left as it is
+ *   counts      device int32 [num_seqs], taken as at most keep_stride
+ *   starts      device int32 [num_seqs] or NULL (0)
+ *   sums        device fp32 [num_pages][num_kv_heads][page_size] or NULL
+ *   ws          device workspace of tabit_kv_compact_workspace_bytes bytes, 16-byte aligned
+ * Tokens behind the last place are left as they are.  Pages of the sequences of a call must
+ * be distinct.
+ */
+int tabit_kv_compact(tabit_ctx* ctx, const tabit_kv_cache* cache, const int32_t* block_table, int table_stride,
+                     int num_seqs, const int32_t* keep, int keep_heads, int keep_stride,
+                     const int32_t* counts, const int32_t* starts, float* sums, void* ws, size_t ws_bytes,
+                     void* stream);
+size_t tabit_kv_compact_workspace_bytes(int num_seqs, int num_kv_heads, int head_dim, int keep_stride);
+
+/*
+ * Low-rank adapters of many requests at once beside a shared projection:
+ *   out[t] = y[t] + scale_a (x[t] A_a^T) B_a^T,   a the adapter of t's segment
+ * on the very rows that the projection reads: bf16, or the codes and scales of
+ * tabit_hadamard_quant_act / tabit_block_norm (then A is to be transformed alike:
+ * tabit_adapter_rotate).  fp32 from the products to the one rounding of out; what lies between
+ * the two products is held to 2^-16 of itself.
+ *   x           x_fmt TABIT_FMT_BF16: bf16 [rows][K], token t at t * x_stride elements
+ *               (multiple of 8); TABIT_FMT_INT8: int8 [rows][K] with x_scale fp32 [rows];
+ *               TABIT_FMT_MXFP4: [rows][K/2] with x_scale uint8 [rows][K/32] (x_stride not
+ *               used: codes are dense)
+ *   a, b        device bf16 [num_adapters][rank][K] and [num_adapters][N][rank]; rank 16, 32,
+ *               64 or 128 (a smaller adapter is filled up with zeros)
+ *   scale       device fp32 [num_adapters] or NULL (1)
+ *   cu_rows     device int32 [num_segments + 1], not falling: segment i is rows
+ *               [cu_rows[i], cu_rows[i+1]); rows of no segment are left as they are in out
+ *   adapter     device int32 [num_segments]; outside [0, num_adapters): out = y
+ *   y, out      device bf16, row t at t * y_stride and t * out_stride elements (multiples
+ *               of 8, at least N); out may be y (then with its stride) or not overlap it
+ *   ws          of tabit_adapter_workspace_bytes bytes, 16-byte aligned
+ * K and N multiples of 32, at most 32768; 1 <= num_adapters * rank; matrices 16-byte aligned.
+ */
+typedef struct tabit_adapter_args {
+  const void *x, *x_scale;
+  int x_fmt, rows, K, N;
+  int64_t x_stride;
+  const uint16_t *a, *b;
+  const float* scale;
+  int num_adapters, rank;
+  const int32_t *cu_rows, *adapter;
+  int num_segments;
+  const uint16_t* y;
+  int64_t y_stride;
+  uint16_t* out;
+  int64_t out_stride;
+  void* ws;
+  size_t ws_bytes;
+} tabit_adapter_args;
+int tabit_adapter_linear(tabit_ctx* ctx, const tabit_adapter_args* args, void* stream);
+size_t tabit_adapter_workspace_bytes(int rows, int rank, int num_segments);
+
+/*
+ * The A matrices of adapters for rows that are transformed before they are quantized
+ * (had_block 32, 64 or 128): each row of a, bf16 [rows][K], becomes (1 / had_block) times its
+ * block Walsh-Hadamard transform, in fp32, rounded to bf16 once: x A^T = (x H) (A H / b)^T.  out may
+ * be a.  Once, when an adapter is loaded.
+ */
+int tabit_adapter_rotate(tabit_ctx* ctx, const uint16_t* a, int rows, int K, int had_block, uint16_t* out,
+                         void* stream);
+
 enum tabit_norm { TABIT_NORM_NONE = 0, TABIT_NORM_LAYER = 1, TABIT_NORM_RMS = 2 };
 
 /*

@@ -6,7 +6,7 @@ package does not load the library; the first Context() or call does, and
 raises if the library has not been built.
 """
 from ._lib import (  # noqa: F401
-    Context, KVCache, Layer, Rope, TabitError, load, version, act_workspace_bytes, gemm_config_info,
+    Adapters, Context, KVCache, Layer, Rope, TabitError, load, version, act_workspace_bytes, gemm_config_info,
     gemm_config_choose, mxfp4_config_info, mxfp4_config_choose, plane_config_info,
     plane_config_choose,
     weight_planes_bytes,
@@ -25,5 +25,5 @@ __all__ = [
     "plane_config_info", "plane_config_choose", "weight_planes_bytes", "dmpq_workspace_bytes",
     "mxfp4_config_choose",
     "PATH_HQDM", "OPT_HQDM_CONFIG", "hqdm_config_info", "noalloc_scratch_bytes",
-    "ACT_NONE", "ACT_GELU", "KVCache", "Rope", "FMT_BF16", "NORM_NONE", "NORM_LAYER", "NORM_RMS",
+    "ACT_NONE", "ACT_GELU", "Adapters", "KVCache", "Rope", "FMT_BF16", "NORM_NONE", "NORM_LAYER", "NORM_RMS",
 ]

@@ -98,6 +98,21 @@ _SIGNATURES = {
     "tabit_kv_attention": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p]),
     "tabit_kv_attention_workspace_bytes": (_c_size_t, [_c_int] * 7),
     "tabit_block_norm": (_c_int, [_c_void_p, _c_void_p, _c_void_p]),
+    "tabit_kv_tree_attention": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_void_p]),
+    "tabit_kv_tree_attention_workspace_bytes": (_c_size_t, [_c_int] * 7),
+    "tabit_tree_mask": (_c_int, [_c_void_p, _c_void_p, _c_int, _c_void_p, _c_int, _c_int, _c_void_p,
+                                 _c_int, _c_void_p, _c_void_p]),
+    "tabit_kv_weigh": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    "tabit_kv_weigh_workspace_bytes": (_c_size_t, [_c_int] * 7),
+    "tabit_kv_evict": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_int,
+                                _c_int, _c_int, _c_int, _c_int, _c_void_p, _c_void_p, _c_void_p]),
+    "tabit_kv_compact": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_void_p, _c_int,
+                                  _c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_size_t,
+                                  _c_void_p]),
+    "tabit_kv_compact_workspace_bytes": (_c_size_t, [_c_int] * 4),
+    "tabit_adapter_linear": (_c_int, [_c_void_p, _c_void_p, _c_void_p]),
+    "tabit_adapter_workspace_bytes": (_c_size_t, [_c_int] * 3),
+    "tabit_adapter_rotate": (_c_int, [_c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_void_p, _c_void_p]),
 }
 
 
@@ -147,6 +162,18 @@ class _BlockNormArgs(ctypes.Structure):
                 ("rows_per_sample", ctypes.c_int), ("res_scale", ctypes.c_float),
                 ("eps", ctypes.c_float), ("x_out", ctypes.c_void_p), ("h", ctypes.c_void_p),
                 ("h_scale", ctypes.c_void_p), ("fmt", ctypes.c_int), ("had_block", ctypes.c_int)]
+
+
+class _AdapterArgs(ctypes.Structure):
+    """tabit_adapter_args."""
+    _fields_ = [("x", ctypes.c_void_p), ("x_scale", ctypes.c_void_p), ("x_fmt", ctypes.c_int),
+                ("rows", ctypes.c_int), ("K", ctypes.c_int), ("N", ctypes.c_int),
+                ("x_stride", ctypes.c_int64), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("num_adapters", ctypes.c_int), ("rank", ctypes.c_int),
+                ("cu_rows", ctypes.c_void_p), ("adapter", ctypes.c_void_p),
+                ("num_segments", ctypes.c_int), ("y", ctypes.c_void_p), ("y_stride", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64), ("ws", ctypes.c_void_p),
+                ("ws_bytes", ctypes.c_size_t)]
 
 
 _lib = None
@@ -292,6 +319,57 @@ class Rope:
         self._c = _Rope(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1],
                         1 if interleaved else 0)
         self._ref = ctypes.addressof(self._c)
+
+
+def _matrix(t: torch.Tensor, name: str, width, device) -> int:
+    """bf16 [T][width] whose rows may be apart (a slice of a fused output): the stride of a row."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != 2 or t.shape[1] != width:
+        raise ValueError(f"{name} must have shape [rows, {width}], got {tuple(t.shape)}")
+    if t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+class Adapters:
+    """Low-rank adapters that one projection's requests choose from, kept alive here.
+
+    a bf16 [adapters][rank][K], b bf16 [adapters][N][rank], scale fp32 [adapters] or None (1); the
+    rank 16, 32, 64 or 128.  For rows that are transformed before they are quantized, a is to be
+    transformed too (Context.adapter_rotate).
+    """
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: Optional[torch.Tensor] = None):
+        _dev(a, torch.bfloat16, "a")
+        if a.dim() != 3:
+            raise ValueError("a must be [adapters][rank][K]")
+        self.num, self.rank, self.K = a.shape
+        _dev(b, torch.bfloat16, "b")
+        if b.dim() != 3 or b.shape[0] != self.num or b.shape[2] != self.rank:
+            raise ValueError(f"b must be [{self.num}][N][{self.rank}], got {tuple(b.shape)}")
+        if b.device != a.device:
+            raise ValueError(f"b must be on {a.device}, got {b.device}")
+        if scale is not None:
+            _on(scale, torch.float32, "scale", (self.num,), a.device)
+        self.N = b.shape[1]
+        self.a, self.b, self.scale, self.device = a, b, scale, a.device
+
+    @classmethod
+    def of(cls, pairs, scale: Optional[torch.Tensor] = None) -> "Adapters":
+        """From pairs of a [r][K] and b [N][r] bf16 of any ranks up to 128: smaller ones are filled up
+        with zeros to the smallest rank the kernels take."""
+        most = max(a.shape[0] for a, _ in pairs)
+        if most > 128:
+            raise ValueError(f"ranks are at most 128, got {most}")
+        rank = next(r for r in (16, 32, 64, 128) if r >= most)
+        pad = torch.nn.functional.pad
+        return cls(torch.stack([pad(a, (0, 0, 0, rank - a.shape[0])) for a, _ in pairs]),
+                   torch.stack([pad(b, (0, rank - b.shape[1])) for _, b in pairs]), scale)
 
 
 def version() -> str:
@@ -833,6 +911,250 @@ class Context:
                              0 if ws is None else ws.numel() * ws.element_size())
         self._check(self._lib.tabit_kv_attention(self._h, cache._ref, ctypes.addressof(a),
                                                  _stream(dev)))
+        return out
+
+    def _rows_args(self, cache: KVCache, q, cu_q, block_table, kv_lens, max_q, max_kv, scale, causal,
+                   rope, positions, out, lse, ws):
+        """Checks and the argument structure of an attention-like call; ws given."""
+        dev = cache.device
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be [tokens][q_heads][head_dim]")
+        T, hq = q.shape[0], q.shape[1]
+        stride = _rows(q, "q", torch.Size((hq, cache.head_dim)), dev)
+        B = kv_lens.shape[0]
+        _counts(T, B, max_q, max_kv)
+        _on(kv_lens, torch.int32, "kv_lens", (B,), dev)
+        _on(cu_q, torch.int32, "cu_q", (B + 1,), dev)
+        _on(block_table, torch.int32, "block_table", (B, block_table.shape[1]), dev)
+        r, pos = self._rope(cache, rope, positions, T)
+        if lse is not None:
+            _on(lse, torch.float32, "lse", (T, hq), dev)
+        if ws is not None and (ws.device != dev or not ws.is_contiguous()):
+            raise ValueError(f"ws must be contiguous and on {dev}")
+        return _KvAttentionArgs(q.data_ptr(), stride, T, hq, cu_q.data_ptr(), B, max_q,
+                                block_table.data_ptr(), block_table.shape[1], kv_lens.data_ptr(), max_kv,
+                                cache.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0,
+                                r, pos, _ptr(out), _ptr(lse), _ptr(ws),
+                                0 if ws is None else ws.numel() * ws.element_size())
+
+    def _rows_workspace(self, fn, cache: KVCache, q, num_seqs, max_q, max_kv):
+        _counts(q.shape[0], num_seqs, max_q, max_kv)
+        n = int(fn(q.shape[0], q.shape[1], cache.num_kv_heads, cache.head_dim, num_seqs, max_q, max_kv))
+        return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
+
+    # ------------------------------------------------------------ drafted trees
+    def tree_mask(self, parents: torch.Tensor, cu_q: torch.Tensor, max_q: int):
+        """Masks int64 [T][ceil(max_q / 64)] (bit j: the row sees node j of its sequence: itself and
+        its ancestors) and depths int32 [T] of trees given by parents int32 [T]: the index of each
+        row's parent among its sequence's rows (smaller than its own), -1 for none."""
+        if not isinstance(parents, torch.Tensor) or parents.dim() != 1:
+            raise ValueError("parents must be [tokens]")
+        _dev(parents, torch.int32, "parents")
+        T = parents.shape[0]
+        _counts(T, max_q)
+        _on(cu_q, torch.int32, "cu_q", (cu_q.shape[0],), parents.device)
+        if cu_q.dim() != 1 or cu_q.shape[0] < 1:
+            raise ValueError("cu_q must be [sequences + 1]")
+        words = max((max_q + 63) // 64, 1)
+        mask = torch.zeros((T, words), dtype=torch.int64, device=parents.device)
+        depth = torch.zeros((T,), dtype=torch.int32, device=parents.device)
+        if T:
+            self._check(self._lib.tabit_tree_mask(
+                self._h, parents.data_ptr(), T, cu_q.data_ptr(), cu_q.shape[0] - 1, max_q, mask.data_ptr(),
+                words, depth.data_ptr(), _stream(parents.device)))
+        return mask, depth
+
+    def kv_tree_attention_workspace(self, cache: KVCache, q: torch.Tensor, num_seqs: int, max_q: int,
+                                    max_kv: int) -> Optional[torch.Tensor]:
+        """A workspace for such calls (None where none is needed)."""
+        return self._rows_workspace(self._lib.tabit_kv_tree_attention_workspace_bytes, cache, q, num_seqs,
+                                    max_q, max_kv)
+
+    def kv_tree_attention(self, cache: KVCache, q: torch.Tensor, mask: torch.Tensor, cu_q: torch.Tensor,
+                          block_table: torch.Tensor, kv_lens: torch.Tensor, max_q: int, max_kv: int,
+                          scale: Optional[float] = None, rope: Optional[Rope] = None,
+                          positions: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                          lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Softmax attention of trees of drafted tokens: as kv_attention, but row i of a sequence's n
+        sees the tokens before the last n, and of those the nodes that its row of mask (int64
+        [T][words], bit j % 64 of word j / 64 for node j; see tree_mask) names."""
+        dev = cache.device
+        if out is None and isinstance(q, torch.Tensor):
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        B = kv_lens.shape[0]
+        if ws is None and isinstance(q, torch.Tensor) and q.dim() == 3 and q.shape[0] and B:
+            ws = self.kv_tree_attention_workspace(cache, q, B, max_q, max_kv)
+        a = self._rows_args(cache, q, cu_q, block_table, kv_lens, max_q, max_kv, scale, False, rope, positions,
+                            out, lse, ws)
+        T = a.num_tokens
+        _on(out, torch.bfloat16, "out", (T, q.shape[1], cache.head_dim), dev)
+        if not isinstance(mask, torch.Tensor) or mask.dim() != 2:
+            raise ValueError("mask must be [tokens][words]")
+        _on(mask, torch.int64, "mask", (T, mask.shape[1]), dev)
+        if T and B:
+            self._check(self._lib.tabit_kv_tree_attention(self._h, cache._ref, ctypes.addressof(a),
+                                                          mask.data_ptr(), mask.shape[1], _stream(dev)))
+        return out
+
+    # ------------------------------------------------------------ eviction
+    def kv_sums(self, cache: KVCache) -> torch.Tensor:
+        """Zeros for the accumulated attention weights of a cache's tokens, a number a key head."""
+        return torch.zeros((cache.num_pages, cache.num_kv_heads, cache.page_size), dtype=torch.float32,
+                           device=cache.device)
+
+    def _sums(self, cache: KVCache, sums) -> None:
+        _on(sums, torch.float32, "sums", (cache.num_pages, cache.num_kv_heads, cache.page_size), cache.device)
+
+    def kv_weigh_workspace(self, cache: KVCache, q: torch.Tensor, num_seqs: int, max_q: int,
+                           max_kv: int) -> Optional[torch.Tensor]:
+        """A workspace for such calls."""
+        return self._rows_workspace(self._lib.tabit_kv_weigh_workspace_bytes, cache, q, num_seqs, max_q, max_kv)
+
+    def kv_weigh(self, cache: KVCache, sums: torch.Tensor, q: torch.Tensor, cu_q: torch.Tensor,
+                 block_table: torch.Tensor, kv_lens: torch.Tensor, max_q: int, max_kv: int,
+                 scale: Optional[float] = None, causal: bool = True, rope: Optional[Rope] = None,
+                 positions: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                 ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Add to sums (fp32 [pages][kv_heads][page_size], see kv_sums) the attention weights that the
+        rows q give to the cached tokens; with causal, the sums of a sequence's last n tokens (n
+        its rows) are set instead.  Arguments as kv_attention; lse fp32 [T][q_heads] is filled if
+        given.  Returns sums."""
+        B = kv_lens.shape[0]
+        if ws is None and isinstance(q, torch.Tensor) and q.dim() == 3 and q.shape[0] and B:
+            ws = self.kv_weigh_workspace(cache, q, B, max_q, max_kv)
+        a = self._rows_args(cache, q, cu_q, block_table, kv_lens, max_q, max_kv, scale, causal, rope, positions,
+                            None, lse, ws)
+        self._sums(cache, sums)
+        if a.num_tokens and B:
+            self._check(self._lib.tabit_kv_weigh(self._h, cache._ref, ctypes.addressof(a), sums.data_ptr(),
+                                                 _stream(cache.device)))
+        return sums
+
+    def kv_evict(self, cache: KVCache, sums: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                 max_kv: int, budget: int, sinks: int = 0, recent: int = 0):
+        """Which tokens each head keeps of sequences longer than budget: the first sinks, the last
+        recent and the largest sums between.  Returns (keep int32 [B][kv_heads][budget], rising, -1
+        behind the last; new lengths int32 [B]); kv_compact then moves them."""
+        dev, B = cache.device, kv_lens.shape[0]
+        _counts(B, max_kv, budget, sinks, recent)
+        self._sums(cache, sums)
+        _on(kv_lens, torch.int32, "kv_lens", (B,), dev)
+        _on(block_table, torch.int32, "block_table", (B, block_table.shape[1]), dev)
+        keep = torch.empty((B, cache.num_kv_heads, max(budget, 0)), dtype=torch.int32, device=dev)
+        lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        if B:
+            self._check(self._lib.tabit_kv_evict(
+                self._h, cache._ref, sums.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+                kv_lens.data_ptr(), B, max_kv, budget, sinks, recent, keep.data_ptr(), lens.data_ptr(),
+                _stream(dev)))
+        return keep, lens
+
+    def kv_compact_workspace(self, cache: KVCache, num_seqs: int, most: int) -> Optional[torch.Tensor]:
+        """A workspace for kv_compact calls of num_seqs lists of up to `most` tokens."""
+        _counts(num_seqs, most)
+        n = int(self._lib.tabit_kv_compact_workspace_bytes(num_seqs, cache.num_kv_heads, cache.head_dim, most))
+        return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
+
+    def kv_compact(self, cache: KVCache, block_table: torch.Tensor, keep: torch.Tensor, counts: torch.Tensor,
+                   starts: Optional[torch.Tensor] = None, sums: Optional[torch.Tensor] = None,
+                   ws: Optional[torch.Tensor] = None) -> None:
+        """Move tokens inside their sequences: token starts[b] + j becomes what token keep[b][h][j] was,
+        j < counts[b], with its sum where sums are given.  keep int32 [B][kv_heads or 1][most], each
+        list rising and none before its place; counts, starts (None: 0) int32 [B]."""
+        dev = cache.device
+        if not isinstance(keep, torch.Tensor) or keep.dim() != 3:
+            raise ValueError("keep must be [sequences][kv_heads or 1][tokens]")
+        B, heads, most = keep.shape
+        _counts(B, most)
+        _on(keep, torch.int32, "keep", (B, heads, most), dev)
+        _on(counts, torch.int32, "counts", (B,), dev)
+        _on(block_table, torch.int32, "block_table", (B, block_table.shape[1]), dev)
+        if starts is not None:
+            _on(starts, torch.int32, "starts", (B,), dev)
+        if sums is not None:
+            self._sums(cache, sums)
+        if B == 0 or most == 0:
+            return
+        if ws is None:
+            ws = self.kv_compact_workspace(cache, B, most)
+        elif ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be contiguous and on {dev}")
+        self._check(self._lib.tabit_kv_compact(
+            self._h, cache._ref, block_table.data_ptr(), block_table.shape[1], B, keep.data_ptr(), heads, most,
+            counts.data_ptr(), _ptr(starts), _ptr(sums), _ptr(ws),
+            0 if ws is None else ws.numel() * ws.element_size(), _stream(dev)))
+
+    # ------------------------------------------------------------ adapters
+    def adapter_rotate(self, a: torch.Tensor, had_block: int, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """A matrices bf16 [..][K] of adapters, transformed for rows that are quantized after a block
+        Hadamard transform: (1 / b) A H, rounded to bf16."""
+        _dev(a, torch.bfloat16, "a")
+        if a.dim() < 1:
+            raise ValueError("a must be [..][K]")
+        out = torch.empty_like(a) if out is None else out
+        _on(out, torch.bfloat16, "out", a.shape, a.device)
+        rows = a.numel() // a.shape[-1] if a.numel() else 0
+        _counts(rows, a.shape[-1])
+        if rows:
+            self._check(self._lib.tabit_adapter_rotate(self._h, a.data_ptr(), rows, a.shape[-1], had_block,
+                                                       out.data_ptr(), _stream(a.device)))
+        return out
+
+    def adapter_workspace(self, adapters: Adapters, x: torch.Tensor, num_segments: int) -> Optional[torch.Tensor]:
+        """A workspace for adapter_linear calls of as many rows."""
+        _counts(x.shape[0], num_segments)
+        n = int(self._lib.tabit_adapter_workspace_bytes(x.shape[0], adapters.rank, num_segments))
+        return torch.empty(n, dtype=torch.uint8, device=adapters.device) if n else None
+
+    def adapter_linear(self, adapters: Adapters, x: torch.Tensor, y: torch.Tensor, cu_rows: torch.Tensor,
+                       which: torch.Tensor, x_scale: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """out = y + scale (x A^T) B^T, with the adapter which[i] of the rows [cu_rows[i], cu_rows[i+1]).
+
+        x bf16 [T][K] (rows of any stride of 8 elements), int8 [T][K] with x_scale fp32 [T], or packed
+        uint8 [T][K/2] with x_scale E8M0 uint8 [T][K/32]: what the projection reads.  y bf16
+        [T][N], the projection's output; out may be y.  cu_rows int32 [S+1], which int32 [S] (outside
+        the adapters: out = y).  Rows of no segment are left unwritten in out.
+        """
+        dev, K, N = adapters.device, adapters.K, adapters.N
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            raise ValueError("x must be [rows][features]")
+        T, xs = x.shape[0], K
+        if x.dtype == torch.bfloat16:
+            fmt, xs = FMT_BF16, _matrix(x, "x", K, dev)
+            if x_scale is not None:
+                raise ValueError("bf16 rows have no scales")
+        elif x.dtype == torch.int8:
+            fmt = FMT_INT8
+            _on(x, torch.int8, "x", (T, K), dev)
+            _on(x_scale, torch.float32, "x_scale", (T,), dev)
+        else:
+            fmt = FMT_MXFP4
+            _on(x, torch.uint8, "x", (T, K // 2), dev)
+            _on(x_scale, torch.uint8, "x_scale", (T, K // 32), dev)
+        ys = _matrix(y, "y", N, dev)
+        if y.shape[0] != T:
+            raise ValueError("x and y disagree on the number of rows")
+        if out is None:
+            out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+        os_ = _matrix(out, "out", N, dev)
+        if out.shape[0] != T:
+            raise ValueError("x and out disagree on the number of rows")
+        S = which.shape[0]
+        _counts(T, S, K, N)
+        _on(which, torch.int32, "which", (S,), dev)
+        _on(cu_rows, torch.int32, "cu_rows", (S + 1,), dev)
+        if T == 0 or S == 0:
+            return out
+        if ws is None:
+            ws = self.adapter_workspace(adapters, x, S)
+        elif ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be contiguous and on {dev}")
+        a = _AdapterArgs(x.data_ptr(), _ptr(x_scale), fmt, T, K, N, xs, adapters.a.data_ptr(),
+                         adapters.b.data_ptr(), _ptr(adapters.scale), adapters.num, adapters.rank,
+                         cu_rows.data_ptr(), which.data_ptr(), S, y.data_ptr(), ys, out.data_ptr(), os_,
+                         _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+        self._check(self._lib.tabit_adapter_linear(self._h, ctypes.addressof(a), _stream(dev)))
         return out
 
     def block_norm(self, x: torch.Tensor, y: Optional[torch.Tensor] = None, post: int = NORM_NONE,

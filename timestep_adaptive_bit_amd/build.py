@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libtabit.so")
 SOURCES = ["api.hip", "quant.hip", "gemm_i8.hip", "gemm_mxfp4.hip", "gemm_planes.hip", "dmpq.hip",
            "gemm_hqdm.hip", "probe.hip", "api_block.hip", "kv_cache.hip", "kv_attention.hip",
-           "block_norm.hip"]
+           "block_norm.hip", "api_serve.hip", "kv_tree.hip", "kv_weigh.hip", "kv_evict.hip", "adapter.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -42,7 +42,7 @@
 // Long caches are split over workgroups (`splits` ranges of whole 64-key tiles of
 // each sequence's own length) whose fp32 partial sums a second kernel joins.
 #include "../../include/tabit.h"
-#include "kv_common.h"
+#include "kv_query.h"
 #include "tile_common.h"
 
 namespace tabit {
@@ -120,103 +120,6 @@ __device__ __forceinline__ int v_off(int key, int c, int half) {
   return key * RS + ((c ^ x) << 5) + ((half ^ ((key >> 3) & 1)) << 4);
 }
 
-// Factor of the products q'.k' that gives scores in base 2.
-__device__ __forceinline__ float base2_scale(const KvAttnArgs& a) {
-  return a.scale * 1.4426950408889634f / (a.cache.had ? 32.0f : 1.0f);
-}
-
-// 32 elements of a query row (block `blk` of the head vector), rotated and
-// transformed as the cache's keys are, times `factor`.  All loads are issued before
-// the first use: elements past the head, and tables outside the rotated part, are
-// read at a valid place and replaced.
-__device__ __forceinline__ bool load_q_block(const KvAttnArgs& a, int token, int head, int blk,
-                                             float factor, float (&x)[32]) {
-  const int D = a.cache.head_dim, R = a.rope.rope_dim;
-  const uint16_t* p = a.q + (long long)token * a.q_stride + (long long)head * D;
-  bool ok = true;
-  uint4 own[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e0 = blk * 32 + i * 8;
-    own[i] = *reinterpret_cast<const uint4*>(p + (e0 < D ? e0 : 0));
-  }
-  auto spread = [](uint4 w, float* v) {
-    v[0] = bf_lo(w.x); v[1] = bf_hi(w.x); v[2] = bf_lo(w.y); v[3] = bf_hi(w.y);
-    v[4] = bf_lo(w.z); v[5] = bf_hi(w.z); v[6] = bf_lo(w.w); v[7] = bf_hi(w.w);
-  };
-  if (R > 0) {
-    const int pos = a.positions[token];
-    ok = pos >= 0 && pos < a.rope.num_positions;
-    const int half = R >> 1;
-    const float* cos = a.rope.cos + (ok ? (size_t)pos * half : 0);
-    const float* sin = a.rope.sin + (ok ? (size_t)pos * half : 0);
-    if (a.rope.interleaved) {
-      float4 c[4], s[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e0 = blk * 32 + i * 8, at = e0 < R ? e0 >> 1 : 0;
-        c[i] = *reinterpret_cast<const float4*>(cos + at);
-        s[i] = *reinterpret_cast<const float4*>(sin + at);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        spread(own[i], x + 8 * i);
-        if (blk * 32 + i * 8 < R) {
-          turn(x[8 * i], x[8 * i + 1], c[i].x, s[i].x);
-          turn(x[8 * i + 2], x[8 * i + 3], c[i].y, s[i].y);
-          turn(x[8 * i + 4], x[8 * i + 5], c[i].z, s[i].z);
-          turn(x[8 * i + 6], x[8 * i + 7], c[i].w, s[i].w);
-        }
-      }
-    } else {
-      uint4 other[4];
-      float4 c[8], s[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e0 = blk * 32 + i * 8;
-        const bool second = e0 >= half;
-        const int at = e0 < R ? (second ? e0 - half : e0) : 0;
-        other[i] = *reinterpret_cast<const uint4*>(p + (e0 < R ? (second ? e0 - half : e0 + half) : 0));
-        const uint32_t sign = second ? 0u : 0x80008000u;   // the first of a pair takes -other sin
-        other[i] = make_uint4(other[i].x ^ sign, other[i].y ^ sign, other[i].z ^ sign, other[i].w ^ sign);
-        c[2 * i] = *reinterpret_cast<const float4*>(cos + at);
-        c[2 * i + 1] = *reinterpret_cast<const float4*>(cos + at + 4);
-        s[2 * i] = *reinterpret_cast<const float4*>(sin + at);
-        s[2 * i + 1] = *reinterpret_cast<const float4*>(sin + at + 4);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e0 = blk * 32 + i * 8;
-        spread(own[i], x + 8 * i);
-        float y[8];
-        spread(other[i], y);
-        const float cc[8] = {c[2 * i].x, c[2 * i].y, c[2 * i].z, c[2 * i].w,
-                             c[2 * i + 1].x, c[2 * i + 1].y, c[2 * i + 1].z, c[2 * i + 1].w};
-        const float ss[8] = {s[2 * i].x, s[2 * i].y, s[2 * i].z, s[2 * i].w,
-                             s[2 * i + 1].x, s[2 * i + 1].y, s[2 * i + 1].z, s[2 * i + 1].w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float u = x[8 * i + e] * cc[e], w = y[e] * ss[e];
-          x[8 * i + e] = e0 >= R ? x[8 * i + e] : u + w;
-        }
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) spread(own[i], x + 8 * i);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (blk * 32 + i * 8 >= D) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[8 * i + e] = 0.0f;
-    }
-  if (a.cache.had) fwht32_lane(x);
-#pragma unroll
-  for (int e = 0; e < 32; ++e) x[e] *= factor;
-  return ok;
-}
-
 // Three FP6 terms of a block of 32 with their E8M0 bytes (bytes 0..2 of `scales`).
 // A block that is not `ok` or not finite gets scale 255 (not a number) for whatever its
 // codes are: its row answers NaN.  An infinity shows in the largest magnitude, NaN in
@@ -280,23 +183,6 @@ __device__ __forceinline__ float2* part_stats(const KvAttnArgs& a, int sp, long 
   return reinterpret_cast<float2*>(a.part + (long long)a.splits * rows * a.cache.dim_pad) + sp * rows + row;
 }
 
-// First query row of sequence b, its queries, inside [0, tokens], and how many of them are
-// computed.
-__device__ __forceinline__ void seq_rows(const KvAttnArgs& a, int b, int& q0, int& all, int& n) {
-  q0 = min(max(a.cu_q[b], 0), a.tokens);
-  all = max(min(a.cu_q[b + 1], a.tokens) - q0, 0);
-  n = min(all, a.max_q);
-}
-
-__device__ __forceinline__ int seq_keys(const KvAttnArgs& a, int b) {
-  return min(max(a.kv_lens[b], 0), a.max_kv);
-}
-
-// Keys that query i of `all` sees, of `len`.
-__device__ __forceinline__ int seen_keys(const KvAttnArgs& a, int len, int all, int i) {
-  return a.causal ? min(max(len - all + i + 1, 0), len) : len;
-}
-
 // One workgroup: 16 rows (queries x heads of the group) of one key head of one
 // sequence over one range of its keys; the range's tiles go to the waves in runs and
 // every wave works by itself until the end.  Bound by the cache's bytes: a wave asks
@@ -311,7 +197,7 @@ __device__ __forceinline__ int seen_keys(const KvAttnArgs& a, int len, int all, 
 // workgroup's start costs 6 us (bounds, pages, then codes and tables: three loads that
 // depend on each other), which is what short caches take.  Six, eight or twelve waves a
 // workgroup level out ragged batches but fill the chip less: 99 to 112 us for 97 then.
-template <int NB>
+template <int NB, bool TREE>
 __global__ void __launch_bounds__(256, 3)
 kv_attention_rows16_kernel(KvAttnArgs a) {
   constexpr int NW = 4;
@@ -337,7 +223,9 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
   const int qi = (r0 + row) / a.group, qh = hk * a.group + (r0 + row) % a.group;
   const bool row_ok = qi < n;
   const int last = (min(r0 + 16, n * a.group) - 1) / a.group;
-  const int seen_hi = seen_keys(a, len, all, last), seen_lo = seen_keys(a, len, all, r0 / a.group);
+  const int seen_hi = seen_keys(a, len, all, last);
+  const int seen_lo = TREE ? before_tree(len, all) : seen_keys(a, len, all, r0 / a.group);
+  const uint64_t* seen_nodes = TREE ? a.mask + (long long)(q0 + min(qi, n - 1)) * a.mask_words : nullptr;
   const int seen = row_ok ? seen_keys(a, len, all, qi) : seen_hi;     // idle rows hide nothing
 
   int t0, t1;
@@ -526,6 +414,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
     // lane: keys 16 k + 4 g + r of its row
     if (seen_lo - j0 < TILE || holes) {
       const int left = seen - j0 - 4 * g;
+      const uint64_t nodes = TREE ? nodes_from(seen_nodes, a.mask_words, j0 - (len - all)) >> (4 * g) : 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int pi = (j0 + 16 * k) >> c.page_shift;
@@ -533,7 +422,7 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
         const int mine = there ? left : 0;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (16 * k + r >= mine) s[k][r] = kNegInf;
+          if (16 * k + r >= mine || (TREE && !(nodes >> (16 * k + r) & 1))) s[k][r] = kNegInf;
       }
     }
     // weights: as in the kernel for 128 rows, 2^(s - ref) with a reference only where needed
@@ -737,7 +626,7 @@ __device__ __forceinline__ v16f score_term(v4i x, const v8i& q, v16f s, int byte
 // would spill: 485 us for 409); 96 and 128 elements take 204 and 232 registers, two
 // workgroups (three spill: 38 us for 30 at 72 elements).  Seeing value scales far from one and
 // keeping sums in range for them costs the first 1.2%, short chunks 1.5%, causal turns nothing.
-template <int NB>
+template <int NB, bool TREE>
 __global__ void __launch_bounds__(256, NB <= 2 ? 3 : 2)
 kv_attention_rows128_kernel(KvAttnArgs a) {
   constexpr int NW = 4, ROWS = NW * 32;              // waves, rows
@@ -781,7 +670,8 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   const int seen_all = seen_keys(a, len, all, (min(r0 + ROWS, rows) - 1) / a.group);
   const int seen = row_ok ? seen_keys(a, len, all, qi) : seen_all;   // idle rows mask nothing
   const int first = r0 + wave * 32;
-  const int seen_lo = seen_keys(a, len, all, min(first, rows - 1) / a.group);
+  const int seen_lo = TREE ? before_tree(len, all) : seen_keys(a, len, all, min(first, rows - 1) / a.group);
+  const uint64_t* seen_nodes = TREE ? a.mask + (long long)(q0 + min(qi, n - 1)) * a.mask_words : nullptr;
   const int seen_hi = first < rows ? seen_keys(a, len, all, min(first + 31, rows - 1) / a.group) : 0;
 
   int t0, t1;
@@ -1047,6 +937,7 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
       const bool any_far = __any(scores(s, sc) != 0);
       if (seen_lo - j0 < TILE || holes) {
         const int left = seen - j0 - half * 4;
+        const uint64_t nodes = TREE ? nodes_from(seen_nodes, a.mask_words, j0 - (len - all)) >> (4 * half) : 0;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -1056,7 +947,9 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
             const int mine = there ? left : 0;
 #pragma unroll
             for (int r = g * 8; r < g * 8 + 8; ++r)
-              if (kb * 32 + (r >> 2) * 8 + (r & 3) >= mine) sc[kb][r] = kNegInf;
+              if (kb * 32 + (r >> 2) * 8 + (r & 3) >= mine ||
+                  (TREE && !(nodes >> (kb * 32 + (r >> 2) * 8 + (r & 3)) & 1)))
+                sc[kb][r] = kNegInf;
           }
       }
       if (any_ref) {
@@ -1292,7 +1185,7 @@ kv_attention_join_kernel(KvAttnArgs a) {
 // keys 43 and 51; at 16 sequences of 64 rows x 8192 keys 89 and 68 us.
 inline bool few_rows(int max_q, int group) { return (long long)max_q * group <= 16; }
 
-template <int NB>
+template <int NB, bool TREE>
 hipError_t launch_nb(const KvAttnArgs& a, hipStream_t s) {
   const bool few = few_rows(a.max_q, a.group);
   const int per = few ? 16 : 128;
@@ -1300,7 +1193,7 @@ hipError_t launch_nb(const KvAttnArgs& a, hipStream_t s) {
   const unsigned per_head = (unsigned)((long long)row_tiles * a.splits);
   hipError_t e = hipSuccess;
   if (few) {
-    kv_attention_rows16_kernel<NB><<<dim3(per_head, (unsigned)a.cache.heads, (unsigned)a.seqs), 256, 0, s>>>(a);
+    kv_attention_rows16_kernel<NB, TREE><<<dim3(per_head, (unsigned)a.cache.heads, (unsigned)a.seqs), 256, 0, s>>>(a);
     e = hipGetLastError();
   } else {
     // one axis, which is limited to 2^32 threads: as many sequences a launch as fit
@@ -1312,7 +1205,7 @@ hipError_t launch_nb(const KvAttnArgs& a, hipStream_t s) {
       part.cu_q += first;
       part.kv_lens += first;
       part.table += (long long)first * a.table_stride;
-      kv_attention_rows128_kernel<NB><<<(unsigned)(per_seq * part.seqs), 256, 0, s>>>(part);
+      kv_attention_rows128_kernel<NB, TREE><<<(unsigned)(per_seq * part.seqs), 256, 0, s>>>(part);
       e = hipGetLastError();
     }
   }
@@ -1371,14 +1264,23 @@ int kv_attention_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_
   return splits;
 }
 
-hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t s) {
+template <bool TREE>
+static hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
   switch (a.cache.dim_pad) {
-    case 32: return launch_nb<1>(a, s);
-    case 64: return launch_nb<2>(a, s);
-    case 96: return launch_nb<3>(a, s);
-    case 128: return launch_nb<4>(a, s);
+    case 32: return launch_nb<1, TREE>(a, s);
+    case 64: return launch_nb<2, TREE>(a, s);
+    case 96: return launch_nb<3, TREE>(a, s);
+    case 128: return launch_nb<4, TREE>(a, s);
     default: return hipErrorInvalidValue;
   }
 }
+
+hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t s) { return launch<false>(a, s); }
+
+int kv_tree_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_kv) {
+  return kv_attention_splits(seqs, max_q, q_heads, kv_heads, max_kv);
+}
+
+hipError_t launch_kv_tree_attention(const KvAttnArgs& a, hipStream_t s) { return launch<true>(a, s); }
 
 }  // namespace tabit

@@ -141,10 +141,65 @@ struct KvAttnArgs {
   float* lse;
   float* part;
   int splits;
+  const uint64_t* mask;    // trees: [tokens][mask_words]
+  int mask_words;
 };
 // Number of ranges the keys of one sequence are split into for this problem.
 int kv_attention_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_kv);
 hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t s);
+
+// Trees of drafted tokens: the same with a.mask, a.mask_words.
+int kv_tree_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_kv);
+hipError_t launch_kv_tree_attention(const KvAttnArgs& a, hipStream_t s);
+hipError_t launch_tree_mask(const int* parents, int tokens, const int* cu_q, int seqs, int max_q,
+                            uint64_t* mask, int mask_words, int* depth, hipStream_t s);
+
+// ---------------------------------------------------------------- eviction
+// Sums [num_pages][heads][2^page_shift] += the rows' attention weights; a.part is the workspace.
+size_t kv_weigh_workspace(int tokens, int q_heads, int kv_heads, int dim_pad, int seqs, int max_q, int max_kv);
+hipError_t launch_kv_weigh(const KvAttnArgs& a, float* sums, hipStream_t s);
+
+struct KvEvictArgs {
+  KvCacheArgs cache;
+  const float* sums;
+  const int *table, *kv_lens;
+  int table_stride, seqs, max_kv, budget, sinks, recent;
+  int *keep, *new_lens;
+};
+hipError_t launch_kv_evict(const KvEvictArgs& a, hipStream_t s);
+
+struct KvCompactArgs {
+  KvCacheArgs cache;
+  const int* table;
+  int table_stride, seqs;
+  const int* keep;
+  int keep_heads, keep_stride;
+  const int *counts, *starts;    // starts may be null
+  float* sums;                   // may be null
+  uint8_t* ws;
+};
+size_t kv_compact_workspace(int seqs, int heads, int dim_pad, int keep_stride);
+hipError_t launch_kv_compact(const KvCompactArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------- low-rank adapters
+struct AdapterArgs {
+  const void *x, *x_scale;
+  int x_fmt, rows, K, N;
+  long long x_stride;
+  const uint16_t *a, *b;
+  const float* scale;            // may be null
+  int num_adapters, rank;
+  const int *cu_rows, *adapter;
+  int segments;
+  const uint16_t* y;
+  long long y_stride;
+  uint16_t* out;
+  long long out_stride;
+  uint16_t *hi, *lo;             // workspace: x A^T in two bf16 terms, [rows][rank] each
+};
+hipError_t launch_adapter_linear(const AdapterArgs& a, hipStream_t s);
+hipError_t launch_adapter_rotate(const uint16_t* a, int rows, int K, int had_block, uint16_t* out,
+                                 hipStream_t s);
 
 // ---------------------------------------------------------------- block norms
 struct BlockNormArgs {
