@@ -694,11 +694,14 @@ size_t tabit_kv_weigh_workspace_bytes(int num_tokens, int num_q_heads, int num_k
  *   keep         device int32 [num_seqs][num_kv_heads][budget] output: the kept tokens'
  *                indexes in their order, then -1
  *   new_lens     device int32 [num_seqs] output: min(kv_len, budget)
+ *   ws           device workspace of tabit_kv_evict_workspace_bytes bytes, 16-byte aligned (NULL
+ *                when that is 0)
  * sinks + recent at most budget.
  */
 int tabit_kv_evict(tabit_ctx* ctx, const tabit_kv_cache* cache, const float* sums, const int32_t* block_table,
                    int table_stride, const int32_t* kv_lens, int num_seqs, int max_kv, int budget, int sinks,
-                   int recent, int32_t* keep, int32_t* new_lens, void* stream);
+                   int recent, int32_t* keep, int32_t* new_lens, void* ws, size_t ws_bytes, void* stream);
+size_t tabit_kv_evict_workspace_bytes(int num_seqs, int num_kv_heads, int max_kv);
 
 /*
  * Moves tokens inside the cache, in place: of each sequence b and key head h, token
@@ -713,7 +716,8 @@ int tabit_kv_evict(tabit_ctx* ctx, const tabit_kv_cache* cache, const float* sum
  *   counts      device int32 [num_seqs], taken as at most keep_stride
  *   starts      device int32 [num_seqs] or NULL (0)
  *   sums        device fp32 [num_pages][num_kv_heads][page_size] or NULL
- *   ws          device workspace of tabit_kv_compact_workspace_bytes bytes, 16-byte aligned
+ *   ws          device workspace of tabit_kv_compact_workspace_bytes bytes, 16-byte aligned (NULL
+ *               when that is 0)
  * Tokens behind the last place are left as they are.  Pages of the sequences of a call must
  * be distinct.
  */

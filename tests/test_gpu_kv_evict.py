@@ -198,7 +198,8 @@ def _sums(rng, kind, shape):
     ([1], 1, 0, 0, 16), ([2], 1, 0, 1, 16), ([100, 7, 0, 33], 8, 2, 3, 16), ([100, 99], 99, 0, 0, 32), ([500], 400, 4, 64, 16),
     ([1000, 1001, 999], 1, 1, 0, 16), ([300], 20, 10, 10, 128), ([4096, 4097, 5000], 1024, 4, 100, 64),
     ([8192, 8191, 100], 2048, 0, 0, 16), ([8193, 20000], 3000, 4, 500, 16), ([40000], 39999, 0, 7, 64), ([9000], 9001, 0, 0, 16),
-    ([70000], 257, 1, 5, 1024),
+    ([70000], 257, 1, 5, 1024), ([8193], 8192, 0, 0, 16), ([140000, 30], 20000, 4, 9000, 64), ([16384, 8192], 4000, 0, 4000, 16),
+    ([16385], 100, 50, 50, 32),
 ])
 @pytest.mark.parametrize("kind", ["spread", "ties", "equal", "all"])
 def test_kept_lists(ctx, lens, budget, sinks, recent, ps, kind):
@@ -244,6 +245,7 @@ def _noise(rng, pages, ps, hk, D):
     (1, 64, 16, [40], 12, False, False), (2, 128, 16, [300, 20, 5], 64, False, False), (3, 96, 32, [100, 90], 50, True, True),
     (2, 8, 16, [33], 33, False, True), (5, 40, 64, [500, 700], 400, False, False), (8, 128, 16, [2000], 1500, False, False),
     (2, 72, 16, [64, 1], 7, True, True), (40, 128, 16, [200] * 8, 60, False, False), (130, 64, 16, [90, 95], 80, False, True),
+    (64, 32, 16, [5000], 4500, False, True), (2, 64, 16, [2100], 2060, True, False), (33, 96, 32, [2500, 4200], 4100, False, False),
 ])
 @pytest.mark.parametrize("with_sums", [True, False])
 def test_moves(ctx, hk, D, ps, lens, most, shared, starts, with_sums):

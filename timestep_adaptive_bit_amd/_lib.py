@@ -105,7 +105,9 @@ _SIGNATURES = {
     "tabit_kv_weigh": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
     "tabit_kv_weigh_workspace_bytes": (_c_size_t, [_c_int] * 7),
     "tabit_kv_evict": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_int,
-                                _c_int, _c_int, _c_int, _c_int, _c_void_p, _c_void_p, _c_void_p]),
+                                _c_int, _c_int, _c_int, _c_int, _c_void_p, _c_void_p, _c_void_p,
+                                _c_size_t, _c_void_p]),
+    "tabit_kv_evict_workspace_bytes": (_c_size_t, [_c_int] * 3),
     "tabit_kv_compact": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_void_p, _c_int,
                                   _c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_size_t,
                                   _c_void_p]),
@@ -1030,8 +1032,14 @@ class Context:
                                                  _stream(cache.device)))
         return sums
 
+    def kv_evict_workspace(self, cache: KVCache, num_seqs: int, max_kv: int) -> Optional[torch.Tensor]:
+        """A workspace for such kv_evict calls (None where none is needed)."""
+        _counts(num_seqs, max_kv)
+        n = int(self._lib.tabit_kv_evict_workspace_bytes(num_seqs, cache.num_kv_heads, max_kv))
+        return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
+
     def kv_evict(self, cache: KVCache, sums: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
-                 max_kv: int, budget: int, sinks: int = 0, recent: int = 0):
+                 max_kv: int, budget: int, sinks: int = 0, recent: int = 0, ws: Optional[torch.Tensor] = None):
         """Which tokens each head keeps of sequences longer than budget: the first sinks, the last
         recent and the largest sums between.  Returns (keep int32 [B][kv_heads][budget], rising, -1
         behind the last; new lengths int32 [B]); kv_compact then moves them."""
@@ -1043,14 +1051,19 @@ class Context:
         keep = torch.empty((B, cache.num_kv_heads, max(budget, 0)), dtype=torch.int32, device=dev)
         lens = torch.empty((B,), dtype=torch.int32, device=dev)
         if B:
+            if ws is None:
+                ws = self.kv_evict_workspace(cache, B, max_kv)
+            elif ws.device != dev or not ws.is_contiguous():
+                raise ValueError(f"ws must be contiguous and on {dev}")
             self._check(self._lib.tabit_kv_evict(
                 self._h, cache._ref, sums.data_ptr(), block_table.data_ptr(), block_table.shape[1],
                 kv_lens.data_ptr(), B, max_kv, budget, sinks, recent, keep.data_ptr(), lens.data_ptr(),
-                _stream(dev)))
+                _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(dev)))
         return keep, lens
 
     def kv_compact_workspace(self, cache: KVCache, num_seqs: int, most: int) -> Optional[torch.Tensor]:
-        """A workspace for kv_compact calls of num_seqs lists of up to `most` tokens."""
+        """A workspace for kv_compact calls of num_seqs lists of up to `most` tokens (None where none is
+        needed)."""
         _counts(num_seqs, most)
         n = int(self._lib.tabit_kv_compact_workspace_bytes(num_seqs, cache.num_kv_heads, cache.head_dim, most))
         return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None

@@ -127,9 +127,14 @@ int tabit_kv_weigh(tabit_ctx* ctx, const tabit_kv_cache* cache, const tabit_kv_a
   return hip_status(ctx, tabit::launch_kv_weigh(k, sums, static_cast<hipStream_t>(stream)), "kv_weigh launch");
 }
 
+size_t tabit_kv_evict_workspace_bytes(int num_seqs, int num_kv_heads, int max_kv) {
+  if (num_seqs <= 0 || num_kv_heads <= 0 || max_kv <= 0) return 0;
+  return tabit::kv_evict_workspace(num_seqs, num_kv_heads, max_kv);
+}
+
 int tabit_kv_evict(tabit_ctx* ctx, const tabit_kv_cache* cache, const float* sums, const int32_t* block_table,
                    int table_stride, const int32_t* kv_lens, int num_seqs, int max_kv, int budget, int sinks,
-                   int recent, int32_t* keep, int32_t* new_lens, void* stream) {
+                   int recent, int32_t* keep, int32_t* new_lens, void* ws, size_t ws_bytes, void* stream) {
   if (ctx == nullptr) return TABIT_EINVAL;
   tabit::KvEvictArgs k{};
   int st = check_cache(ctx, cache, &k.cache);
@@ -146,9 +151,12 @@ int tabit_kv_evict(tabit_ctx* ctx, const tabit_kv_cache* cache, const float* sum
   if (kv_lens == nullptr || keep == nullptr || new_lens == nullptr) return fail(ctx, TABIT_EINVAL, "null pointer");
   if (sums == nullptr && k.cache.num_pages > 0) return fail(ctx, TABIT_EINVAL, "null sums");
   if (!aligned(sums, 16) || !aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(keep, 4) ||
-      !aligned(new_lens, 4))
-    return fail(ctx, TABIT_EALIGN, "sums must be 16-byte aligned, the others 4-byte");
+      !aligned(new_lens, 4) || !aligned(ws, 16))
+    return fail(ctx, TABIT_EALIGN, "sums and ws must be 16-byte aligned, the others 4-byte");
   if (num_seqs == 0) return TABIT_OK;
+  if ((st = check_ws(ctx, ws, ws_bytes, tabit_kv_evict_workspace_bytes(num_seqs, k.cache.heads, max_kv))) != TABIT_OK)
+    return st;
+  k.ws = static_cast<uint8_t*>(ws);
   k.sums = sums;
   k.table = block_table;
   k.kv_lens = kv_lens;

@@ -165,7 +165,9 @@ struct KvEvictArgs {
   const int *table, *kv_lens;
   int table_stride, seqs, max_kv, budget, sinks, recent;
   int *keep, *new_lens;
+  uint8_t* ws;
 };
+size_t kv_evict_workspace(int seqs, int heads, int max_kv);
 hipError_t launch_kv_evict(const KvEvictArgs& a, hipStream_t s);
 
 struct KvCompactArgs {
