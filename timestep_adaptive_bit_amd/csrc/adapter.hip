@@ -6,11 +6,13 @@
 // Two kernels.  The first forms h = c s x A^T for tiles of rows of one segment and 16 to 64
 // of the adapter's ranks, its waves sharing the sum over K; h goes out as two bf16 terms (2^-16 of
 // itself is lost at most).  The second adds h B^T to y: the product starts from y in the
-// accumulator, so out is rounded once.  Both use the 16x16x32 bf16 MFMA with operands loaded from
-// memory as they lie: x and A (h and B) are contiguous along the summed axis, and a wave's tile
-// of A or B is read by nobody else in its workgroup, so LDS would only delay it.
+// accumulator, so out is rounded once.  Both use the 16x16x32 bf16 MFMA.  x, A and B come through LDS, straight from
+// memory by whole lines: loaded as the operands' lanes hold them, 16 rows in turn, each lane's 16 bytes
+// were a cache access of their own (60 an instruction; 17776 rows of 1920 to 5760 by rank 32 took 121 us
+// for the second kernel then, its address units busy throughout).
 #include "../../include/tabit.h"
 #include "kv_common.h"
+#include "tile_common.h"
 
 namespace tabit {
 namespace {
@@ -52,41 +54,53 @@ __device__ __forceinline__ bool find_tile(const AdapterArgs& a, int tile, int ro
 
 __device__ __forceinline__ v8bf zero8() { return __builtin_bit_cast(v8bf, make_uint4(0u, 0u, 0u, 0u)); }
 
-// 16 consecutive elements of a row of x, as two operands.
+typedef const __attribute__((address_space(1))) void* from_t;
+typedef __attribute__((address_space(3))) void* to_t;
+
+// Rows of PIECES 16-byte pieces in LDS: piece p of row i lies at place p ^ turned(i) of its row, so that
+// the 16 rows that 16 lanes read at once cover the banks' 256 bytes.
+template <int PIECES>
+__device__ __forceinline__ int turned(int i) {
+  return PIECES >= 16 ? i & 15 : (i / (16 / PIECES)) & (PIECES - 1);
+}
+template <int PIECES>
+__device__ __forceinline__ int place(int i, int p) { return (i * PIECES + (p ^ turned<PIECES>(i))) * 16; }
+
+// 64 elements of a row of x: PIECES of 16 bytes; get gives 16 consecutive ones, from 16 g on, as two
+// operands.
 template <int FMT>
 struct Rows;
 template <>
 struct Rows<TABIT_FMT_BF16> {
-  struct Raw { uint4 w[2]; };
-  static __device__ __forceinline__ Raw load(const AdapterArgs& a, int t, int k) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + t * a.x_stride + k);
-    return {p[0], p[1]};
+  static constexpr int PIECES = 8;
+  static __device__ __forceinline__ const void* at(const AdapterArgs& a, int t, int k) {
+    return static_cast<const uint16_t*>(a.x) + t * a.x_stride + k;
   }
-  static __device__ __forceinline__ void get(const Raw& r, v8bf (&x)[2]) {
-    x[0] = __builtin_bit_cast(v8bf, r.w[0]);
-    x[1] = __builtin_bit_cast(v8bf, r.w[1]);
+  static __device__ __forceinline__ void get(const uint8_t* lds, int i, int g, uint32_t, v8bf (&x)[2]) {
+    x[0] = *reinterpret_cast<const v8bf*>(lds + place<8>(i, 2 * g));
+    x[1] = *reinterpret_cast<const v8bf*>(lds + place<8>(i, 2 * g + 1));
   }
 };
 template <>
 struct Rows<TABIT_FMT_INT8> {
-  struct Raw { uint4 w; };
-  static __device__ __forceinline__ Raw load(const AdapterArgs& a, int t, int k) {
-    return {*reinterpret_cast<const uint4*>(static_cast<const int8_t*>(a.x) + (long long)t * a.K + k)};
+  static constexpr int PIECES = 4;
+  static __device__ __forceinline__ const void* at(const AdapterArgs& a, int t, int k) {
+    return static_cast<const int8_t*>(a.x) + (long long)t * a.K + k;
   }
   static __device__ __forceinline__ uint32_t pair(uint32_t w, int at) {
     return pack_bf16((float)(int8_t)(w >> at), (float)(int8_t)(w >> (at + 8)));
   }
-  static __device__ __forceinline__ void get(const Raw& r, v8bf (&x)[2]) {
-    x[0] = __builtin_bit_cast(v8bf, make_uint4(pair(r.w.x, 0), pair(r.w.x, 16), pair(r.w.y, 0), pair(r.w.y, 16)));
-    x[1] = __builtin_bit_cast(v8bf, make_uint4(pair(r.w.z, 0), pair(r.w.z, 16), pair(r.w.w, 0), pair(r.w.w, 16)));
+  static __device__ __forceinline__ void get(const uint8_t* lds, int i, int g, uint32_t, v8bf (&x)[2]) {
+    const uint4 w = *reinterpret_cast<const uint4*>(lds + place<4>(i, g));
+    x[0] = __builtin_bit_cast(v8bf, make_uint4(pair(w.x, 0), pair(w.x, 16), pair(w.y, 0), pair(w.y, 16)));
+    x[1] = __builtin_bit_cast(v8bf, make_uint4(pair(w.z, 0), pair(w.z, 16), pair(w.w, 0), pair(w.w, 16)));
   }
 };
 template <>
 struct Rows<TABIT_FMT_MXFP4> {
-  struct Raw { uint2 w; uint32_t scale; };
-  static __device__ __forceinline__ Raw load(const AdapterArgs& a, int t, int k) {
-    return {*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) + ((long long)t * a.K + k) / 2),
-            static_cast<const uint8_t*>(a.x_scale)[(long long)t * (a.K / 32) + k / 32]};
+  static constexpr int PIECES = 2;
+  static __device__ __forceinline__ const void* at(const AdapterArgs& a, int t, int k) {
+    return static_cast<const uint8_t*>(a.x) + ((long long)t * a.K + k) / 2;
   }
   static __device__ __forceinline__ v8bf eight(uint32_t w, uint32_t scale) {
     const float s = __uint_as_float(scale << 23);      // the conversion reads the exponent alone
@@ -98,20 +112,25 @@ struct Rows<TABIT_FMT_MXFP4> {
     if (scale == 255u) y = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
     return __builtin_bit_cast(v8bf, y);
   }
-  static __device__ __forceinline__ void get(const Raw& r, v8bf (&x)[2]) {
-    x[0] = eight(r.w.x, r.scale);
-    x[1] = eight(r.w.y, r.scale);
+  static __device__ __forceinline__ void get(const uint8_t* lds, int i, int g, uint32_t scale, v8bf (&x)[2]) {
+    const uint2 w = *reinterpret_cast<const uint2*>(lds + place<2>(i, g >> 1) + 8 * (g & 1));
+    x[0] = eight(w.x, scale);
+    x[1] = eight(w.y, scale);
   }
 };
 
-// h of 16 MR rows and 16 RB ranks.  A wave takes 64 elements of K at a time, every NW-th: lane l
-// holds row l % 16 of x (and rank l % 16 of A), 16 consecutive elements from 16 (l / 16) on, the
-// first eight for one product and the others for a second.
+// h of 16 MR rows and 16 RB ranks.  A wave takes 64 elements of K at a time, every NW-th, through LDS of its
+// own, a step ahead: lane l holds row l % 16 of x (and rank l % 16 of A), 16 consecutive elements from
+// 16 (l / 16) on, the first eight for one product and the others for a second.
 template <int FMT, int MR, int RB, int NW>
 __global__ void __launch_bounds__(NW * 64)
 adapter_down_kernel(AdapterArgs a) {
+  using X = Rows<FMT>;
   constexpr int ROWS = 16 * MR, RANKS = 16 * RB;
-  __shared__ float part[NW][ROWS][RANKS + 4];
+  constexpr int XB = ROWS * X::PIECES * 16, WB = RANKS * 128, STAGES = 2;
+  constexpr int XI = (XB + 1023) / 1024, WI = WB / 1024;             // instructions of a step
+  constexpr int PART = ROWS * (RANKS + 4) * 4, PER_WAVE = STAGES * (XB + WB) > PART ? STAGES * (XB + WB) : PART;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NW][PER_WAVE];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int seg, row0, row1;
@@ -121,27 +140,71 @@ adapter_down_kernel(AdapterArgs a) {
   if ((unsigned)ad >= (unsigned)a.num_adapters) return;
   const int r0 = blockIdx.x % blocks * RANKS;
   const int row = lane & 15, g = lane >> 4;
-  const uint16_t* ap = a.a + ((long long)ad * a.rank + r0 + row) * a.K;
+  // (asked for here, waited for at the end)
+  const float c = a.scale != nullptr ? a.scale[ad] : 1.0f;
+  constexpr int PAIRS = RANKS / 2, MINE = (ROWS * PAIRS + NW * 64 - 1) / (NW * 64);
+  float f[MINE];
+#pragma unroll
+  for (int i = 0; i < MINE; ++i) {
+    f[i] = 1.0f;
+    if (FMT == TABIT_FMT_INT8)
+      f[i] = static_cast<const float*>(a.x_scale)[min(row0 + (i * NW * 64 + (int)threadIdx.x) / PAIRS, row1 - 1)];
+  }
+  const uint16_t* ap = a.a + ((long long)ad * a.rank + r0) * a.K;
   v4f acc[MR][RB];
 #pragma unroll
   for (int m = 0; m < MR; ++m)
 #pragma unroll
     for (int r = 0; r < RB; ++r) acc[m][r] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k0 = wave * 64; k0 < a.K; k0 += NW * 64) {
-    const int k = k0 + 16 * g;
-    const bool in = k < a.K;                     // (K is a multiple of 32)
+  uint32_t scale[STAGES][MR];
+  // Rows past the segment read its last one, pieces past K (a multiple of 32) the row's first: neither is
+  // kept.
+  auto ask = [&](int step) {
+    const int k0 = (step * NW + wave) * 64;
+    if (k0 >= a.K) return;
+    uint8_t* to = smem[wave] + step % STAGES * (XB + WB);
+#pragma unroll
+    for (int i = 0; i < XI; ++i) {
+      const int s = i * 64 + lane, r = s / X::PIECES, p = (s % X::PIECES) ^ turned<X::PIECES>(r);
+      const int k = k0 + p * (64 / X::PIECES);
+      if (XB >= 1024 || s < XB / 16)
+        __builtin_amdgcn_global_load_lds((from_t)X::at(a, min(row0 + r, row1 - 1), k < a.K ? k : 0), (to_t)(to + i * 1024), 16, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < WI; ++i) {
+      const int s = i * 64 + lane, r = s / 8, k = k0 + ((s % 8) ^ turned<8>(r)) * 8;
+      __builtin_amdgcn_global_load_lds((from_t)(ap + (long long)r * a.K + (k < a.K ? k : 0)), (to_t)(to + XB + i * 1024), 16, 0, 0);
+    }
+    if constexpr (FMT == TABIT_FMT_MXFP4) {
+#pragma unroll
+      for (int m = 0; m < MR; ++m) {
+        const int k = k0 + 16 * g;
+        scale[step % STAGES][m] = static_cast<const uint8_t*>(
+            a.x_scale)[(long long)min(row0 + 16 * m + row, row1 - 1) * (a.K / 32) + (k < a.K ? k : 0) / 32];
+      }
+    }
+  };
+  ask(0);
+  for (int step = 0;; ++step) {
+    const int k0 = (step * NW + wave) * 64;
+    if (k0 >= a.K) break;
+    ask(step + 1);
+    if (k0 + NW * 64 < a.K) tile::wait_vmcnt<XI + WI>();     // this step's are here, the next one's not
+    else tile::wait_vmcnt0();
+    __builtin_amdgcn_wave_barrier();
+    const uint8_t* st = smem[wave] + step % STAGES * (XB + WB);
     v8bf x[MR][2], w[RB][2];
+#pragma unroll
+    for (int m = 0; m < MR; ++m) X::get(st, 16 * m + row, g, FMT == TABIT_FMT_MXFP4 ? scale[step % STAGES][m] : 0u, x[m]);
 #pragma unroll
     for (int r = 0; r < RB; ++r)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        w[r][e] = in ? *reinterpret_cast<const v8bf*>(ap + (long long)16 * r * a.K + k + 8 * e) : zero8();
+      for (int e = 0; e < 2; ++e) w[r][e] = *reinterpret_cast<const v8bf*>(st + XB + place<8>(16 * r + row, 2 * g + e));
+    if (k0 + 64 > a.K && k0 + 16 * g >= a.K) {
 #pragma unroll
-    for (int m = 0; m < MR; ++m) {
-      // (rows past the segment read its last row: their products are not kept)
-      const auto raw = Rows<FMT>::load(a, min(row0 + 16 * m + row, row1 - 1), in ? k : 0);
-      Rows<FMT>::get(raw, x[m]);
-      if (!in) x[m][0] = x[m][1] = zero8();
+      for (int m = 0; m < MR; ++m) x[m][0] = x[m][1] = zero8();
+#pragma unroll
+      for (int r = 0; r < RB; ++r) w[r][0] = w[r][1] = zero8();
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e)
@@ -150,29 +213,30 @@ adapter_down_kernel(AdapterArgs a) {
 #pragma unroll
         for (int r = 0; r < RB; ++r)
           acc[m][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[m][e], w[r][e], acc[m][r], 0, 0, 0);
+    __builtin_amdgcn_wave_barrier();             // (LDS serves a wave in order: its reads are before what comes)
   }
   // lane: rank l % 16, rows 4 (l / 16) + i
+  float* part = reinterpret_cast<float*>(smem[wave]);
 #pragma unroll
   for (int m = 0; m < MR; ++m)
 #pragma unroll
     for (int r = 0; r < RB; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) part[wave][16 * m + 4 * g + i][16 * r + row] = acc[m][r][i];
+      for (int i = 0; i < 4; ++i) part[(16 * m + 4 * g + i) * (RANKS + 4) + 16 * r + row] = acc[m][r][i];
   __syncthreads();
-  const float c = a.scale != nullptr ? a.scale[ad] : 1.0f;
-  for (int i = threadIdx.x; i < ROWS * RANKS / 2; i += NW * 64) {
-    const int t = i / (RANKS / 2), r = i % (RANKS / 2) * 2;
-    if (row0 + t >= row1) continue;
+#pragma unroll
+  for (int i = 0; i < MINE; ++i) {
+    const int t = (i * NW * 64 + (int)threadIdx.x) / PAIRS, r = (i * NW * 64 + (int)threadIdx.x) % PAIRS * 2;
+    if (t >= ROWS || row0 + t >= row1) continue;
     float u = 0.0f, v = 0.0f;
 #pragma unroll
     for (int n = 0; n < NW; ++n) {
-      u += part[n][t][r];
-      v += part[n][t][r + 1];
+      const float2 x = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(smem[n]) + t * (RANKS + 4) + r);
+      u += x.x;
+      v += x.y;
     }
-    float f = c;
-    if (FMT == TABIT_FMT_INT8) f *= static_cast<const float*>(a.x_scale)[row0 + t];
-    u *= f;
-    v *= f;
+    u *= c * f[i];
+    v *= c * f[i];
     const uint32_t hi = pack_bf16(u, v);
     const long long at = (long long)(row0 + t) * a.rank + r0 + r;
     *reinterpret_cast<uint32_t*>(a.hi + at) = hi;
@@ -182,46 +246,47 @@ adapter_down_kernel(AdapterArgs a) {
   }
 }
 
-// out of 16 rows and 64 columns a wave: D[n][t] with B the first operand, so that a lane holds one
-// row (l % 16) and, over four products with n = 16 (i / 4) + 4 j + i % 4 for row i of product j, 16
-// consecutive columns.  R = 16: one product takes both terms of h, [hi | lo] . [B | B].
-// WIDE: the workgroup's waves take 64 rows, 16 each, of the same columns; else 16 rows, and each
-// wave columns of its own.
+// out of 16 rows a wave, 128 columns at a time: h is the first operand and product j takes columns
+// 8 i + j (i = l % 16), so that a lane holds eight consecutive columns of four rows, and 16 lanes read and
+// write 256 bytes of a row at once.  R = 16: one product takes both terms of h, [hi | lo] . [B | B].
+// WIDE: the workgroup's waves take 64 rows, 16 each, of the same columns, which they bring to LDS together;
+// else 16 rows, and each wave columns of its own.
 template <int R, bool WIDE>
 __global__ void __launch_bounds__(256)
-adapter_up_kernel(AdapterArgs a) {
-  constexpr int ROWS = WIDE ? 64 : 16, COLS = WIDE ? 64 : 256;
+adapter_up_kernel(AdapterArgs a, int cols) {
+  constexpr int ROWS = WIDE ? 64 : 16, COLS = 128;
   constexpr int KC = R <= 32 ? 1 : R / 32;             // 32-rank chunks
+  constexpr int PIECES = R / 8, BYTES = COLS * R * 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[WIDE ? 2 : 4][BYTES];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int seg, row0, row1;
-  const unsigned blocks = ((unsigned)a.N + COLS - 1) / COLS;
+  const unsigned blocks = ((unsigned)a.N + cols - 1) / cols;
   if (!find_tile(a, blockIdx.x / blocks, ROWS, lane, seg, row0, row1)) return;
   const int row = lane & 15, g = lane >> 4;
-  const int t = row0 + (WIDE ? wave * 16 : 0) + row;
-  const int n0 = (int)(blockIdx.x % blocks) * COLS + (WIDE ? 0 : wave * 64);
-  if (n0 >= a.N) return;
-  const bool in = n0 + 16 * g < a.N, mine = t < row1 && in;
   const int ad = a.adapter[seg];
   const bool has = (unsigned)ad < (unsigned)a.num_adapters;
   if (!has && a.out == a.y) return;
-  uint4 yw[2] = {};
-  if (mine) {
-    const uint4* p = reinterpret_cast<const uint4*>(a.y + t * a.y_stride + n0 + 16 * g);
-    yw[0] = p[0];
-    yw[1] = p[1];
-  }
-  v4f acc[4];
-  float y[8];
+  const int t0 = row0 + (WIDE ? wave * 16 : 0);
+  constexpr int STRIDE = WIDE ? COLS : 4 * COLS;
+  const int first = (int)(blockIdx.x % blocks) * cols + (WIDE ? 0 : wave * COLS);
+  const int last = min((int)(blockIdx.x % blocks + 1) * cols, a.N);
+  const uint16_t* bp = a.b + (long long)(has ? ad : 0) * a.N * R;
+  // Columns n0 + 8 i + j as row 16 j + i (those past N read the last one and are not kept)
+  auto bring = [&](int n0, uint8_t* to) {
+    if (!has || n0 >= last) return;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    unpack8(yw[e], y);
-    acc[2 * e] = v4f{y[0], y[1], y[2], y[3]};
-    acc[2 * e + 1] = v4f{y[4], y[5], y[6], y[7]};
-  }
+    for (int i = WIDE ? wave : 0; i < BYTES / 1024; i += WIDE ? 4 : 1) {
+      const int s = i * 64 + lane, q = s / PIECES, p = (s % PIECES) ^ turned<PIECES>(q & 15);
+      const int n = min(n0 + 8 * (q & 15) + (q >> 4), a.N - 1);
+      __builtin_amdgcn_global_load_lds((from_t)(bp + (long long)n * R + p * 8), (to_t)(to + i * 1024), 16, 0, 0);
+    }
+  };
+  uint8_t* stage = smem[WIDE ? 0 : wave];
+  bring(first, stage);
+  v8bf hi[KC], lo[KC];
   if (has) {
-    const int th = min(t, row1 - 1);
-    v8bf hi[KC], lo[KC];
+    const int th = min(t0 + row, row1 - 1);
     if constexpr (R == 16) {
       hi[0] = *reinterpret_cast<const v8bf*>((g < 2 ? a.hi : a.lo) + (long long)th * R + 8 * (g & 1));
     } else {
@@ -231,30 +296,59 @@ adapter_up_kernel(AdapterArgs a) {
         lo[kc] = *reinterpret_cast<const v8bf*>(a.lo + (long long)th * R + 32 * kc + 8 * g);
       }
     }
+  }
+  int at = 0;
+  for (int n0 = first; n0 < last; n0 += STRIDE) {
+    // lane: rows t0 + 4 g + r, columns n0 + 8 (l % 16) on
+    const int n = n0 + 8 * row;
+    uint4 y[4] = {};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      // (columns past N read the last ones: their products are not kept)
-      const int n = min(n0 + 16 * (row >> 2) + 4 * j + (row & 3), a.N - 1);
-      const uint16_t* bp = a.b + ((long long)ad * a.N + n) * R;
-      if constexpr (R == 16) {
-        const v8bf w = *reinterpret_cast<const v8bf*>(bp + 8 * (g & 1));
-        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, hi[0], acc[j], 0, 0, 0);
-      } else {
+    for (int r = 0; r < 4; ++r)
+      if (n < a.N && t0 + 4 * g + r < row1) y[r] = *reinterpret_cast<const uint4*>(a.y + (t0 + 4 * g + r) * a.y_stride + n);
+    tile::wait_vmcnt0();
+    if constexpr (WIDE) {
+      tile::lds_barrier();
+      bring(n0 + STRIDE, smem[at ^ 1]);
+      stage = smem[at];
+      at ^= 1;
+    } else {
+      __builtin_amdgcn_wave_barrier();
+    }
+    v4f acc[8];
 #pragma unroll
-        for (int kc = 0; kc < KC; ++kc) {
-          const v8bf w = *reinterpret_cast<const v8bf*>(bp + 32 * kc + 8 * g);
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, lo[kc], acc[j], 0, 0, 0);
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, hi[kc], acc[j], 0, 0, 0);
+    for (int r = 0; r < 4; ++r) {
+      float v[8];
+      unpack8(y[r], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j][r] = v[j];
+    }
+    if (has) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint8_t* b = stage + j * 16 * R * 2;
+        if constexpr (R == 16) {
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[0], *reinterpret_cast<const v8bf*>(b + place<PIECES>(row, g & 1)), acc[j], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int kc = 0; kc < KC; ++kc) {
+            const v8bf w = *reinterpret_cast<const v8bf*>(b + place<PIECES>(row, 4 * kc + g));
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[kc], w, acc[j], 0, 0, 0);
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[kc], w, acc[j], 0, 0, 0);
+          }
         }
       }
     }
-  }
-  if (!mine) return;
-  uint4* o = reinterpret_cast<uint4*>(a.out + t * a.out_stride + n0 + 16 * g);
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
-    o[e] = make_uint4(pack_bf16(acc[2 * e][0], acc[2 * e][1]), pack_bf16(acc[2 * e][2], acc[2 * e][3]),
-                      pack_bf16(acc[2 * e + 1][0], acc[2 * e + 1][1]), pack_bf16(acc[2 * e + 1][2], acc[2 * e + 1][3]));
+    for (int r = 0; r < 4; ++r)
+      if (n < a.N && t0 + 4 * g + r < row1)
+        *reinterpret_cast<uint4*>(a.out + (t0 + 4 * g + r) * a.out_stride + n) =
+            make_uint4(pack_bf16(acc[0][r], acc[1][r]), pack_bf16(acc[2][r], acc[3][r]),
+                       pack_bf16(acc[4][r], acc[5][r]), pack_bf16(acc[6][r], acc[7][r]));
+    if constexpr (!WIDE) {
+      __builtin_amdgcn_wave_barrier();
+      bring(n0 + STRIDE, stage);
+    }
+  }
 }
 
 // Each row of A times the block transform over 1 / b.  A wave holds 512 elements, eight a lane.
@@ -281,6 +375,10 @@ unsigned tiles(const AdapterArgs& a, int rows) { return (unsigned)((a.rows + row
 // Segments of few rows (single tokens): small tiles, more waves on one sum.
 bool few_rows(const AdapterArgs& a) { return a.rows <= 16ll * a.segments; }
 
+// Measured, 64 rows of 4096 in INT8, rank 64, 40 adapters: 4, 8 and 16 waves 12.5, 9.1 and 8.6 us, one row of
+// 2240 in each of four segments 4.5, 3.8 and 4.2.  17776 rows of 1920, rank 32: 16, 32 and 64 rows by four
+// waves 25, 19.5 and 19.6, 32 by eight 24.5; a third stage 25.5 (13 us where the rows come from a cache;
+// 2.6 TB/s, A from the L2 as often as x from memory).
 template <int FMT>
 hipError_t down(const AdapterArgs& a, hipStream_t s) {
   if (few_rows(a)) adapter_down_kernel<FMT, 1, 1, 8><<<tiles(a, 16) * (a.rank / 16), 512, 0, s>>>(a);
@@ -290,10 +388,12 @@ hipError_t down(const AdapterArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Columns of a workgroup: 512 (128 a wave) of single tokens, 256 of many rows (17776 rows to 5760, rank 32, in
+// 128, 256, 512 and 1024: both kernels 92, 92, 100 and 103 us; 77 of it this one, 5.3 TB/s).
 template <int R>
 hipError_t up(const AdapterArgs& a, hipStream_t s) {
-  if (few_rows(a)) adapter_up_kernel<R, false><<<tiles(a, 16) * ((a.N + 255) / 256), 256, 0, s>>>(a);
-  else adapter_up_kernel<R, true><<<tiles(a, 64) * ((a.N + 63) / 64), 256, 0, s>>>(a);
+  if (few_rows(a)) adapter_up_kernel<R, false><<<tiles(a, 16) * ((a.N + 511) / 512), 256, 0, s>>>(a, 512);
+  else adapter_up_kernel<R, true><<<tiles(a, 64) * ((a.N + 255) / 256), 256, 0, s>>>(a, 256);
   return hipGetLastError();
 }
 
