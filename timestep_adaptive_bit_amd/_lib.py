@@ -915,6 +915,14 @@ class Context:
                                                  _stream(dev)))
         return out
 
+    def _launch(self, device: torch.device, fn, *args) -> None:
+        """fn on the tensors' device, whichever is the current one, and on torch's stream of it."""
+        if device.index == torch.cuda.current_device():
+            self._check(fn(self._h, *args, _stream(device)))
+        else:
+            with torch.cuda.device(device):
+                self._check(fn(self._h, *args, _stream(device)))
+
     def _rows_args(self, cache: KVCache, q, cu_q, block_table, kv_lens, max_q, max_kv, scale, causal,
                    rope, positions, out, lse, ws):
         """Checks and the argument structure of an attention-like call; ws given."""
@@ -961,9 +969,8 @@ class Context:
         mask = torch.zeros((T, words), dtype=torch.int64, device=parents.device)
         depth = torch.zeros((T,), dtype=torch.int32, device=parents.device)
         if T:
-            self._check(self._lib.tabit_tree_mask(
-                self._h, parents.data_ptr(), T, cu_q.data_ptr(), cu_q.shape[0] - 1, max_q, mask.data_ptr(),
-                words, depth.data_ptr(), _stream(parents.device)))
+            self._launch(parents.device, self._lib.tabit_tree_mask, parents.data_ptr(), T, cu_q.data_ptr(),
+                         cu_q.shape[0] - 1, max_q, mask.data_ptr(), words, depth.data_ptr())
         return mask, depth
 
     def kv_tree_attention_workspace(self, cache: KVCache, q: torch.Tensor, num_seqs: int, max_q: int,
@@ -994,8 +1001,8 @@ class Context:
             raise ValueError("mask must be [tokens][words]")
         _on(mask, torch.int64, "mask", (T, mask.shape[1]), dev)
         if T and B:
-            self._check(self._lib.tabit_kv_tree_attention(self._h, cache._ref, ctypes.addressof(a),
-                                                          mask.data_ptr(), mask.shape[1], _stream(dev)))
+            self._launch(dev, self._lib.tabit_kv_tree_attention, cache._ref, ctypes.addressof(a), mask.data_ptr(),
+                         mask.shape[1])
         return out
 
     # ------------------------------------------------------------ eviction
@@ -1028,8 +1035,7 @@ class Context:
                             None, lse, ws)
         self._sums(cache, sums)
         if a.num_tokens and B:
-            self._check(self._lib.tabit_kv_weigh(self._h, cache._ref, ctypes.addressof(a), sums.data_ptr(),
-                                                 _stream(cache.device)))
+            self._launch(cache.device, self._lib.tabit_kv_weigh, cache._ref, ctypes.addressof(a), sums.data_ptr())
         return sums
 
     def kv_evict_workspace(self, cache: KVCache, num_seqs: int, max_kv: int) -> Optional[torch.Tensor]:
@@ -1055,10 +1061,9 @@ class Context:
                 ws = self.kv_evict_workspace(cache, B, max_kv)
             elif ws.device != dev or not ws.is_contiguous():
                 raise ValueError(f"ws must be contiguous and on {dev}")
-            self._check(self._lib.tabit_kv_evict(
-                self._h, cache._ref, sums.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-                kv_lens.data_ptr(), B, max_kv, budget, sinks, recent, keep.data_ptr(), lens.data_ptr(),
-                _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(dev)))
+            self._launch(dev, self._lib.tabit_kv_evict, cache._ref, sums.data_ptr(), block_table.data_ptr(),
+                         block_table.shape[1], kv_lens.data_ptr(), B, max_kv, budget, sinks, recent, keep.data_ptr(),
+                         lens.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
         return keep, lens
 
     def kv_compact_workspace(self, cache: KVCache, num_seqs: int, most: int) -> Optional[torch.Tensor]:
@@ -1092,10 +1097,9 @@ class Context:
             ws = self.kv_compact_workspace(cache, B, most)
         elif ws.device != dev or not ws.is_contiguous():
             raise ValueError(f"ws must be contiguous and on {dev}")
-        self._check(self._lib.tabit_kv_compact(
-            self._h, cache._ref, block_table.data_ptr(), block_table.shape[1], B, keep.data_ptr(), heads, most,
-            counts.data_ptr(), _ptr(starts), _ptr(sums), _ptr(ws),
-            0 if ws is None else ws.numel() * ws.element_size(), _stream(dev)))
+        self._launch(dev, self._lib.tabit_kv_compact, cache._ref, block_table.data_ptr(), block_table.shape[1], B,
+                     keep.data_ptr(), heads, most, counts.data_ptr(), _ptr(starts), _ptr(sums), _ptr(ws),
+                     0 if ws is None else ws.numel() * ws.element_size())
 
     # ------------------------------------------------------------ adapters
     def adapter_rotate(self, a: torch.Tensor, had_block: int, out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -1109,8 +1113,8 @@ class Context:
         rows = a.numel() // a.shape[-1] if a.numel() else 0
         _counts(rows, a.shape[-1])
         if rows:
-            self._check(self._lib.tabit_adapter_rotate(self._h, a.data_ptr(), rows, a.shape[-1], had_block,
-                                                       out.data_ptr(), _stream(a.device)))
+            self._launch(a.device, self._lib.tabit_adapter_rotate, a.data_ptr(), rows, a.shape[-1], had_block,
+                         out.data_ptr())
         return out
 
     def adapter_workspace(self, adapters: Adapters, x: torch.Tensor, num_segments: int) -> Optional[torch.Tensor]:
@@ -1167,7 +1171,7 @@ class Context:
                          adapters.b.data_ptr(), _ptr(adapters.scale), adapters.num, adapters.rank,
                          cu_rows.data_ptr(), which.data_ptr(), S, y.data_ptr(), ys, out.data_ptr(), os_,
                          _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
-        self._check(self._lib.tabit_adapter_linear(self._h, ctypes.addressof(a), _stream(dev)))
+        self._launch(dev, self._lib.tabit_adapter_linear, ctypes.addressof(a))
         return out
 
     def block_norm(self, x: torch.Tensor, y: Optional[torch.Tensor] = None, post: int = NORM_NONE,

@@ -370,10 +370,12 @@ adapter_rotate_kernel(const uint16_t* a, long long n, uint16_t* out) {
 }
 
 // Row tiles of a launch: every segment ends inside one at most.
-unsigned tiles(const AdapterArgs& a, int rows) { return (unsigned)((a.rows + rows - 1) / rows + a.segments); }
+long long tiles_of(int rows, int segments, int tile) { return ((long long)rows + tile - 1) / tile + segments; }
+unsigned tiles(const AdapterArgs& a, int tile) { return (unsigned)tiles_of(a.rows, a.segments, tile); }
 
 // Segments of few rows (single tokens): small tiles, more waves on one sum.
-bool few_rows(const AdapterArgs& a) { return a.rows <= 16ll * a.segments; }
+bool few_rows(int rows, int segments) { return rows <= 16ll * segments; }
+bool few_rows(const AdapterArgs& a) { return few_rows(a.rows, a.segments); }
 
 // Measured, 64 rows of 4096 in INT8, rank 64, 40 adapters: 4, 8 and 16 waves 12.5, 9.1 and 8.6 us, one row of
 // 2240 in each of four segments 4.5, 3.8 and 4.2.  17776 rows of 1920, rank 32: 16, 32 and 64 rows by four
@@ -398,6 +400,13 @@ hipError_t up(const AdapterArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+bool adapter_fits(int rows, int segments, int rank, int N) {
+  // 2^32 threads a launch, in workgroups of 512 or 256
+  return few_rows(rows, segments)
+             ? tiles_of(rows, segments, 16) * (rank / 16) < (1ll << 23) && tiles_of(rows, segments, 16) * ((N + 511) / 512) < (1ll << 24)
+             : tiles_of(rows, segments, 32) * ((rank + 63) / 64) < (1ll << 24) && tiles_of(rows, segments, 64) * ((N + 255) / 256) < (1ll << 24);
+}
 
 hipError_t launch_adapter_linear(const AdapterArgs& a, hipStream_t s) {
   const hipError_t e = a.x_fmt == TABIT_FMT_BF16   ? down<TABIT_FMT_BF16>(a, s)

@@ -118,8 +118,10 @@ int tabit_kv_weigh(tabit_ctx* ctx, const tabit_kv_cache* cache, const tabit_kv_a
   if (a->num_tokens == 0 || a->num_seqs == 0 || a->max_q == 0) return TABIT_OK;
   if (a->max_kv == 0 && a->lse == nullptr) return TABIT_OK;
   if ((st = check_grid(ctx, a, 1)) != TABIT_OK) return st;
-  if ((int64_t)a->max_kv * a->num_seqs > INT_MAX)
-    return fail(ctx, TABIT_ESHAPE, "max_kv * num_seqs is too large (%d * %d)", a->max_kv, a->num_seqs);
+  if (!tabit::kv_weigh_fits(a->num_tokens, a->num_q_heads, k.cache.heads, k.cache.dim_pad, a->num_seqs, a->max_q,
+                            a->max_kv))
+    return fail(ctx, TABIT_ESHAPE, "too many rows or keys for one call (%d sequences of %d rows, %d keys)", a->num_seqs,
+                a->max_q, a->max_kv);
   const size_t need = tabit::kv_weigh_workspace(a->num_tokens, a->num_q_heads, k.cache.heads, k.cache.dim_pad,
                                                 a->num_seqs, a->max_q, a->max_kv);
   if ((st = check_ws(ctx, a->ws, a->ws_bytes, need)) != TABIT_OK) return st;
@@ -240,9 +242,8 @@ int tabit_adapter_linear(tabit_ctx* ctx, const tabit_adapter_args* a, void* stre
       (a->x_fmt == TABIT_FMT_INT8 && !aligned(a->x_scale, 4)))
     return fail(ctx, TABIT_EALIGN, "matrices and ws must be 16-byte aligned, vectors 4-byte");
   if (a->rows == 0 || a->num_segments == 0) return TABIT_OK;
-  // workgroups of either kernel: tiles of 16 rows and one a segment, by 64 columns or 16 ranks
-  const int64_t most = ((int64_t)a->rows / 16 + 1 + a->num_segments) * ((a->N + 63) / 64 + a->rank / 16);
-  if (most >= (1 << 23)) return fail(ctx, TABIT_ESHAPE, "too many rows and columns (%d, %d)", a->rows, a->N);
+  if (!tabit::adapter_fits(a->rows, a->num_segments, a->rank, a->N))
+    return fail(ctx, TABIT_ESHAPE, "too many rows and columns (%d, %d)", a->rows, a->N);
   const size_t need = tabit_adapter_workspace_bytes(a->rows, a->rank, a->num_segments);
   const int st = check_ws(ctx, a->ws, a->ws_bytes, need);
   if (st != TABIT_OK) return st;

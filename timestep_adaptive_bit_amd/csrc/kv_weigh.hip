@@ -741,7 +741,7 @@ kv_weigh_scores_kernel(KvAttnArgs a, FewPlan p) {
 #pragma unroll
         for (int i = TERMS - 1; i >= 0; --i) x = term<false>(k[kb].codes[ds], k[kb].scale[ds], q.q[ds][i], q.scale[ds], i, x);
       const int j = t * 64 + kb * 32 + key;
-      const int first = a.causal ? max(j - old, 0) * a.group : 0;      // (j - old is at most the rows' count)
+      const int first = a.causal ? min(max(j - old, 0), 8) * a.group : 0;
 #pragma unroll
       for (int r = 0; r < 4; ++r) s[kb][r] = (key & 15) < there[kb] && 4 * half + r >= first ? x[r] : kNegInf;
       if (4 * half < R) *reinterpret_cast<v4f*>(scores + (long long)j * R + 4 * half) = v4f{s[kb][0], s[kb][1], s[kb][2], s[kb][3]};
@@ -927,6 +927,20 @@ size_t plan_of(int tokens, int q_heads, int kv_heads, int dim_pad, int seqs, int
 }
 
 }  // namespace
+
+bool kv_weigh_fits(int tokens, int q_heads, int kv_heads, int dim_pad, int seqs, int max_q, int max_kv) {
+  const long long most = (1ll << 24) - 1;        // workgroups of 256 threads: 2^32 threads are the limit
+  const long long pairs = (long long)seqs * kv_heads;
+  if ((long long)max_q * (q_heads / kv_heads) <= 8) {
+    FewPlan p;
+    few_plan_of(seqs, kv_heads, 8, max_kv, nullptr, p);
+    return (long long)p.splits * seqs <= most && ((long long)max_kv / 1024 + 1) * seqs <= most;
+  }
+  Plan p;
+  plan_of(tokens, q_heads, kv_heads, dim_pad, seqs, max_q, max_kv, nullptr, p);
+  return (long long)p.row_tiles * seqs <= most && ((p.row_tiles + 3ll) / 4) * p.splits * pairs <= most &&
+         ((long long)max_kv / kKeys + 1) * pairs * p.ranges <= most && ((long long)max_kv / 1024 + 1) * seqs <= most;
+}
 
 size_t kv_weigh_workspace(int tokens, int q_heads, int kv_heads, int dim_pad, int seqs, int max_q, int max_kv) {
   const long long rows = (long long)max_q * (q_heads / kv_heads);

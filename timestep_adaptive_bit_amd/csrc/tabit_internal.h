@@ -157,6 +157,7 @@ hipError_t launch_tree_mask(const int* parents, int tokens, const int* cu_q, int
 // ---------------------------------------------------------------- eviction
 // Sums [num_pages][heads][2^page_shift] += the rows' attention weights; a.part is the workspace.
 size_t kv_weigh_workspace(int tokens, int q_heads, int kv_heads, int dim_pad, int seqs, int max_q, int max_kv);
+bool kv_weigh_fits(int tokens, int q_heads, int kv_heads, int dim_pad, int seqs, int max_q, int max_kv);
 hipError_t launch_kv_weigh(const KvAttnArgs& a, float* sums, hipStream_t s);
 
 struct KvEvictArgs {
@@ -199,6 +200,7 @@ struct AdapterArgs {
   long long out_stride;
   uint16_t *hi, *lo;             // workspace: x A^T in two bf16 terms, [rows][rank] each
 };
+bool adapter_fits(int rows, int segments, int rank, int N);      // the launches' limits
 hipError_t launch_adapter_linear(const AdapterArgs& a, hipStream_t s);
 hipError_t launch_adapter_rotate(const uint16_t* a, int rows, int K, int had_block, uint16_t* out,
                                  hipStream_t s);
