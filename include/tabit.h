@@ -635,8 +635,8 @@ size_t tabit_kv_attention_workspace_bytes(int num_tokens, int num_q_heads, int n
  * j % 64 of word j / 64 of its row of the mask is set.
  *   args        as tabit_kv_attention; args->causal must be 0, max_q at most 8192
  *   mask        device uint64 [num_tokens][mask_words], 8-byte aligned;
- *               mask_words at least ceil(max_q / 64); bits past n are not read.  Nodes past
- *               the mask's words are not seen
+ *               mask_words at least ceil(max_q / 64); bits past n count for nothing.  Nodes
+ *               past the mask's words are not seen
  * A row that sees no key answers zeros (lse -inf).  ws: of
  * tabit_kv_tree_attention_workspace_bytes, arguments as the other's.
  */
@@ -696,7 +696,7 @@ size_t tabit_kv_weigh_workspace_bytes(int num_tokens, int num_q_heads, int num_k
  *   new_lens     device int32 [num_seqs] output: min(kv_len, budget)
  *   ws           device workspace of tabit_kv_evict_workspace_bytes bytes, 16-byte aligned (NULL
  *                when that is 0)
- * sinks + recent at most budget.
+ * sinks + recent at most budget, which is 1 to 2^30.
  */
 int tabit_kv_evict(tabit_ctx* ctx, const tabit_kv_cache* cache, const float* sums, const int32_t* block_table,
                    int table_stride, const int32_t* kv_lens, int num_seqs, int max_kv, int budget, int sinks,

@@ -148,6 +148,12 @@ def test_evict_refusals(lib, ctx):
     assert lib.tabit_kv_evict_workspace_bytes(2, 2, 8192) == 0 < lib.tabit_kv_evict_workspace_bytes(2, 2, 8193)
 
 
+@pytest.mark.parametrize("budget", [(1 << 30) + 1, (1 << 31) - 1])
+def test_evict_budget_limit(lib, ctx, budget):
+    """Indexes of a list are whole numbers of 32 bits that the kernel steps by thousands."""
+    assert _evict(lib, ctx, budget=budget) == T.ESHAPE
+
+
 def test_compact_refusals(lib, ctx):
     cases = [(dict(seqs=-1), T.ESHAPE), (dict(table=None), T.EINVAL), (dict(stride=0), T.ESHAPE), (dict(heads=3), T.ESHAPE),
              (dict(heads=0), T.ESHAPE), (dict(most=-1), T.ESHAPE), (dict(most=(1 << 26) + 1), T.ESHAPE), (dict(keep=None), T.EINVAL),

@@ -147,7 +147,7 @@ int tabit_kv_evict(tabit_ctx* ctx, const tabit_kv_cache* cache, const float* sum
   if ((int64_t)table_stride * cache->page_size < max_kv)
     return fail(ctx, TABIT_ESHAPE, "a table row of %d pages of %d tokens does not hold max_kv = %d", table_stride,
                 cache->page_size, max_kv);
-  if (budget < 1) return fail(ctx, TABIT_ESHAPE, "budget must be >= 1 (got %d)", budget);
+  if (budget < 1 || budget > (1 << 30)) return fail(ctx, TABIT_ESHAPE, "budget must be in [1, 2^30] (got %d)", budget);
   if (sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget)
     return fail(ctx, TABIT_ESHAPE, "the first %d and last %d tokens do not fit a budget of %d", sinks, recent, budget);
   if (kv_lens == nullptr || keep == nullptr || new_lens == nullptr) return fail(ctx, TABIT_EINVAL, "null pointer");
