@@ -212,3 +212,10 @@ def test_binding_refusals(ctx):
         ctx.tree_mask(z(4, 4, dtype=torch.int32), z(2, dtype=torch.int32), 4)
     with pytest.raises(ValueError):
         ctx.adapter_rotate(z(4, 64, dtype=torch.bfloat16), 32)
+
+
+@pytest.mark.parametrize("a,b", [((8, 64), (32, 16)), ((16, 64), (32, 8)), ((8, 64), (32, 200)), ((64,), (32, 8))])
+def test_pairs_of_unequal_ranks(a, b):
+    """Filling up to a common rank must not hide that a pair's matrices do not belong together."""
+    with pytest.raises(ValueError, match="pair"):
+        T.Adapters.of([(torch.zeros(a, dtype=torch.bfloat16), torch.zeros(b, dtype=torch.bfloat16))])

@@ -365,6 +365,9 @@ class Adapters:
     def of(cls, pairs, scale: Optional[torch.Tensor] = None) -> "Adapters":
         """From pairs of a [r][K] and b [N][r] bf16 of any ranks up to 128: smaller ones are filled up
         with zeros to the smallest rank the kernels take."""
+        for a, b in pairs:
+            if a.dim() != 2 or b.dim() != 2 or a.shape[0] != b.shape[1]:
+                raise ValueError(f"a pair must be [r][K] and [N][r], got {tuple(a.shape)} and {tuple(b.shape)}")
         most = max(a.shape[0] for a, _ in pairs)
         if most > 128:
             raise ValueError(f"ranks are at most 128, got {most}")
