@@ -25,6 +25,7 @@ constexpr int kWaves = 16, kThreads = kWaves * 64;
 constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr int kCopies = 4;       // of a histogram, by lane: fewer lanes meet at one place
 constexpr int kWhole = 8192;     // tokens whose numbers one workgroup holds
+constexpr int kChunks = 16;      // of a longer sequence, at most
 
 // Whole number of the same order as w: NaN 0, then -infinity ... infinity (-0 as 0).
 __device__ __forceinline__ uint32_t order_of(float w) {
@@ -68,7 +69,8 @@ __device__ __forceinline__ void find_bin(int high, int low, int missing, int* ro
   __syncthreads();
   if (lane == 63) room[wave] = sum;
   __syncthreads();
-  for (int k = 0; k < wave; ++k) sum += room[k];
+#pragma unroll
+  for (int k = 0; k < kWaves; ++k) sum += k < wave ? room[k] : 0;
   const int before = sum - high - low;                     // exactly one thread finds its bin
   if (before < missing && sum >= missing) {
     const bool first = before + high >= missing;
@@ -131,6 +133,15 @@ kv_evict_kernel(KvEvictArgs a) {
   __shared__ int room[kWaves + 2], counted[kWaves][2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int h = blockIdx.x, b = blockIdx.y;
+  const int* table = a.table + (long long)b * a.table_stride;
+  // (before the length is known: the table has room for max_kv tokens, and what lies past the length
+  // is not looked at)
+  uint4 mine[kWhole / (kThreads * 4)];
+#pragma unroll
+  for (int k = 0; k < kWhole / (kThreads * 4); ++k) {
+    const int i = (k * kThreads + tid) * 4;
+    mine[k] = i < a.max_kv ? load4(a, table, h, i) : make_uint4(0u, 0u, 0u, 0u);
+  }
   const int n = min(max(a.kv_lens[b], 0), a.max_kv);
   int* keep = a.keep + ((long long)b * a.cache.heads + h) * a.budget;
   if (h == 0 && tid == 0) a.new_lens[b] = min(n, a.budget);
@@ -139,8 +150,8 @@ kv_evict_kernel(KvEvictArgs a) {
     return;
   }
   const int first = a.sinks, last = n - a.recent;          // those between compete: first < last
-  const int* table = a.table + (long long)b * a.table_stride;
-  for (int i = tid * 4; i < n; i += kThreads * 4) *reinterpret_cast<uint4*>(held + i) = load4(a, table, h, i);
+#pragma unroll
+  for (int k = 0; k < kWhole / (kThreads * 4); ++k) *reinterpret_cast<uint4*>(held + (k * kThreads + tid) * 4) = mine[k];
   auto get4 = [&](int i) { return *reinterpret_cast<const uint4*>(held + i); };
 
   // The smallest kept number T, and how many equal to it are kept
@@ -186,9 +197,10 @@ kv_evict_kernel(KvEvictArgs a) {
   }
   __syncthreads();
   sure = equal = 0;
-  for (int k = 0; k < wave; ++k) {
-    sure += counted[k][0];
-    equal += counted[k][1];
+#pragma unroll
+  for (int k = 0; k < kWaves; ++k) {
+    sure += k < wave ? counted[k][0] : 0;
+    equal += k < wave ? counted[k][1] : 0;
   }
   write_kept<false>(from, to, first, last, any, T, missing, sure, equal, keep, get4);
 }
@@ -211,9 +223,11 @@ template <int PASS>
 __global__ void __launch_bounds__(kThreads)
 kv_evict_long_kernel(KvEvictArgs a, LongPlan p) {
   __shared__ uint32_t hist[PASS < 3 ? kCopies : 1][PASS < 3 ? kBins : 1];
+  __shared__ __attribute__((aligned(16))) uint32_t held[kWhole];
   __shared__ int room[kWaves + 2], counted[kWaves][2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int chunk = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  // (heads first: the chunks of a head share a die's L2 where the heads are a multiple of eight)
+  const int h = blockIdx.x, chunk = blockIdx.y, b = blockIdx.z;
   const int n = min(max(a.kv_lens[b], 0), a.max_kv);
   int* keep = a.keep + ((long long)b * a.cache.heads + h) * a.budget;
   if (n <= a.budget) {
@@ -230,6 +244,14 @@ kv_evict_long_kernel(KvEvictArgs a, LongPlan p) {
   uint32_t T = 0u;
   int missing = a.budget - a.sinks - a.recent, before = 0, equal = 0;
   const bool any = missing > 0;
+  // The numbers of a chunk that LDS holds are on their way while the last digit is found.
+  const bool whole = p.tokens <= kWhole;
+  uint4 own[kWhole / (kThreads * 4)];
+#pragma unroll
+  for (int k = 0; k < kWhole / (kThreads * 4); ++k) {
+    const int i = c0 + (k * kThreads + tid) * 4;
+    own[k] = whole && i < c1 ? load4(a, table, h, i) : make_uint4(0u, 0u, 0u, 0u);
+  }
   if constexpr (PASS > 0) {
     if constexpr (PASS > 1) {
       const Found f = p.found[pair * p.chunks + chunk];
@@ -242,9 +264,9 @@ kv_evict_long_kernel(KvEvictArgs a, LongPlan p) {
       const uint32_t* from = p.hist[(PASS - 1) & 1] + pair * p.chunks * kBins;
       const int top = kBins - 1 - 2 * tid;
       int high = 0, low = 0, high_before = 0, low_before = 0, bin, above;
-#pragma unroll 4
-      for (int k = 0; k < p.chunks; ++k) {
-        const uint2 x = *reinterpret_cast<const uint2*>(from + (long long)k * kBins + top - 1);
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        const uint2 x = k < p.chunks ? *reinterpret_cast<const uint2*>(from + (long long)k * kBins + top - 1) : make_uint2(0u, 0u);
         high += (int)x.y;
         low += (int)x.x;
         high_before += k < chunk ? (int)x.y : 0;
@@ -262,6 +284,7 @@ kv_evict_long_kernel(KvEvictArgs a, LongPlan p) {
         counted[wave][1] = same;
       }
       __syncthreads();
+#pragma unroll
       for (int k = 0; k < kWaves; ++k) {
         before += counted[k][0];
         equal += counted[k][1];
@@ -269,7 +292,9 @@ kv_evict_long_kernel(KvEvictArgs a, LongPlan p) {
     }
     if (PASS < 3 && tid == 0) p.found[pair * p.chunks + chunk] = {T, missing, before};
   }
-  auto get4 = [&](int i) { return load4(a, table, h, i); };
+#pragma unroll
+  for (int k = 0; k < kWhole / (kThreads * 4); ++k) *reinterpret_cast<uint4*>(held + (k * kThreads + tid) * 4) = own[k];
+  auto get4 = [&](int i) { return whole ? *reinterpret_cast<const uint4*>(held + (i - c0)) : load4(a, table, h, i); };
   if constexpr (PASS < 3) {
     for (int k = tid; k < kCopies * kBins; k += kThreads) (&hist[0][0])[k] = 0u;
     __syncthreads();
@@ -295,6 +320,7 @@ kv_evict_long_kernel(KvEvictArgs a, LongPlan p) {
       to[k] = sum;
     }
   } else {
+    __syncthreads();                                       // the numbers are in LDS
     if (h == 0 && chunk == 0 && tid == 0) a.new_lens[b] = a.budget;
     // the first and the last ones before this chunk are kept for sure, too
     before += min(c0, first) + max(c0 - last, 0);
@@ -308,17 +334,18 @@ kv_evict_long_kernel(KvEvictArgs a, LongPlan p) {
       counted[wave][1] = q;
     }
     __syncthreads();
-    for (int k = 0; k < wave; ++k) {
-      before += counted[k][0];
-      equal += counted[k][1];
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) {
+      before += k < wave ? counted[k][0] : 0;
+      equal += k < wave ? counted[k][1] : 0;
     }
     write_kept<false>(from, to, first, last, any, T, missing, before, equal, keep, get4);
   }
 }
 
-// Up to 16 chunks of 8192 tokens or more: every workgroup reads all chunks' counts.
+// Up to kChunks chunks of 8192 tokens or more: every workgroup reads all chunks' counts.
 size_t long_plan(int seqs, int heads, int max_kv, uint8_t* ws, LongPlan& p) {
-  const long long even = ((long long)max_kv + 15) / 16;
+  const long long even = ((long long)max_kv + kChunks - 1) / kChunks;
   p.tokens = (int)(even <= kWhole ? kWhole : (even + 4095) / 4096 * 4096);
   p.chunks = (int)(((long long)max_kv + p.tokens - 1) / p.tokens);
   const size_t all = (size_t)seqs * (size_t)heads * (size_t)p.chunks, hist = all * kBins * 4;
@@ -426,16 +453,17 @@ kv_compact_run_kernel(KvCompactArgs a) {
   const int h = blockIdx.x >> 1, b = blockIdx.y;
   const bool keys = (blockIdx.x & 1) == 0;
   const KvCacheArgs& c = a.cache;
-  const int count = min(a.counts[b], a.keep_stride), start = a.starts != nullptr ? a.starts[b] : 0;
   const int* table = a.table + (long long)b * a.table_stride;
   const int* keep = a.keep + ((long long)b * a.keep_heads + (a.keep_heads > 1 ? h : 0)) * a.keep_stride;
+  const int first = tid < a.keep_stride ? keep[tid] : -1;  // (before the count is known)
+  const int count = min(a.counts[b], a.keep_stride), start = a.starts != nullptr ? a.starts[b] : 0;
   uint4* codes = reinterpret_cast<uint4*>(keys ? c.k_codes : c.v_codes);
   uint8_t* scales = keys ? c.k_scales : c.v_scales;
   for (int j0 = 0; j0 < count; j0 += kRun) {
     const int j = j0 + tid;
     long long own = -1, own_to = -1;
     if (j < count) {
-      own = row_of(c, table, a.table_stride, h, keep[j]);
+      own = row_of(c, table, a.table_stride, h, j0 == 0 ? first : keep[j]);
       own_to = start > 0x7FFFFFFF - j ? -1 : row_of(c, table, a.table_stride, h, start + j);
       if (own == own_to || own_to < 0) own = -1;           // (in its place already, or no place)
     }
@@ -503,7 +531,7 @@ hipError_t launch_kv_evict(const KvEvictArgs& a, hipStream_t s) {
   }
   LongPlan p;
   long_plan(a.seqs, a.cache.heads, a.max_kv, a.ws, p);
-  const dim3 grid((unsigned)p.chunks, (unsigned)a.cache.heads, (unsigned)a.seqs);
+  const dim3 grid((unsigned)a.cache.heads, (unsigned)p.chunks, (unsigned)a.seqs);
   kv_evict_long_kernel<0><<<grid, kThreads, 0, s>>>(a, p);
   if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   kv_evict_long_kernel<1><<<grid, kThreads, 0, s>>>(a, p);
