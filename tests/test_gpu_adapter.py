@@ -206,3 +206,21 @@ def test_captured(ctx):
         eager = ctx.adapter_linear(bank, x, y, cu, which)
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(eager, want)
+
+
+@pytest.mark.parametrize("rank,fmt", [(16, "bf16"), (32, "int8"), (32, "mxfp4")])
+def test_one_kernel_or_two_the_same_bits(ctx, rank, fmt):
+    """Segments by themselves (one kernel) as all of them in one call (whose matrices are too many for that)."""
+    rng = np.random.default_rng(rank)
+    rows, K, N = 96, 2240, 6144
+    x, xs, _ = _rows(rng, fmt, rows, K)
+    y = _bf(rng, rows, N).to(DEV)
+    bank = T.Adapters(_bf(rng, 5, rank, K, scale=K ** -0.5).to(DEV), _bf(rng, 5, N, rank).to(DEV))
+    cu = np.array(sorted([0, rows] + list(rng.permutation(np.arange(1, rows))[:79])), np.int32)
+    which = rng.integers(-1, 5, 80).astype(np.int32)
+    out = ctx.adapter_linear(bank, x, y, S.dev(cu), S.dev(which), x_scale=xs)
+    for i in range(0, 80, 8):
+        a, b = int(cu[i]), int(cu[i + 8])
+        part = ctx.adapter_linear(bank, x[a:b].contiguous(), y[a:b].contiguous(), S.dev(cu[i:i + 9] - a), S.dev(which[i:i + 8]),
+                                  x_scale=None if xs is None else xs[a:b].contiguous())
+        assert torch.equal(part, out[a:b]), (a, b)

@@ -3,13 +3,13 @@
 //   out[t] = y[t] + c_a s_t (x[t] A_a^T) B_a^T,   a the adapter of row t's segment, s_t its
 //                                               row scale (INT8 codes), x bf16, INT8 or MXFP4
 //
-// Two kernels.  The first forms h = c s x A^T for tiles of rows of one segment and 16 to 64
-// of the adapter's ranks, its waves sharing the sum over K; h goes out as two bf16 terms (2^-16 of
-// itself is lost at most).  The second adds h B^T to y: the product starts from y in the
-// accumulator, so out is rounded once.  Both use the 16x16x32 bf16 MFMA.  x, A and B come through LDS, straight from
-// memory by whole lines: loaded as the operands' lanes hold them, 16 rows in turn, each lane's 16 bytes
-// were a cache access of their own (60 an instruction; 17776 rows of 1920 to 5760 by rank 32 took 121 us
-// for the second kernel then, its address units busy throughout).
+// Two kernels.  The first forms h = c s x A^T for tiles of rows of one segment and 16 to 64 of the adapter's
+// ranks, its waves sharing the sum over K; h goes out as two bf16 terms (2^-16 of itself is lost at most).
+// The second adds h B^T to y: the product starts from y in the accumulator, so out is rounded once.  Few rows
+// at low ranks have one kernel of both parts, with the same bits.  All use the 16x16x32 bf16 MFMA.  x, A and B
+// come through LDS, straight from memory by whole lines: loaded as the operands' lanes hold them, 16 rows in
+// turn, each lane's 16 bytes were a cache access of their own (60 an instruction; 17776 rows of 1920 to 5760
+// by rank 32 took 121 us for the second kernel then, its address units busy throughout).
 #include "../../include/tabit.h"
 #include "kv_common.h"
 #include "tile_common.h"
@@ -122,23 +122,24 @@ struct Rows<TABIT_FMT_MXFP4> {
 // h of 16 MR rows and 16 RB ranks.  A wave takes 64 elements of K at a time, every NW-th, through LDS of its
 // own, a step ahead: lane l holds row l % 16 of x (and rank l % 16 of A), 16 consecutive elements from
 // 16 (l / 16) on, the first eight for one product and the others for a second.
-template <int FMT, int MR, int RB, int NW>
-__global__ void __launch_bounds__(NW * 64)
-adapter_down_kernel(AdapterArgs a) {
+template <int FMT, int MR, int RB>
+struct Down {
+  static constexpr int ROWS = 16 * MR, RANKS = 16 * RB, STAGES = 2;
+  static constexpr int XB = ROWS * Rows<FMT>::PIECES * 16, WB = RANKS * 128;        // bytes of a step
+  static constexpr int PART = ROWS * (RANKS + 4) * 4;
+  static constexpr int PER_WAVE = STAGES * (XB + WB) > PART ? STAGES * (XB + WB) : PART;
+};
+// Adapter ad's ranks from r0 on of rows row0 .. row1 - 1 (16 MR at most); put(row of the tile, rank, high terms
+// of two ranks, low terms).
+template <int FMT, int MR, int RB, int NW, typename Put>
+__device__ __forceinline__ void form_h(const AdapterArgs& a, uint8_t (*smem)[Down<FMT, MR, RB>::PER_WAVE], int ad, int row0,
+                                       int row1, int r0, Put put) {
   using X = Rows<FMT>;
-  constexpr int ROWS = 16 * MR, RANKS = 16 * RB;
-  constexpr int XB = ROWS * X::PIECES * 16, WB = RANKS * 128, STAGES = 2;
+  using D = Down<FMT, MR, RB>;
+  constexpr int ROWS = D::ROWS, RANKS = D::RANKS, STAGES = D::STAGES, XB = D::XB, WB = D::WB;
   constexpr int XI = (XB + 1023) / 1024, WI = WB / 1024;             // instructions of a step
-  constexpr int PART = ROWS * (RANKS + 4) * 4, PER_WAVE = STAGES * (XB + WB) > PART ? STAGES * (XB + WB) : PART;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[NW][PER_WAVE];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int seg, row0, row1;
-  const unsigned blocks = (unsigned)a.rank / RANKS;
-  if (!find_tile(a, blockIdx.x / blocks, ROWS, lane, seg, row0, row1)) return;
-  const int ad = a.adapter[seg];
-  if ((unsigned)ad >= (unsigned)a.num_adapters) return;
-  const int r0 = blockIdx.x % blocks * RANKS;
   const int row = lane & 15, g = lane >> 4;
   // (asked for here, waited for at the end)
   const float c = a.scale != nullptr ? a.scale[ad] : 1.0f;
@@ -238,12 +239,76 @@ adapter_down_kernel(AdapterArgs a) {
     u *= c * f[i];
     v *= c * f[i];
     const uint32_t hi = pack_bf16(u, v);
-    const long long at = (long long)(row0 + t) * a.rank + r0 + r;
-    *reinterpret_cast<uint32_t*>(a.hi + at) = hi;
     // (what rounds to infinity has no second term)
     const float ul = u - bf_lo(hi), vl = v - bf_hi(hi);
-    *reinterpret_cast<uint32_t*>(a.lo + at) = pack_bf16(finite_f32(ul) ? ul : 0.0f, finite_f32(vl) ? vl : 0.0f);
+    put(t, r, hi, pack_bf16(finite_f32(ul) ? ul : 0.0f, finite_f32(vl) ? vl : 0.0f));
   }
+}
+
+template <int FMT, int MR, int RB, int NW>
+__global__ void __launch_bounds__(NW * 64)
+adapter_down_kernel(AdapterArgs a) {
+  using D = Down<FMT, MR, RB>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NW][D::PER_WAVE];
+  int seg, row0, row1;
+  const unsigned blocks = (unsigned)a.rank / D::RANKS;
+  if (!find_tile(a, blockIdx.x / blocks, D::ROWS, threadIdx.x & 63, seg, row0, row1)) return;
+  const int ad = a.adapter[seg];
+  if ((unsigned)ad >= (unsigned)a.num_adapters) return;
+  const int r0 = blockIdx.x % blocks * D::RANKS;
+  form_h<FMT, MR, RB, NW>(a, smem, ad, row0, row1, r0, [&](int t, int r, uint32_t hi, uint32_t lo) {
+    const long long at = (long long)(row0 + t) * a.rank + r0 + r;
+    *reinterpret_cast<uint32_t*>(a.hi + at) = hi;
+    *reinterpret_cast<uint32_t*>(a.lo + at) = lo;
+  });
+}
+
+// Columns n0 + 8 i + j of B as row 16 j + i of 128 in LDS (those past N read the last one and are not kept), every
+// EACH-th instruction of them from `from` on.
+template <int R, int EACH>
+__device__ __forceinline__ void bring_b(const AdapterArgs& a, const uint16_t* bp, int n0, uint8_t* to, int from, int lane) {
+  constexpr int PIECES = R / 8;
+#pragma unroll
+  for (int i = from; i < 128 * R * 2 / 1024; i += EACH) {
+    const int s = i * 64 + lane, q = s / PIECES, p = (s % PIECES) ^ turned<PIECES>(q & 15);
+    const int n = min(n0 + 8 * (q & 15) + (q >> 4), a.N - 1);
+    __builtin_amdgcn_global_load_lds((from_t)(bp + (long long)n * R + p * 8), (to_t)(to + i * 1024), 16, 0, 0);
+  }
+}
+
+// acc (rows 4 (l / 16) + r, columns 8 (l % 16) + j) + h . B of those columns
+template <int R, int KC>
+__device__ __forceinline__ void add_up(const uint8_t* stage, const v8bf (&hi)[KC], const v8bf (&lo)[KC], int row, int g, v4f (&acc)[8]) {
+  constexpr int PIECES = R / 8;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint8_t* b = stage + j * 16 * R * 2;
+    if constexpr (R == 16) {
+      acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[0], *reinterpret_cast<const v8bf*>(b + place<PIECES>(row, g & 1)), acc[j], 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int kc = 0; kc < KC; ++kc) {
+        const v8bf w = *reinterpret_cast<const v8bf*>(b + place<PIECES>(row, 4 * kc + g));
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[kc], w, acc[j], 0, 0, 0);
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[kc], w, acc[j], 0, 0, 0);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void start_from(const uint4 (&y)[4], v4f (&acc)[8]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    float v[8];
+    unpack8(y[r], v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j][r] = v[j];
+  }
+}
+
+__device__ __forceinline__ uint4 row_of(const v4f (&acc)[8], int r) {
+  return make_uint4(pack_bf16(acc[0][r], acc[1][r]), pack_bf16(acc[2][r], acc[3][r]),
+                    pack_bf16(acc[4][r], acc[5][r]), pack_bf16(acc[6][r], acc[7][r]));
 }
 
 // out of 16 rows a wave, 128 columns at a time: h is the first operand and product j takes columns
@@ -256,7 +321,7 @@ __global__ void __launch_bounds__(256)
 adapter_up_kernel(AdapterArgs a, int cols) {
   constexpr int ROWS = WIDE ? 64 : 16, COLS = 128;
   constexpr int KC = R <= 32 ? 1 : R / 32;             // 32-rank chunks
-  constexpr int PIECES = R / 8, BYTES = COLS * R * 2;
+  constexpr int BYTES = COLS * R * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[WIDE ? 2 : 4][BYTES];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -272,15 +337,8 @@ adapter_up_kernel(AdapterArgs a, int cols) {
   const int first = (int)(blockIdx.x % blocks) * cols + (WIDE ? 0 : wave * COLS);
   const int last = min((int)(blockIdx.x % blocks + 1) * cols, a.N);
   const uint16_t* bp = a.b + (long long)(has ? ad : 0) * a.N * R;
-  // Columns n0 + 8 i + j as row 16 j + i (those past N read the last one and are not kept)
   auto bring = [&](int n0, uint8_t* to) {
-    if (!has || n0 >= last) return;
-#pragma unroll
-    for (int i = WIDE ? wave : 0; i < BYTES / 1024; i += WIDE ? 4 : 1) {
-      const int s = i * 64 + lane, q = s / PIECES, p = (s % PIECES) ^ turned<PIECES>(q & 15);
-      const int n = min(n0 + 8 * (q & 15) + (q >> 4), a.N - 1);
-      __builtin_amdgcn_global_load_lds((from_t)(bp + (long long)n * R + p * 8), (to_t)(to + i * 1024), 16, 0, 0);
-    }
+    if (has && n0 < last) bring_b<R, WIDE ? 4 : 1>(a, bp, n0, to, WIDE ? wave : 0, lane);
   };
   uint8_t* stage = smem[WIDE ? 0 : wave];
   bring(first, stage);
@@ -315,40 +373,74 @@ adapter_up_kernel(AdapterArgs a, int cols) {
       __builtin_amdgcn_wave_barrier();
     }
     v4f acc[8];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float v[8];
-      unpack8(y[r], v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j][r] = v[j];
-    }
-    if (has) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint8_t* b = stage + j * 16 * R * 2;
-        if constexpr (R == 16) {
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[0], *reinterpret_cast<const v8bf*>(b + place<PIECES>(row, g & 1)), acc[j], 0, 0, 0);
-        } else {
-#pragma unroll
-          for (int kc = 0; kc < KC; ++kc) {
-            const v8bf w = *reinterpret_cast<const v8bf*>(b + place<PIECES>(row, 4 * kc + g));
-            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[kc], w, acc[j], 0, 0, 0);
-            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[kc], w, acc[j], 0, 0, 0);
-          }
-        }
-      }
-    }
+    start_from(y, acc);
+    if (has) add_up<R, KC>(stage, hi, lo, row, g, acc);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
       if (n < a.N && t0 + 4 * g + r < row1)
-        *reinterpret_cast<uint4*>(a.out + (t0 + 4 * g + r) * a.out_stride + n) =
-            make_uint4(pack_bf16(acc[0][r], acc[1][r]), pack_bf16(acc[2][r], acc[3][r]),
-                       pack_bf16(acc[4][r], acc[5][r]), pack_bf16(acc[6][r], acc[7][r]));
+        *reinterpret_cast<uint4*>(a.out + (t0 + 4 * g + r) * a.out_stride + n) = row_of(acc, r);
     if constexpr (!WIDE) {
       __builtin_amdgcn_wave_barrier();
       bring(n0 + STRIDE, stage);
     }
   }
+}
+
+// Both at once, for few rows and low ranks: every workgroup (16 rows, 1024 columns, 128 a wave) forms h for itself.
+template <int FMT, int R>
+__global__ void __launch_bounds__(512)
+adapter_few_kernel(AdapterArgs a) {
+  using D = Down<FMT, 1, R / 16>;
+  constexpr int NW = 8, COLS = 128, KC = 1, BYTES = COLS * R * 2;
+  static_assert(R <= 32, "one operand of h");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NW][D::PER_WAVE];
+  __shared__ __attribute__((aligned(1024))) uint8_t stage[NW][BYTES];
+  auto h = reinterpret_cast<uint16_t (*)[16][R]>(smem[0]);         // [2][16][R]: both terms, when x and A are done with
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row = lane & 15, g = lane >> 4;
+  int seg, row0, row1;
+  const unsigned blocks = ((unsigned)a.N + NW * COLS - 1) / (NW * COLS);
+  if (!find_tile(a, blockIdx.x / blocks, 16, lane, seg, row0, row1)) return;
+  const int ad = a.adapter[seg];
+  const bool has = (unsigned)ad < (unsigned)a.num_adapters;
+  if (!has && a.out == a.y) return;
+  const int n0 = (int)(blockIdx.x % blocks) * NW * COLS + wave * COLS, n = n0 + 8 * row;
+  uint4 y[4] = {};
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (n < a.N && row0 + 4 * g + r < row1) y[r] = *reinterpret_cast<const uint4*>(a.y + (row0 + 4 * g + r) * a.y_stride + n);
+  v4f acc[8];
+  if (has) {
+    if (n0 < a.N) bring_b<R, 1>(a, a.b + (long long)ad * a.N * R, n0, stage[wave], 0, lane);
+    static_assert(16 * R / 2 <= NW * 64, "at most two ranks a thread");
+    int t = -1, r = 0;
+    uint32_t high = 0u, low = 0u;
+    form_h<FMT, 1, R / 16, NW>(a, smem, ad, row0, row1, 0, [&](int t_, int r_, uint32_t hi, uint32_t lo) {
+      t = t_;
+      r = r_;
+      high = hi;
+      low = lo;
+    });
+    __syncthreads();
+    if (t >= 0) {
+      *reinterpret_cast<uint32_t*>(&h[0][t][r]) = high;
+      *reinterpret_cast<uint32_t*>(&h[1][t][r]) = low;
+    }
+    tile::wait_vmcnt0();
+    __syncthreads();
+    // (rows past the segment have no h, and no place)
+    const v8bf hi[1] = {R == 16 ? *reinterpret_cast<const v8bf*>(&h[g >> 1][row][8 * (g & 1)]) : *reinterpret_cast<const v8bf*>(&h[0][row][8 * g])};
+    const v8bf lo[1] = {*reinterpret_cast<const v8bf*>(&h[1][row][R == 16 ? 0 : 8 * g])};
+    start_from(y, acc);
+    add_up<R, KC>(stage[wave], hi, lo, row, g, acc);
+  } else {
+    start_from(y, acc);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (n < a.N && row0 + 4 * g + r < row1)
+      *reinterpret_cast<uint4*>(a.out + (row0 + 4 * g + r) * a.out_stride + n) = row_of(acc, r);
 }
 
 // Each row of A times the block transform over 1 / b.  A wave holds 512 elements, eight a lane.
@@ -376,6 +468,14 @@ unsigned tiles(const AdapterArgs& a, int tile) { return (unsigned)tiles_of(a.row
 // Segments of few rows (single tokens): small tiles, more waves on one sum.
 bool few_rows(int rows, int segments) { return rows <= 16ll * segments; }
 bool few_rows(const AdapterArgs& a) { return few_rows(a.rows, a.segments); }
+// One kernel for both, where reading A again for every 1024 columns costs less than a launch: up to 32 MB in all.
+// Measured under a graph, two kernels and one: 4 rows of 2240 to 2240, rank 16 (0.9 MB) 7.0 and 5.0 us; 32 rows
+// of 4096 to 6144, ranks 16 (26 MB) and 32 (53 MB) 8.9 and 6.8, 9.2 and 12.5; 64 of 2240 to 2240, rank 32 (28 MB)
+// 8.5 and 7.4; 256 of 1152 to 1152, ranks 16 (20 MB) and 32 (40 MB) 10.1 and 7.4, 11.9 and 15.0.
+bool at_once(const AdapterArgs& a) {
+  return few_rows(a) && a.rank <= 32 &&
+         (long long)tiles(a, 16) * ((a.N + 1023) / 1024) * a.rank * a.K * 2 <= (1ll << 25);
+}
 
 // Measured, 64 rows of 4096 in INT8, rank 64, 40 adapters: 4, 8 and 16 waves 12.5, 9.1 and 8.6 us, one row of
 // 2240 in each of four segments 4.5, 3.8 and 4.2.  17776 rows of 1920, rank 32: 16, 32 and 64 rows by four
@@ -387,6 +487,14 @@ hipError_t down(const AdapterArgs& a, hipStream_t s) {
   else if (a.rank == 16) adapter_down_kernel<FMT, 2, 1, 4><<<tiles(a, 32), 256, 0, s>>>(a);
   else if (a.rank == 32) adapter_down_kernel<FMT, 2, 2, 4><<<tiles(a, 32), 256, 0, s>>>(a);
   else adapter_down_kernel<FMT, 2, 4, 4><<<tiles(a, 32) * (a.rank / 64), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int FMT>
+hipError_t few(const AdapterArgs& a, hipStream_t s) {
+  const unsigned grid = tiles(a, 16) * ((a.N + 1023) / 1024);
+  if (a.rank == 16) adapter_few_kernel<FMT, 16><<<grid, 512, 0, s>>>(a);
+  else adapter_few_kernel<FMT, 32><<<grid, 512, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -409,6 +517,10 @@ bool adapter_fits(int rows, int segments, int rank, int N) {
 }
 
 hipError_t launch_adapter_linear(const AdapterArgs& a, hipStream_t s) {
+  if (at_once(a))
+    return a.x_fmt == TABIT_FMT_BF16   ? few<TABIT_FMT_BF16>(a, s)
+           : a.x_fmt == TABIT_FMT_INT8 ? few<TABIT_FMT_INT8>(a, s)
+                                       : few<TABIT_FMT_MXFP4>(a, s);
   const hipError_t e = a.x_fmt == TABIT_FMT_BF16   ? down<TABIT_FMT_BF16>(a, s)
                        : a.x_fmt == TABIT_FMT_INT8 ? down<TABIT_FMT_INT8>(a, s)
                                                    : down<TABIT_FMT_MXFP4>(a, s);
