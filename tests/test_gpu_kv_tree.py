@@ -66,6 +66,18 @@ def test_against_64_bits(ctx, lens, qs, hq, hk, D, ps, had, kind):
     A.check(*_run(ctx, p, _mask(p, see)), S.tree_want(p, see))
 
 
+@pytest.mark.parametrize("lens,qs,hq,hk,D,ps", [
+    ([1000, 300, 20], [8, 3, 6], 16, 4, 128, 16), ([90], [32], 2, 2, 96, 32), ([513, 70], [10, 1], 6, 2, 72, 16),
+    ([4000, 17], [17, 17], 1, 1, 128, 64), ([200, 90], [33, 5], 1, 1, 128, 16),
+])
+@pytest.mark.parametrize("kind", ["tree", "any"])
+def test_about_32_rows(ctx, lens, qs, hq, hk, D, ps, kind):
+    """Rows of two tiles of 16, where there are no more (33: one of 128)."""
+    p = A.problem(sum(lens) + 7 * D, lens, qs, hq, hk, D, ps, 32, k=3)
+    see = _see(p, np.random.default_rng(D), kind)
+    A.check(*_run(ctx, p, _mask(p, see)), S.tree_want(p, see))
+
+
 @pytest.mark.parametrize("n", [3, 40])
 def test_rows_that_see_nothing_answer_zeros(ctx, n):
     """A cache that holds the tree alone, and a mask without a node: zeros and -infinity."""

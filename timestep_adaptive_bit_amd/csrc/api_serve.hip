@@ -47,7 +47,7 @@ extern "C" {
 size_t tabit_kv_tree_attention_workspace_bytes(int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
                                                int num_seqs, int max_q, int max_kv) {
   if (!valid_sizes(num_tokens, num_q_heads, num_kv_heads, head_dim, num_seqs, max_q, max_kv)) return 0;
-  const int splits = tabit::kv_tree_splits(num_seqs, max_q, num_q_heads, num_kv_heads, max_kv);
+  const int splits = tabit::kv_tree_splits(num_seqs, max_q, num_q_heads, num_kv_heads, max_kv, (head_dim + 31) / 32 * 32);
   if (splits <= 1) return 0;
   return (size_t)splits * (size_t)num_tokens * (size_t)num_q_heads * (size_t)((head_dim + 31) / 32 * 32 + 2) *
          sizeof(float);
@@ -67,7 +67,7 @@ int tabit_kv_tree_attention(tabit_ctx* ctx, const tabit_kv_cache* cache, const t
     return fail(ctx, TABIT_ESHAPE, "%d words do not hold the mask of %d nodes", mask_words, a->max_q);
   if (!aligned(mask, 8)) return fail(ctx, TABIT_EALIGN, "mask must be 8-byte aligned");
   if (a->num_tokens == 0 || a->num_seqs == 0 || a->max_q == 0) return TABIT_OK;
-  k.splits = tabit::kv_tree_splits(a->num_seqs, a->max_q, a->num_q_heads, k.cache.heads, a->max_kv);
+  k.splits = tabit::kv_tree_splits(a->num_seqs, a->max_q, a->num_q_heads, k.cache.heads, a->max_kv, k.cache.dim_pad);
   if ((st = check_grid(ctx, a, k.splits)) != TABIT_OK) return st;
   const size_t need = tabit_kv_tree_attention_workspace_bytes(
       a->num_tokens, a->num_q_heads, k.cache.heads, k.cache.head_dim, a->num_seqs, a->max_q, a->max_kv);

@@ -1182,12 +1182,16 @@ kv_attention_join_kernel(KvAttnArgs a) {
 // waves) while they fit, else 128.  Measured for up to 16 rows, by 16 and by 128: 64 rows
 // of up to 8192 keys 87 and 158 us, one row of 131072 keys 40 and 55, of 1000 keys 15 and
 // 18.  At 32 rows neither form is ahead: 64 sequences x 4096 keys 92 and 84 us, one of 131072
-// keys 43 and 51; at 16 sequences of 64 rows x 8192 keys 89 and 68 us.
-inline bool few_rows(int max_q, int group) { return (long long)max_q * group <= 16; }
+// keys 43 and 51; at 16 sequences of 64 rows x 8192 keys 89 and 68 us.  Trees of up to 32 rows of more than
+// 64 elements go by 16, too: 16 x 32 rows x up to 8192 keys 46 and 51 us, 64 x 32 x 1000 (72 elements) 44 and
+// 58, one of 32 x 1000 16.6 and 18.0; with 64 elements 8 x 32 x 4000 45 and 38, one of 20 x 50000 37 and 34.
+inline bool few_rows(int max_q, int group, bool tree, int dim_pad) {
+  return (long long)max_q * group <= (tree && dim_pad > 64 ? 32 : 16);
+}
 
 template <int NB, bool TREE>
 hipError_t launch_nb(const KvAttnArgs& a, hipStream_t s) {
-  const bool few = few_rows(a.max_q, a.group);
+  const bool few = few_rows(a.max_q, a.group, TREE, a.cache.dim_pad);
   const int per = few ? 16 : 128;
   const int row_tiles = (int)(((long long)a.max_q * a.group + per - 1) / per);
   const unsigned per_head = (unsigned)((long long)row_tiles * a.splits);
@@ -1223,12 +1227,10 @@ hipError_t launch_nb(const KvAttnArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-}  // namespace
-
-int kv_attention_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_kv) {
+int splits_of(int seqs, int max_q, int q_heads, int kv_heads, int max_kv, bool tree, int dim_pad) {
   if (seqs <= 0 || max_q <= 0 || kv_heads <= 0) return 1;
   const int group = q_heads / kv_heads;
-  const bool few = few_rows(max_q, group);
+  const bool few = few_rows(max_q, group, tree, dim_pad);
   const long long row_tiles = ((long long)max_q * group + (few ? 15 : 127)) / (few ? 16 : 128);
   const long long base = (long long)seqs * kv_heads * row_tiles;
   const long long tiles = ((long long)max_kv + TILE - 1) / TILE;
@@ -1265,7 +1267,7 @@ int kv_attention_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_
 }
 
 template <bool TREE>
-static hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
+hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
   switch (a.cache.dim_pad) {
     case 32: return launch_nb<1, TREE>(a, s);
     case 64: return launch_nb<2, TREE>(a, s);
@@ -1275,10 +1277,16 @@ static hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
   }
 }
 
+}  // namespace
+
+int kv_attention_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_kv) {
+  return splits_of(seqs, max_q, q_heads, kv_heads, max_kv, false, 0);
+}
+
 hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t s) { return launch<false>(a, s); }
 
-int kv_tree_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_kv) {
-  return kv_attention_splits(seqs, max_q, q_heads, kv_heads, max_kv);
+int kv_tree_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_kv, int dim_pad) {
+  return splits_of(seqs, max_q, q_heads, kv_heads, max_kv, true, dim_pad);
 }
 
 hipError_t launch_kv_tree_attention(const KvAttnArgs& a, hipStream_t s) { return launch<true>(a, s); }
