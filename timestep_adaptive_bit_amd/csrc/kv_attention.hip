@@ -7,6 +7,10 @@
 // once per row).  Keys j < len are visible, with `causal` also only j <= len - n + i
 // to query i of the n of a sequence.  A row that sees no key answers 0.
 //
+// Trees of drafted tokens (TREE) see by a mask: of the last n keys of a sequence those whose bit is set in the
+// row's words, 64 of which are lined up with a tile of 64 keys by two loads and a shift, and every key before
+// them.  Only tiles that reach into the tree look at it, so it costs nothing beside the rest.
+//
 // Rows of one key head are packed as (query, head of the group), so the heads
 // that share keys share every byte read of them.  A wave takes 64 keys at a time
 // and 16 rows:

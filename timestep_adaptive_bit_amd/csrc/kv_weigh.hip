@@ -97,6 +97,7 @@ __device__ __forceinline__ void split_terms(float (&x)[32], bool ok, uint32_t& s
   }
 }
 
+// The rows' terms, a lane a block of 32 elements (3584 rows of 32 heads x 128: 24 us, 57 MB written).
 template <int NB>
 __global__ void __launch_bounds__(64 * ((NB + 1) / 2))
 kv_weigh_rows_kernel(KvAttnArgs a, Plan p) {
@@ -280,7 +281,12 @@ __device__ __forceinline__ float join_ranges(const KvAttnArgs& a, const Plan& p,
 }
 
 // L of 128 rows, 32 a wave, over one range of keys.  A tile of 64 keys comes to LDS once for all waves, 16
-// keys each, while the tile before is worked on (two stages, one barrier a tile).
+// keys each, while the tile before is worked on (two stages, one barrier a tile).  Bound by the matrix cores at
+// the power that such operands take: a wave's tile is 20 products, which take 1130 cycles of a SIMD by
+// themselves with random codes (722 with constant ones), 1264 with the exponentials and 1478 in here, batches of
+// equal lengths without a mask; causal ragged ones 1880, their workgroups' ends included (2 x 2048 rows behind
+// 6144 keys at most, 32 heads over 8: 138 us).  Level or slower: one barrier for two tiles, the chains of products
+// fenced or given a priority.
 template <int NB>
 __global__ void __launch_bounds__(256, 3)
 kv_weigh_stats_kernel(KvAttnArgs a, Plan p) {
@@ -436,8 +442,9 @@ kv_weigh_join_kernel(KvAttnArgs a, Plan p) {
   if (a.lse != nullptr && rr < n * a.group) write_lse(a, q0, hk, rr, sum, l);
 }
 
-// Sums of 64 keys a wave over all rows that see them.  (128 keys a wave take 208 registers and leave two waves
-// a SIMD: 415 us for 315, long prompts, the whole call.)  The workgroup's waves go over the row
+// Sums of 64 keys a wave over all rows that see them; bound as the statistics (150 us there).  (128 keys a wave take
+// 208 registers and leave two waves a SIMD: 415 us for 315, long prompts, the whole call; a tile's terms in
+// registers, not read from LDS for every product, 64 and 128 keys a wave, 166 and 172 us for 147, this kernel.)  The workgroup's waves go over the row
 // tiles together: a tile's terms come to LDS once for all, straight from memory, while the tile before is
 // worked on (two stages, one barrier a tile).  With more than one range of row tiles, sums
 // go to the workspace and are added up by a kernel of their own.
@@ -623,8 +630,10 @@ __device__ __forceinline__ void few_range(const KvAttnArgs& a, int splits, int l
 }
 
 // Scores of a range of keys of one key head, and each row's (reference, sum) over it.  Its tiles go
-// to the waves in runs.  Bound by the keys' bytes: a wave has two tiles on their way to its own LDS while it
-// works on a third.
+// to the waves in runs.  Bound by the keys' bytes and by the longest sequences, which end alone: a wave has two
+// tiles on their way to its own LDS while it works on a third (64 rows of up to 8192 keys, 8 key heads of 128:
+// 54 us, 4.2 TB/s with the scores that go out).  Level or slower: a third tile on its way, heads as the fastest
+// index, four rows held twice so that each half of a wave weighs half of a tile's keys (59 us).
 template <int NB, int R>
 __global__ void __launch_bounds__(256)
 kv_weigh_scores_kernel(KvAttnArgs a, FewPlan p) {
