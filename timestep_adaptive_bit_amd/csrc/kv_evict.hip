@@ -445,9 +445,9 @@ kv_compact_kernel(KvCompactArgs a) {
 
 // In place: one workgroup takes the keys (or values) of one head, kRun rows at a time, which are read
 // whole before the first is written.  What comes later lies behind all places written so far.  Bound by rows of
-// 64 bytes in any place: 32 lists of 2048 of 8 heads x 128 elements (101 MB read, 105 written) 51 us, 4.0 TB/s.
+// 64 bytes in any place: 32 lists of 2048 of 8 heads x 128 elements (70 MB read, 73 written) 51 us, 2.8 TB/s.
 // 2048, 1024 and 512 rows at a time by a thread each were 74, 54 and 56 us, by half as many threads 71 to 80;
-// with the next run's places looked up beside this one's rows 66.
+// with the next run's places looked up beside this one's rows 66, with its rows read beside this one's writes 57.
 constexpr int kRun = kThreads;
 template <int NB>
 __global__ void __launch_bounds__(kRun)
