@@ -52,6 +52,8 @@ __device__ __forceinline__ bool find_tile(const AdapterArgs& a, int tile, int ro
   return false;
 }
 
+typedef int v2i __attribute__((ext_vector_type(2)));
+
 __device__ __forceinline__ v8bf zero8() { return __builtin_bit_cast(v8bf, make_uint4(0u, 0u, 0u, 0u)); }
 
 typedef const __attribute__((address_space(1))) void* from_t;
@@ -87,13 +89,15 @@ struct Rows<TABIT_FMT_INT8> {
   static __device__ __forceinline__ const void* at(const AdapterArgs& a, int t, int k) {
     return static_cast<const int8_t*>(a.x) + (long long)t * a.K + k;
   }
-  static __device__ __forceinline__ uint32_t pair(uint32_t w, int at) {
+  static __device__ __forceinline__ uint32_t pair(int w, int at) {
     return pack_bf16((float)(int8_t)(w >> at), (float)(int8_t)(w >> (at + 8)));
   }
   static __device__ __forceinline__ void get(const uint8_t* lds, int i, int g, uint32_t, v8bf (&x)[2]) {
-    const uint4 w = *reinterpret_cast<const uint4*>(lds + place<4>(i, g));
-    x[0] = __builtin_bit_cast(v8bf, make_uint4(pair(w.x, 0), pair(w.x, 16), pair(w.y, 0), pair(w.y, 16)));
-    x[1] = __builtin_bit_cast(v8bf, make_uint4(pair(w.z, 0), pair(w.z, 16), pair(w.w, 0), pair(w.w, 16)));
+    // (a vector type, as v8bf: a HIP struct loses the access's alias information, and the compiler then has it
+    // wait for every copy that is on its way to LDS, the next step's, too)
+    const v4i w = *reinterpret_cast<const v4i*>(lds + place<4>(i, g));
+    x[0] = __builtin_bit_cast(v8bf, make_uint4(pair(w[0], 0), pair(w[0], 16), pair(w[1], 0), pair(w[1], 16)));
+    x[1] = __builtin_bit_cast(v8bf, make_uint4(pair(w[2], 0), pair(w[2], 16), pair(w[3], 0), pair(w[3], 16)));
   }
 };
 template <>
@@ -113,9 +117,9 @@ struct Rows<TABIT_FMT_MXFP4> {
     return __builtin_bit_cast(v8bf, y);
   }
   static __device__ __forceinline__ void get(const uint8_t* lds, int i, int g, uint32_t scale, v8bf (&x)[2]) {
-    const uint2 w = *reinterpret_cast<const uint2*>(lds + place<2>(i, g >> 1) + 8 * (g & 1));
-    x[0] = eight(w.x, scale);
-    x[1] = eight(w.y, scale);
+    const v2i w = *reinterpret_cast<const v2i*>(lds + place<2>(i, g >> 1) + 8 * (g & 1));
+    x[0] = eight((uint32_t)w[0], scale);
+    x[1] = eight((uint32_t)w[1], scale);
   }
 };
 
@@ -130,8 +134,11 @@ struct Down {
   static constexpr int PER_WAVE = STAGES * (XB + WB) > PART ? STAGES * (XB + WB) : PART;
 };
 // Adapter ad's ranks from r0 on of rows row0 .. row1 - 1 (16 MR at most); put(row of the tile, rank, high terms
-// of two ranks, low terms).
-template <int FMT, int MR, int RB, int NW, typename Put>
+// of two ranks, low terms).  LATE: the next step is asked for when this one has been read, not before it is waited
+// for.  A third step on its way is level in either order.  4 rows of 2240, rank 16, 4.6 us late and 4.8 first, one of
+// 12288 in INT8 9.3 and 11.0 (one kernel for both products); 32 rows of 12288, rank 64, 17.7 and 14.3, 17776 of
+// 1920 in bf16, rank 32, 101 and 98 (two kernels).
+template <int FMT, int MR, int RB, int NW, bool LATE, typename Put>
 __device__ __forceinline__ void form_h(const AdapterArgs& a, uint8_t (*smem)[Down<FMT, MR, RB>::PER_WAVE], int ad, int row0,
                                        int row1, int r0, Put put) {
   using X = Rows<FMT>;
@@ -189,8 +196,8 @@ __device__ __forceinline__ void form_h(const AdapterArgs& a, uint8_t (*smem)[Dow
   for (int step = 0;; ++step) {
     const int k0 = (step * NW + wave) * 64;
     if (k0 >= a.K) break;
-    ask(step + 1);
-    if (k0 + NW * 64 < a.K) tile::wait_vmcnt<XI + WI>();     // this step's are here, the next one's not
+    if (!LATE) ask(step + 1);
+    if (!LATE && k0 + NW * 64 < a.K) tile::wait_vmcnt<XI + WI>();     // this step's are here, the next one's not
     else tile::wait_vmcnt0();
     __builtin_amdgcn_wave_barrier();
     const uint8_t* st = smem[wave] + step % STAGES * (XB + WB);
@@ -201,6 +208,10 @@ __device__ __forceinline__ void form_h(const AdapterArgs& a, uint8_t (*smem)[Dow
     for (int r = 0; r < RB; ++r)
 #pragma unroll
       for (int e = 0; e < 2; ++e) w[r][e] = *reinterpret_cast<const v8bf*>(st + XB + place<8>(16 * r + row, 2 * g + e));
+    if (LATE) {
+      __builtin_amdgcn_wave_barrier();
+      ask(step + 1);
+    }
     if (k0 + 64 > a.K && k0 + 16 * g >= a.K) {
 #pragma unroll
       for (int m = 0; m < MR; ++m) x[m][0] = x[m][1] = zero8();
@@ -256,7 +267,7 @@ adapter_down_kernel(AdapterArgs a) {
   const int ad = a.adapter[seg];
   if ((unsigned)ad >= (unsigned)a.num_adapters) return;
   const int r0 = blockIdx.x % blocks * D::RANKS;
-  form_h<FMT, MR, RB, NW>(a, smem, ad, row0, row1, r0, [&](int t, int r, uint32_t hi, uint32_t lo) {
+  form_h<FMT, MR, RB, NW, false>(a, smem, ad, row0, row1, r0, [&](int t, int r, uint32_t hi, uint32_t lo) {
     const long long at = (long long)(row0 + t) * a.rank + r0 + r;
     *reinterpret_cast<uint32_t*>(a.hi + at) = hi;
     *reinterpret_cast<uint32_t*>(a.lo + at) = lo;
@@ -393,8 +404,10 @@ adapter_few_kernel(AdapterArgs a) {
   using D = Down<FMT, 1, R / 16>;
   constexpr int NW = 8, COLS = 128, KC = 1, BYTES = COLS * R * 2;
   static_assert(R <= 32, "one operand of h");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[NW][D::PER_WAVE];
-  __shared__ __attribute__((aligned(1024))) uint8_t stage[NW][BYTES];
+  // (one array: with two, the compiler tells their copies apart and has reads of one wait for all of its copies)
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NW * (BYTES + D::PER_WAVE)];
+  auto stage = reinterpret_cast<uint8_t (*)[BYTES]>(lds);
+  auto smem = reinterpret_cast<uint8_t (*)[D::PER_WAVE]>(lds + NW * BYTES);
   auto h = reinterpret_cast<uint16_t (*)[16][R]>(smem[0]);         // [2][16][R]: both terms, when x and A are done with
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -416,7 +429,7 @@ adapter_few_kernel(AdapterArgs a) {
     static_assert(16 * R / 2 <= NW * 64, "at most two ranks a thread");
     int t = -1, r = 0;
     uint32_t high = 0u, low = 0u;
-    form_h<FMT, 1, R / 16, NW>(a, smem, ad, row0, row1, 0, [&](int t_, int r_, uint32_t hi, uint32_t lo) {
+    form_h<FMT, 1, R / 16, NW, true>(a, smem, ad, row0, row1, 0, [&](int t_, int r_, uint32_t hi, uint32_t lo) {
       t = t_;
       r = r_;
       high = hi;
@@ -469,7 +482,7 @@ unsigned tiles(const AdapterArgs& a, int tile) { return (unsigned)tiles_of(a.row
 bool few_rows(int rows, int segments) { return rows <= 16ll * segments; }
 bool few_rows(const AdapterArgs& a) { return few_rows(a.rows, a.segments); }
 // One kernel for both, where reading A again for every 1024 columns costs less than a launch: up to 32 MB in all.
-// Measured under a graph, two kernels and one: 4 rows of 2240 to 2240, rank 16 (0.9 MB) 7.0 and 5.0 us; 32 rows
+// Measured under a graph, two kernels and one: 4 rows of 2240 to 2240, rank 16 (0.9 MB) 7.0 and 4.6 us; 32 rows
 // of 4096 to 6144, ranks 16 (26 MB) and 32 (53 MB) 8.9 and 6.8, 9.2 and 12.5; 64 of 2240 to 2240, rank 32 (28 MB)
 // 8.5 and 7.4; 256 of 1152 to 1152, ranks 16 (20 MB) and 32 (40 MB) 10.1 and 7.4, 11.9 and 15.0.
 bool at_once(const AdapterArgs& a) {
