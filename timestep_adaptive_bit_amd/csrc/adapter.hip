@@ -491,9 +491,9 @@ bool at_once(const AdapterArgs& a) {
 }
 
 // Measured, 64 rows of 4096 in INT8, rank 64, 40 adapters: 4, 8 and 16 waves 12.5, 9.1 and 8.6 us, one row of
-// 2240 in each of four segments 4.5, 3.8 and 4.2.  17776 rows of 1920, rank 32: 16, 32 and 64 rows by four
-// waves 25, 19.5 and 19.6, 32 by eight 24.5; a third stage 25.5 (13 us where the rows come from a cache;
-// 2.6 TB/s, A from the L2 as often as x from memory).
+// 2240 in each of four segments 4.5, 3.8 and 4.2 (8 waves are 8.1 us now for the first).  17776 rows of 1920, rank
+// 32: 16, 32 and 64 rows by four waves 25, 19.5 and 19.6 (17.5 now), 32 by eight 24.5; a third stage 25.5 (13 us
+// where the rows come from a cache; 2.6 TB/s, A from the L2 as often as x from memory).
 template <int FMT>
 hipError_t down(const AdapterArgs& a, hipStream_t s) {
   if (few_rows(a)) adapter_down_kernel<FMT, 1, 1, 8><<<tiles(a, 16) * (a.rank / 16), 512, 0, s>>>(a);
@@ -512,7 +512,7 @@ hipError_t few(const AdapterArgs& a, hipStream_t s) {
 }
 
 // Columns of a workgroup: 512 (128 a wave) of single tokens, 256 of many rows (17776 rows to 5760, rank 32, in
-// 128, 256, 512 and 1024: both kernels 92, 92, 100 and 103 us; 77 of it this one, 5.3 TB/s).
+// 128, 256, 512 and 1024: both kernels 92, 92, 100 and 103 us; 74 of it this one, 5.5 TB/s).
 template <int R>
 hipError_t up(const AdapterArgs& a, hipStream_t s) {
   if (few_rows(a)) adapter_up_kernel<R, false><<<tiles(a, 16) * ((a.N + 511) / 512), 256, 0, s>>>(a, 512);
