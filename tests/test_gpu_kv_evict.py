@@ -75,6 +75,22 @@ def test_weights_against_64_bits(ctx, lens, qs, hq, hk, D, ps, had, causal):
     assert np.abs(glse - lse)[seen].max(initial=0) < 2.0 ** -14
 
 
+@pytest.mark.parametrize("seqs,hq,hk,D,most", [(3, 8, 8, 64, 1024), (40, 8, 8, 64, 90), (2, 4, 1, 128, 1025), (30, 32, 8, 128, 1000), (40, 16, 8, 32, 1024)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_weights_of_single_tokens(ctx, seqs, hq, hk, D, most, causal):
+    """About the sizes where single tokens have one kernel or two: keys, and pairs of sequence and key head."""
+    rng = np.random.default_rng(seqs + most)
+    lens = [most, 0] + list(rng.integers(1, 60, seqs - 2))
+    p, rng = _random(seqs + D, lens, [1] * seqs, hq, hk, D, 16, 32)
+    sums = rng.random((p["arr"]["k_codes"].shape[:3])).astype(np.float32)
+    want, room, lse = S.weigh_want(p, sums, causal)
+    got, glse = _weigh(ctx, p, sums, causal)
+    _near(got, want, room)
+    seen = np.isfinite(lse)
+    assert np.array_equal(np.isneginf(glse), np.isneginf(lse))
+    assert np.abs(glse - lse)[seen].max(initial=0) < 2.0 ** -14
+
+
 @pytest.mark.parametrize("rope", ["half", "pairs"])
 def test_weights_of_rotated_queries(ctx, rope):
     p, rng = _random(3, [150, 33], [20, 1], 4, 2, 64, 16, 32)

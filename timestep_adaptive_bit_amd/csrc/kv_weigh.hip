@@ -13,7 +13,7 @@
 // lane has one key and adds up rows in registers; the accumulator starts at -L, so what leaves the
 // matrix core goes into the exponential as it is.
 //
-// Up to eight rows a key head (single tokens), two kernels: the first prepares the rows by itself,
+// Up to eight rows a key head (single tokens), two kernels (one for few short sequences, `held`): the first prepares the rows by itself,
 // forms the scores with a lane a key, keeps each row's largest score and sum, and leaves the scores in the
 // workspace (16 or 32 bytes a key; reading the keys again would be 68 at 128 elements); the second adds up
 // their exponentials.
@@ -37,6 +37,7 @@ constexpr int TERMS = 5, STEP = TERMS * 1536 + 512;      // bytes of one 64-elem
 constexpr int NUM_CUS = 256;
 constexpr int kMaxSplits = 64;
 constexpr int kKeys = 256;       // of a workgroup of the last pass
+constexpr int kHeld = 1024;      // whose scores stay in LDS
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -634,10 +635,13 @@ __device__ __forceinline__ void few_range(const KvAttnArgs& a, int splits, int l
 // tiles on their way to its own LDS while it works on a third (64 rows of up to 8192 keys, 8 key heads of 128:
 // 54 us, 4.2 TB/s with the scores that go out).  Level or slower: a third tile on its way, heads as the fastest
 // index, four rows held twice so that each half of a wave weighs half of a tile's keys (59 us).
-template <int NB, int R>
-__global__ void __launch_bounds__(256)
-kv_weigh_scores_kernel(KvAttnArgs a, FewPlan p) {
-  constexpr int NS = (NB + 1) / 2, NW = 4, STAGES = 3;
+// HELD: at most kHeld keys, whose scores stay in LDS and whose weights this kernel adds up, too.
+template <int NB, int R, bool HELD>
+__global__ void __launch_bounds__(HELD ? 512 : 256)
+kv_weigh_scores_kernel(KvAttnArgs a, FewPlan p, float* sums) {
+  constexpr int NS = (NB + 1) / 2, NW = HELD ? 8 : 4, STAGES = 3;
+  __shared__ __attribute__((aligned(16))) float held_scores[HELD ? kHeld * R : 1];
+  __shared__ float minus_l[8];
   __shared__ __attribute__((aligned(16))) uint32_t terms[TERMS][NB][8][6];
   __shared__ uint2 term_scales[NB][8];
   __shared__ float2 part[NW][8];
@@ -655,7 +659,11 @@ kv_weigh_scores_kernel(KvAttnArgs a, FewPlan p) {
   int t0, t1;
   few_range(a, p.splits, len, sp, t0, t1);
   if (t0 >= t1 || a.cache.num_pages == 0) {
-    if (threadIdx.x < 8) stats[threadIdx.x] = make_float2(kLowest, 0.0f);
+    if constexpr (HELD) {
+      if (a.lse != nullptr && (int)threadIdx.x < rows) write_lse(a, q0, hk, threadIdx.x, 0.0f, 0.0f);
+    } else if (threadIdx.x < 8) {
+      stats[threadIdx.x] = make_float2(kLowest, 0.0f);
+    }
     return;
   }
   const int per = (t1 - t0 + NW - 1) / NW;
@@ -687,7 +695,7 @@ kv_weigh_scores_kernel(KvAttnArgs a, FewPlan p) {
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) bring(w0 + i);
   // the rows, a lane a block of one, through LDS to the operand's lanes
-  for (int i = threadIdx.x; i < 8 * NB; i += 256) {
+  for (int i = threadIdx.x; i < 8 * NB; i += NW * 64) {
     const int row = i & 7, blk = i >> 3;
     float x[32];
     bool ok = true;
@@ -718,6 +726,20 @@ kv_weigh_scores_kernel(KvAttnArgs a, FewPlan p) {
         const uint32_t* w = terms[t][blk][key];
         q.q[ds][t] = v8i{(int)w[0], (int)w[1], (int)w[2], (int)w[3], (int)w[4], (int)w[5], 0, 0};
       }
+    }
+  }
+
+  // (of its own keys a thread has place and sum on their way)
+  constexpr int OWN = HELD ? kHeld / (NW * 64) : 1;
+  long long place[OWN];
+  float before[OWN];
+  if constexpr (HELD) {
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+      const int j = i * NW * 64 + (int)threadIdx.x;
+      const bool there = key_row(a, key_page(a, table, j, len), hk, j, place[i]);
+      before[i] = there && !(a.causal && j >= len - all) ? sums[place[i]] : 0.0f;
+      if (!there) place[i] = -1;
     }
   }
 
@@ -753,7 +775,11 @@ kv_weigh_scores_kernel(KvAttnArgs a, FewPlan p) {
       const int first = a.causal ? min(max(j - old, 0), 8) * a.group : 0;
 #pragma unroll
       for (int r = 0; r < 4; ++r) s[kb][r] = (key & 15) < there[kb] && 4 * half + r >= first ? x[r] : kNegInf;
-      if (4 * half < R) *reinterpret_cast<v4f*>(scores + (long long)j * R + 4 * half) = v4f{s[kb][0], s[kb][1], s[kb][2], s[kb][3]};
+      if (4 * half < R) {
+        const v4f w = {s[kb][0], s[kb][1], s[kb][2], s[kb][3]};
+        if constexpr (HELD) *reinterpret_cast<v4f*>(held_scores + j * R + 4 * half) = w;
+        else *reinterpret_cast<v4f*>(scores + (long long)j * R + 4 * half) = w;
+      }
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -780,7 +806,26 @@ kv_weigh_scores_kernel(KvAttnArgs a, FewPlan p) {
     for (int w = 0; w < NW; ++w) top = fmaxf(top, part[w][threadIdx.x].x);
 #pragma unroll
     for (int w = 0; w < NW; ++w) total += part[w][threadIdx.x].y * exp2_fast(part[w][threadIdx.x].x - top);
-    stats[threadIdx.x] = make_float2(top, total);
+    if constexpr (HELD) {
+      const float l = top + __builtin_log2f(total);
+      minus_l[threadIdx.x] = (int)threadIdx.x < rows && counts(total, l) ? -l : kNegInf;
+      if (a.lse != nullptr && (int)threadIdx.x < rows) write_lse(a, q0, hk, threadIdx.x, total, l);
+    } else {
+      stats[threadIdx.x] = make_float2(top, total);
+    }
+  }
+  if constexpr (HELD) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kHeld / (NW * 64); ++i) {
+      const int j = i * NW * 64 + (int)threadIdx.x;
+      if (place[i] < 0) continue;
+      float w = 0.0f;
+#pragma unroll
+      for (int r = 0; r < R; ++r)                // (as below)
+        w += minus_l[r] == kNegInf ? 0.0f : exp2_fast(held_scores[j * R + r] + minus_l[r]);
+      sums[place[i]] = before[i] + w;
+    }
   }
 }
 
@@ -869,12 +914,21 @@ size_t few_plan_of(int seqs, int kv_heads, int rows, int max_kv, uint8_t* ws, Fe
   return scores + heads * (size_t)p.splits * 64;
 }
 
+// One kernel for short sequences while each (sequence, key head) has a CU to itself (8 waves and 120 KB of LDS).
+// Measured under a graph, two kernels and one, 8 key heads of 128: one row x 1000 keys 12.4 and 10.5 us, x 200 10.5
+// and 8.6, 16 of 700 (64 elements, 16 heads) 14.5 and 10.1; 64 rows x 1000 18.7 and 19.7, 256 x 500 40 and 60.
+bool held(const KvAttnArgs& a) { return a.max_kv <= kHeld && (long long)a.seqs * a.cache.heads <= NUM_CUS; }
+
 template <int NB, int R>
 hipError_t launch_few(const KvAttnArgs& a, float* sums, hipStream_t s) {
+  const unsigned heads = (unsigned)a.cache.heads;
+  if (held(a)) {
+    kv_weigh_scores_kernel<NB, R, true><<<dim3((unsigned)a.seqs, heads), 512, 0, s>>>(a, FewPlan{0, nullptr, nullptr, 1}, sums);
+    return hipGetLastError();
+  }
   FewPlan p;
   few_plan_of(a.seqs, a.cache.heads, R, a.max_kv, reinterpret_cast<uint8_t*>(a.part), p);
-  const unsigned heads = (unsigned)a.cache.heads;
-  kv_weigh_scores_kernel<NB, R><<<dim3((unsigned)(p.splits * a.seqs), heads), 256, 0, s>>>(a, p);
+  kv_weigh_scores_kernel<NB, R, false><<<dim3((unsigned)(p.splits * a.seqs), heads), 256, 0, s>>>(a, p, sums);
   if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   const unsigned chunks = max((unsigned)((a.max_kv + 1023ll) / 1024), 1u);
   kv_weigh_add_kernel<R><<<dim3(chunks * a.seqs, heads), 256, 0, s>>>(a, p, sums, chunks);
