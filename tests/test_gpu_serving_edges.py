@@ -1,0 +1,77 @@
+"""Operators for serving many requests where the ordinary problems do not reach."""
+import numpy as np
+import pytest
+import torch
+
+from tests import attention_check as A
+from tests import serve_check as S
+import timestep_adaptive_bit_amd as T
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    c = T.Context()
+    yield c
+    c.close()
+
+
+# ------------------------------------------------------------------ trees
+def _tree(ctx, p, see):
+    words = max((int(np.diff(p["cu"]).max()) + 63) // 64, 1)
+    mask = np.concatenate([S.packed(m, words) for m in see])
+    q = S.dev(p["q"]).bfloat16()
+    lse = torch.full(q.shape[:2], 7.0, device=DEV)
+    out = ctx.kv_tree_attention(S.cache_of(p), q, S.dev(mask), S.dev(np.asarray(p["cu"], np.int32)), S.dev(p["table"]),
+                                S.dev(np.asarray(p["lens"], np.int32)), int(np.diff(p["cu"]).max()), max(p["lens"]),
+                                scale=p["scale"], lse=lse)
+    return out.double().cpu().numpy(), lse.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("rows,n", [(8, 30), (16, 200), (30, 60), (32, 300), (40, 60), (150, 400), (700, 800)])
+@pytest.mark.parametrize("D", [64, 96, 128])
+def test_far_values_of_other_branches(ctx, rows, n, D):
+    """Two branches whose nodes lie among each other: a far value of one leaves the other's rows their bits,
+    whether those see far values of their own or not."""
+    print("tree", rows, n, D, flush=True)
+    rng = np.random.default_rng(rows + D)
+    branch = rng.integers(0, 2, rows)
+    branch[:2] = 0, 1
+    see = (branch[:, None] == branch[None]) & np.tril(np.ones((rows, rows), bool))
+    p = A.steep_problem(rows, n, rows, 2, D, 32, lambda _, shape: np.full(shape, 127))
+    scales = p["arr"]["v_scales"]
+
+    def far(nodes, b):
+        j = n - rows + np.asarray(nodes)
+        scales[p["table"][0, j // 16], :, j % 16, 1] = b
+
+    ones, zeros = np.flatnonzero(branch == 1), np.flatnonzero(branch == 0)
+    for own, others in ((0, 240), (0, 20), (240, 20), (20, 240), (240, 240)):
+        scales[...] = 127
+        if own:
+            far(rng.permutation(ones)[:max(len(ones) // 30, 1)], own)
+        clean = _tree(ctx, p, [see])
+        far(rng.permutation(zeros)[:max(len(zeros) // 20, 1)], others)
+        got = _tree(ctx, p, [see])
+        A.check(*got, S.tree_want(p, [see]))
+        assert np.array_equal(got[0][ones], clean[0][ones]) and np.array_equal(got[1][ones], clean[1][ones]), (own, others)
+
+
+@pytest.mark.parametrize("rows", [8, 30, 150])
+@pytest.mark.parametrize("byte", [253, 255])
+def test_values_that_are_no_number_in_other_branches(ctx, rows, byte):
+    """A node whose value is none makes NaN of the rows that see it and leaves the others their bits."""
+    p = A.problem(rows, [300], [rows], 2, 2, 128, 16, 32)
+    rng = np.random.default_rng(rows)
+    branch = rng.integers(0, 2, rows)
+    see = (branch[:, None] == branch[None]) & np.tril(np.ones((rows, rows), bool))
+    clean = _tree(ctx, p, [see])
+    node = rows // 2
+    j = 300 - rows + node
+    p["arr"]["v_scales"][p["table"][0][j // 16], :, j % 16, 2] = byte
+    got = _tree(ctx, p, [see])
+    touched = see[:, node]
+    assert np.isnan(got[0][touched]).all() and touched.any() and not touched.all()
+    assert np.array_equal(got[0][~touched], clean[0][~touched]) and np.array_equal(got[1][~touched], clean[1][~touched])

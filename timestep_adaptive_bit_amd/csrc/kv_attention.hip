@@ -76,12 +76,13 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 
 __device__ __forceinline__ bool far_scale(uint32_t s) { return s - kFarLow > kFarHigh - kFarLow; }
 
-// Lowest of 16 keys that has one of a wave's bits (lane % 16: the key).
-__device__ __forceinline__ int lowest_key(unsigned long long m) {
+// Which of 16 keys have one of a wave's bits (lane % 16: the key), and the lowest of them.
+__device__ __forceinline__ uint32_t keys_of(unsigned long long m) {
   m |= m >> 32;
   m |= m >> 16;
-  return __builtin_ctz((unsigned)m & 0xFFFFu);
+  return (uint32_t)m & 0xFFFFu;
 }
+__device__ __forceinline__ int lowest_key(unsigned long long m) { return __builtin_ctz(keys_of(m)); }
 
 // What a part (reference, sum of weights) of a row is taken relative to when parts are joined: the
 // exponent of its sum, so that every part's sum of weights becomes less than one.  A part
@@ -388,8 +389,10 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
       }
     }
     // a value scale beyond bf16 (or NaN): the key's scores become NaN, its values zero; one far from
-    // one: the rows that see the first such key of the tile keep their reference near their scores
+    // one: the rows that see the first such key of the tile (of a tree, any such key) keep their reference
+    // near their scores
     int far_from = kNever, high_from = kNever;
+    uint64_t far_keys = 0, high_keys = 0;            // (of a tree)
     if (__any(has && max(max(vs[0] - kFarLow, vs[1] - kFarLow), max(vs[2] - kFarLow, vs[3] - kFarLow)) > kFarHigh - kFarLow)) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -401,8 +404,13 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
         }
         const unsigned long long far = __ballot(has && far_scale(vs[k]));
         const unsigned long long high = __ballot(has && vs[k] > kFarHigh);
-        if (far != 0) far_from = min(far_from, j0 + 16 * k + lowest_key(far));
-        if (high != 0) high_from = min(high_from, j0 + 16 * k + lowest_key(high));
+        if constexpr (TREE) {
+          far_keys |= (uint64_t)keys_of(far) << (16 * k);
+          high_keys |= (uint64_t)keys_of(high) << (16 * k);
+        } else {
+          if (far != 0) far_from = min(far_from, j0 + 16 * k + lowest_key(far));
+          if (high != 0) high_from = min(high_from, j0 + 16 * k + lowest_key(high));
+        }
       }
     }
 #pragma unroll
@@ -433,12 +441,13 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
     float sum;
     uint32_t p[8];
     bool over = false;
+    const bool any_far = TREE ? far_keys != 0 : far_from != kNever;
     if (any_ref) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) s[k] -= ref;
     }
     for (int pass = 0; pass < 2; ++pass) {
-      if (pass == 1 || far_from != kNever || (any_fresh && __any(fresh && j0 < seen))) {
+      if (pass == 1 || any_far || (any_fresh && __any(fresh && j0 < seen))) {
         float top = kNegInf;
         asm volatile("" : "+v"(top));                // (else the compiler takes the maximum of every tile)
 #pragma unroll
@@ -452,12 +461,18 @@ kv_attention_rows16_kernel(KvAttnArgs a) {
         any_fresh = __any(fresh);
         const bool up = first ? fabsf(top) > 40.0f : over && top > 0.0f;
         float by = up ? top : 0.0f;
-        if (pass == 0 && far_from != kNever) {
-          float all = l + __shfl_xor(l, 16, 64);
-          all += __shfl_xor(all, 32, 64);
-          const float m = fmaxf(top, __builtin_amdgcn_logf(all));
-          far_room = seen > high_from ? kFarRoom : far_room;
-          if (seen > far_from && m > kNegInf) by = m + far_room;
+        if (pass == 0 && any_far) {
+          float so_far = l + __shfl_xor(l, 16, 64);
+          so_far += __shfl_xor(so_far, 32, 64);
+          const float m = fmaxf(top, __builtin_amdgcn_logf(so_far));
+          bool sees_far = seen > far_from, sees_high = seen > high_from;
+          if constexpr (TREE) {
+            const uint64_t nodes = nodes_from(seen_nodes, a.mask_words, j0 - (len - all));
+            sees_far = (nodes & far_keys) != 0;
+            sees_high = (nodes & high_keys) != 0;
+          }
+          far_room = sees_high ? kFarRoom : far_room;
+          if (sees_far && m > kNegInf) by = m + far_room;
         }
         ref += by;
         any_ref = __any(ref != 0.0f);
@@ -651,6 +666,9 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   // Like the stage's marks written before the barrier that hands a tile over and read in that tile
   // alone, so neither depends on timing.
   __shared__ int2 far_at[2];
+  // Of a tree, whose rows see keys by their bits: by stage and wave the last tile that has such keys, which
+  // of the wave's 16 they are, and in the upper half those far above.
+  __shared__ int2 far_in[TREE ? 2 : 1][NW];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = lane & 31, half = lane >> 5;
@@ -803,8 +821,12 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
     const int key = (int)((unsigned)t * TILE) + wave * KPW;
     if (has_k && ((far >> lkey) & 0x0001000100010001ull) != 0)
       st[(t - t0) & 1].ks[kblk & 1][skey & 31][4 + (skey >> 5) * 2 + (kblk >> 1)] = 1;
-    if (far != 0 && lane == 0) atomicMin(&far_at[(t - t0) & 1].x, key + lowest_key(far));
-    if (high != 0 && lane == 0) atomicMin(&far_at[(t - t0) & 1].y, key + lowest_key(high));
+    if constexpr (TREE) {
+      if (far != 0 && lane == 0) far_in[(t - t0) & 1][wave] = make_int2(t, (int)(keys_of(far) | keys_of(high) << 16));
+    } else {
+      if (far != 0 && lane == 0) atomicMin(&far_at[(t - t0) & 1].x, key + lowest_key(far));
+      if (high != 0 && lane == 0) atomicMin(&far_at[(t - t0) & 1].y, key + lowest_key(high));
+    }
   };
   auto store_keys = [&](Stage& s) {
     if (has_k) {
@@ -858,6 +880,7 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   float alpha = 1.0f;
   bool any_fresh = true, any_ref = false, any_alpha = false;     // over the wave
   float far_room = 0.0f;
+  uint32_t far_seen = 0u;        // of a tree: the stages in which the row has seen a far value scale
   auto raise = [&](v16f (&sc)[2], bool over, bool far, float least) {
     float top = kNegInf;
     asm volatile("" : "+v"(top));    // (else the compiler takes the maximum of every tile)
@@ -927,6 +950,7 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
   if (tid < 2 * 64)              // scale bytes of blocks that do not exist: any finite scale; no marks
     reinterpret_cast<uint2*>(st[tid / 64].ks)[tid % 64] = make_uint2(0x7F7F7F7Fu, 0u);
   if (tid < 2) far_at[tid] = make_int2(kNever, kNever);
+  if (TREE && tid < 2 * NW) (&far_in[0][0])[tid] = make_int2(-1, 0);
   __syncthreads();
   settle(t0);
   store(st[0]);
@@ -968,12 +992,28 @@ kv_attention_rows128_kernel(KvAttnArgs a) {
           float least = kNegInf;         // the logarithm of what a row has summed
           bool far = false;
           if (pass == 0 && any_far) {
-            const int2 from = far_at[(t - t0) & 1];
-            if (seen > from.y) far_room = kFarRoom;
+            if constexpr (TREE) {
+              // (what a row has seen is noted by stage, as the marks that bring it here are)
+              const uint64_t nodes = nodes_from(seen_nodes, a.mask_words, j0 - (len - all));
+              uint64_t far_keys = 0, high_keys = 0;
+#pragma unroll
+              for (int w = 0; w < NW; ++w) {
+                const int2 in = far_in[(t - t0) & 1][w];
+                const uint32_t keys = in.x == t ? (uint32_t)in.y : 0u;
+                far_keys |= (uint64_t)(keys & 0xFFFFu) << (KPW * w);
+                high_keys |= (uint64_t)(keys >> 16) << (KPW * w);
+              }
+              if ((nodes & high_keys) != 0) far_room = kFarRoom;
+              if ((nodes & far_keys) != 0) far_seen |= 1u << ((t - t0) & 1);
+              far = (far_seen >> ((t - t0) & 1) & 1u) != 0u;
+            } else {
+              const int2 from = far_at[(t - t0) & 1];
+              if (seen > from.y) far_room = kFarRoom;
+              far = seen > from.x;
+            }
             float tl, th;
             halves(l, tl, th);
             least = __builtin_amdgcn_logf(tl + th);
-            far = seen > from.x;
           }
           raise(sc, over, far, least);
         }
