@@ -693,7 +693,8 @@ size_t tabit_kv_weigh_workspace_bytes(int num_tokens, int num_q_heads, int num_k
  *                most 2^30
  *   keep         device int32 [num_seqs][num_kv_heads][budget] output: the kept tokens'
  *                indexes in their order, then -1
- *   new_lens     device int32 [num_seqs] output: min(kv_len, budget)
+ *   new_lens     device int32 [num_seqs] output: min(kv_len, budget).  keep and new_lens may not
+ *                overlap each other, kv_lens, block_table or sums
  *   ws           device workspace of tabit_kv_evict_workspace_bytes bytes, 16-byte aligned (NULL
  *                when that is 0)
  * sinks + recent at most budget, which is 1 to 2^30.

@@ -38,6 +38,12 @@ bool valid_sizes(int num_tokens, int num_q_heads, int num_kv_heads, int head_dim
          max_kv > 0 && num_q_heads % num_kv_heads == 0;
 }
 
+// Whether n bytes at p and m at q share one.
+bool meet(const void* p, uint64_t n, const void* q, uint64_t m) {
+  const uint64_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return n > 0 && m > 0 && (a < b ? b - a < n : a - b < m);
+}
+
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
@@ -158,6 +164,15 @@ int tabit_kv_evict(tabit_ctx* ctx, const tabit_kv_cache* cache, const float* sum
   if (num_seqs == 0) return TABIT_OK;
   if ((st = check_ws(ctx, ws, ws_bytes, tabit_kv_evict_workspace_bytes(num_seqs, k.cache.heads, max_kv))) != TABIT_OK)
     return st;
+  // (other workgroups still read the lengths, tables and sums when one writes its outputs)
+  const uint64_t seqs = (uint64_t)num_seqs, heads = (uint64_t)k.cache.heads;
+  const struct { const void* p; uint64_t n; } in[] = {{kv_lens, seqs * 4}, {block_table, seqs * (uint64_t)table_stride * 4},
+                                                      {sums, ((uint64_t)k.cache.num_pages * heads << k.cache.page_shift) * 4}},
+                                              out[] = {{new_lens, seqs * 4}, {keep, seqs * heads * (uint64_t)budget * 4}};
+  bool met = meet(out[0].p, out[0].n, out[1].p, out[1].n);
+  for (const auto& o : out)
+    for (const auto& i : in) met = met || meet(o.p, o.n, i.p, i.n);
+  if (met) return fail(ctx, TABIT_EINVAL, "keep and new_lens may not overlap each other or what the call reads");
   k.ws = static_cast<uint8_t*>(ws);
   k.sums = sums;
   k.table = block_table;
