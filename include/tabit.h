@@ -746,7 +746,8 @@ size_t tabit_kv_compact_workspace_bytes(int num_seqs, int num_kv_heads, int head
  *               [cu_rows[i], cu_rows[i+1]); rows of no segment are left as they are in out
  *   adapter     device int32 [num_segments]; outside [0, num_adapters): out = y
  *   y, out      device bf16, row t at t * y_stride and t * out_stride elements (multiples
- *               of 8, at least N); out may be y (then with its stride) or not overlap it
+ *               of 8, at least N); out may be y (then with its stride) or not overlap it, and
+ *               may not overlap x (columns of one wider matrix do not overlap)
  *   ws          of tabit_adapter_workspace_bytes bytes, 16-byte aligned
  * K and N multiples of 32, at most 32768; 1 <= num_adapters * rank; matrices 16-byte aligned.
  */

@@ -47,3 +47,28 @@ def test_lists_over_what_is_read(lib, ctx, kw):
     """Other workgroups still read lengths, tables and sums when one writes its list or length."""
     assert _evict(lib, ctx, **kw) == T.EINVAL
     assert "overlap" in ctx.last_error()
+
+
+def _adapter(lib, ctx, **kw):
+    a = dict(x=_at(0), x_scale=_at(1), x_fmt=T.FMT_BF16, rows=100, K=64, N=96, x_stride=64, a=_at(2), b=_at(3), scale=None,
+             num_adapters=2, rank=16, cu_rows=_at(4), adapter=_at(5), num_segments=2, y=_at(6), y_stride=96, out=_at(7),
+             out_stride=96, ws=_at(8), ws_bytes=1 << 20)
+    a.update(kw)
+    s = L._AdapterArgs(*[a[n] for n, _ in L._AdapterArgs._fields_])
+    return lib.tabit_adapter_linear(ctx.handle, ctypes.addressof(s), None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=_at(0)), dict(out=_at(0) + 64 * 2 * 100 - 16), dict(out=_at(0) - 96 * 2 * 100 + 16),
+    dict(out=_at(0), x_fmt=T.FMT_INT8), dict(out=_at(0) + 64 * 100 - 16, x_fmt=T.FMT_INT8),
+    dict(out=_at(0) + 32 * 100 - 16, x_fmt=T.FMT_MXFP4),
+    dict(out=_at(6) + 16), dict(out=_at(6) - 16), dict(out=_at(6) + 192 * 99), dict(out=_at(6) - 192 * 100 + 16),
+    dict(out=_at(0) + 112, x_stride=160, out_stride=160), dict(out=_at(0) - 176, x_stride=160, out_stride=160),
+    dict(out=_at(0) + 320 * 99 + 112, x_stride=160, out_stride=160), dict(out=_at(0) - 320 * 99 - 176, x_stride=160, out_stride=160),
+    dict(out=_at(6) + 176, y_stride=192, out_stride=192), dict(out=_at(6) - 176, y_stride=192, out_stride=192),
+    dict(out=_at(0) + 128, x_stride=160, out_stride=168),
+])
+def test_products_over_what_is_read(lib, ctx, kw):
+    """Other workgroups still read a row of x, or of y, when one writes its part of out."""
+    assert _adapter(lib, ctx, **kw) == T.EINVAL
+    assert "overlap" in ctx.last_error()

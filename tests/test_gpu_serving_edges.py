@@ -75,3 +75,26 @@ def test_values_that_are_no_number_in_other_branches(ctx, rows, byte):
     touched = see[:, node]
     assert np.isnan(got[0][touched]).all() and touched.any() and not touched.all()
     assert np.array_equal(got[0][~touched], clean[0][~touched]) and np.array_equal(got[1][~touched], clean[1][~touched])
+
+
+# ------------------------------------------------------------------ adapters
+def _bf(rng, *shape, scale=1.0):
+    return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).bfloat16().to(DEV)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 200])
+def test_columns_of_one_matrix(ctx, rows):
+    """x, y and out beside each other in one matrix: the bits of separate ones, and nothing else is written."""
+    rng = np.random.default_rng(rows)
+    K, N = 64, 96
+    whole = _bf(rng, rows, 8 + N + K + N)
+    x, y = whole[:, 8 + N:8 + N + K], whole[:, 8 + N + K:]
+    bank = T.Adapters(_bf(rng, 2, 16, K, scale=0.1), _bf(rng, 2, N, 16))
+    cu, which = S.dev(np.array([0, rows // 2, rows], np.int32)), S.dev(np.array([1, 0], np.int32))
+    want = ctx.adapter_linear(bank, x.contiguous(), y.contiguous(), cu, which)
+    before = whole.clone()
+    ctx.adapter_linear(bank, x, y, cu, which, out=whole[:, 8:8 + N])
+    assert torch.equal(whole[:, 8:8 + N], want)
+    assert torch.equal(whole[:, :8], before[:, :8]) and torch.equal(whole[:, 8 + N:], before[:, 8 + N:])
+    with pytest.raises(T.TabitError):
+        ctx.adapter_linear(bank, x, y, cu, which, out=whole[:, 16:16 + N])

@@ -4,6 +4,8 @@
 // caller's stream; no device memory is allocated here.
 #include "api_cache.h"
 
+#include <cstdlib>
+
 namespace {
 
 constexpr int kMaxNodes = 8192;      // of a tree
@@ -42,6 +44,25 @@ bool valid_sizes(int num_tokens, int num_q_heads, int num_kv_heads, int head_dim
 bool meet(const void* p, uint64_t n, const void* q, uint64_t m) {
   const uint64_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
   return n > 0 && m > 0 && (a < b ? b - a < n : a - b < m);
+}
+
+// Whether `rows` rows of n bytes, `step` bytes (n at least) apart from p on, share a byte with as many of m bytes
+// from q on.  Columns of one wider matrix do not.
+bool rows_meet(const void* p, int64_t n, int64_t step, const void* q, int64_t m, int64_t q_step, int rows) {
+  if (rows == 1) return meet(p, (uint64_t)n, q, (uint64_t)m);
+  const int64_t a = (int64_t)reinterpret_cast<uintptr_t>(p), b = (int64_t)reinterpret_cast<uintptr_t>(q);
+  if (a + (rows - 1) * step + n <= b || b + (rows - 1) * q_step + m <= a) return false;
+  if (step == q_step) {          // row i + k of p and row i of q are b - a - k step apart
+    const int64_t d = b - a, k = d >= 0 ? d / step : -((-d + step - 1) / step), r = d - k * step;      // 0 <= r < step
+    return (r < n && std::abs(k) < rows) || (step - r < m && std::abs(k + 1) < rows);
+  }
+  for (int64_t i = 0, j = 0; i < rows && j < rows;) {
+    const int64_t x = a + i * step, y = b + j * q_step;
+    if (x + n <= y) ++i;
+    else if (y + m <= x) ++j;
+    else return true;
+  }
+  return false;
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -262,6 +283,12 @@ int tabit_adapter_linear(tabit_ctx* ctx, const tabit_adapter_args* a, void* stre
   const size_t need = tabit_adapter_workspace_bytes(a->rows, a->rank, a->num_segments);
   const int st = check_ws(ctx, a->ws, a->ws_bytes, need);
   if (st != TABIT_OK) return st;
+  // (workgroups of other columns still read a row of x when one writes its part of out)
+  const int64_t x_row = a->x_fmt == TABIT_FMT_BF16 ? 2ll * a->K : a->x_fmt == TABIT_FMT_INT8 ? a->K : a->K / 2;
+  if (rows_meet(a->out, 2ll * a->N, 2 * a->out_stride, a->x, x_row, a->x_fmt == TABIT_FMT_BF16 ? 2 * a->x_stride : x_row, a->rows))
+    return fail(ctx, TABIT_EINVAL, "out may not overlap x");
+  if (a->out != a->y && rows_meet(a->out, 2ll * a->N, 2 * a->out_stride, a->y, 2ll * a->N, 2 * a->y_stride, a->rows))
+    return fail(ctx, TABIT_EINVAL, "out may be y or not overlap it");
   tabit::AdapterArgs k{};
   k.x = a->x;
   k.x_scale = a->x_scale;
