@@ -667,7 +667,7 @@ int tabit_tree_mask(tabit_ctx* ctx, const int32_t* parents, int num_tokens, cons
  * with rows, masks and lengths as tabit_kv_attention.  With args->causal the last n tokens
  * of a sequence (the queries' own) are set, not added to: a token's sum starts with the call
  * that has its query.  Without, clear the sums of tokens when they are appended.
- *   args    as tabit_kv_attention; out is not used and must be NULL; lse may be NULL, or
+ *   args    as tabit_kv_attention, max_kv at most 2^30; out is not used and must be NULL; lse may be NULL, or
  *           receives the logarithm of each row's sum of exp(score), here of exact weights
  *   sums    device fp32 [num_pages][num_kv_heads][page_size], 16-byte aligned
  *   ws      of tabit_kv_weigh_workspace_bytes bytes, 16-byte aligned

@@ -72,3 +72,29 @@ def test_products_over_what_is_read(lib, ctx, kw):
     """Other workgroups still read a row of x, or of y, when one writes its part of out."""
     assert _adapter(lib, ctx, **kw) == T.EINVAL
     assert "overlap" in ctx.last_error()
+
+
+def _weigh(lib, ctx, max_kv, heads=1, max_q=1):
+    a = dict(q=_at(0), q_stride=1024, num_tokens=16, num_q_heads=heads, cu_q=_at(1), num_seqs=1, max_q=max_q, block_table=_at(2),
+             table_stride=1 << 27, kv_lens=_at(3), max_kv=max_kv, scale=0.125, causal=1, rope=None, positions=None, out=None,
+             lse=None, ws=_at(4), ws_bytes=1 << 62)
+    args = L._KvAttentionArgs(*[a[n] for n, _ in L._KvAttentionArgs._fields_])
+    c = L._KvCache(_at(10), _at(11), _at(12), _at(13), 4, 16, 1, 64, 32)
+    return lib.tabit_kv_weigh(ctx.handle, ctypes.addressof(c), ctypes.addressof(args), _at(5), None)
+
+
+@pytest.mark.parametrize("max_kv", [(1 << 30) + 1, (1 << 31) - 300, (1 << 31) - 1])
+@pytest.mark.parametrize("heads,max_q", [(1, 1), (8, 1), (16, 1), (4, 16)])
+def test_weights_of_too_many_keys(lib, ctx, max_kv, heads, max_q):
+    """Places of keys are whole numbers of 32 bits that the kernels step by hundreds past the last one."""
+    assert _weigh(lib, ctx, max_kv, heads, max_q) == T.ESHAPE
+    assert "max_kv" in ctx.last_error()
+    assert lib.tabit_kv_weigh_workspace_bytes(16, heads, 1, 64, 1, max_q, max_kv) == 0
+
+
+@pytest.mark.parametrize("heads,max_q", [(1, 1), (8, 1), (16, 1), (4, 16)])
+def test_workspace_of_the_most_keys(lib, heads, max_q):
+    """Scores of 4 or 8 rows a key; of more rows the tiles' terms and sums of up to 16 ranges."""
+    n = lib.tabit_kv_weigh_workspace_bytes(16, heads, 1, 64, 1, max_q, 1 << 30)
+    rows = heads * max_q
+    assert (1 << 30) * (16 if rows <= 4 else 32) <= n < 1 << 36 if rows <= 8 else 0 < n < 1 << 37

@@ -9,6 +9,7 @@
 namespace {
 
 constexpr int kMaxNodes = 8192;      // of a tree
+constexpr int kMaxKeys = 1 << 30;    // of a sequence: kernels step past the last one by less than as many again
 
 // Sizes that an attention-like launch takes.
 int check_grid(tabit_ctx* ctx, const tabit_kv_attention_args* a, int splits) {
@@ -126,6 +127,7 @@ int tabit_tree_mask(tabit_ctx* ctx, const int32_t* parents, int num_tokens, cons
 
 size_t tabit_kv_weigh_workspace_bytes(int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
                                       int num_seqs, int max_q, int max_kv) {
+  if (max_kv > kMaxKeys) return 0;
   // (a call without keys may still ask for lse)
   if (!valid_sizes(num_tokens, num_q_heads, num_kv_heads, head_dim, num_seqs, max_q, max_kv == 0 ? 1 : max_kv)) return 0;
   return tabit::kv_weigh_workspace(num_tokens, num_q_heads, num_kv_heads, (head_dim + 31) / 32 * 32, num_seqs,
@@ -142,6 +144,7 @@ int tabit_kv_weigh(tabit_ctx* ctx, const tabit_kv_cache* cache, const tabit_kv_a
   if (a->out != nullptr) return fail(ctx, TABIT_EINVAL, "weights have no attention output: out must be NULL");
   if (sums == nullptr && k.cache.num_pages > 0) return fail(ctx, TABIT_EINVAL, "null sums");
   if (!aligned(sums, 16)) return fail(ctx, TABIT_EALIGN, "sums must be 16-byte aligned");
+  if (a->max_kv > kMaxKeys) return fail(ctx, TABIT_ESHAPE, "max_kv must be in [0, 2^30] (got %d)", a->max_kv);
   if (a->num_tokens == 0 || a->num_seqs == 0 || a->max_q == 0) return TABIT_OK;
   if (a->max_kv == 0 && a->lse == nullptr) return TABIT_OK;
   if ((st = check_grid(ctx, a, 1)) != TABIT_OK) return st;
@@ -170,7 +173,7 @@ int tabit_kv_evict(tabit_ctx* ctx, const tabit_kv_cache* cache, const float* sum
   if (st != TABIT_OK) return st;
   st = check_table(ctx, block_table, table_stride, num_seqs);
   if (st != TABIT_OK) return st;
-  if (max_kv < 0 || max_kv > (1 << 30)) return fail(ctx, TABIT_ESHAPE, "max_kv must be in [0, 2^30] (got %d)", max_kv);
+  if (max_kv < 0 || max_kv > kMaxKeys) return fail(ctx, TABIT_ESHAPE, "max_kv must be in [0, 2^30] (got %d)", max_kv);
   if ((int64_t)table_stride * cache->page_size < max_kv)
     return fail(ctx, TABIT_ESHAPE, "a table row of %d pages of %d tokens does not hold max_kv = %d", table_stride,
                 cache->page_size, max_kv);
