@@ -74,8 +74,8 @@ def test_products_over_what_is_read(lib, ctx, kw):
     assert "overlap" in ctx.last_error()
 
 
-def _weigh(lib, ctx, max_kv, heads=1, max_q=1):
-    a = dict(q=_at(0), q_stride=1024, num_tokens=16, num_q_heads=heads, cu_q=_at(1), num_seqs=1, max_q=max_q, block_table=_at(2),
+def _weigh(lib, ctx, max_kv, heads=1, max_q=1, tokens=16):
+    a = dict(q=_at(0), q_stride=8192, num_tokens=tokens, num_q_heads=heads, cu_q=_at(1), num_seqs=1, max_q=max_q, block_table=_at(2),
              table_stride=1 << 27, kv_lens=_at(3), max_kv=max_kv, scale=0.125, causal=1, rope=None, positions=None, out=None,
              lse=None, ws=_at(4), ws_bytes=1 << 62)
     args = L._KvAttentionArgs(*[a[n] for n, _ in L._KvAttentionArgs._fields_])
@@ -98,3 +98,11 @@ def test_workspace_of_the_most_keys(lib, heads, max_q):
     n = lib.tabit_kv_weigh_workspace_bytes(16, heads, 1, 64, 1, max_q, 1 << 30)
     rows = heads * max_q
     assert (1 << 30) * (16 if rows <= 4 else 32) <= n < 1 << 36 if rows <= 8 else 0 < n < 1 << 37
+
+
+@pytest.mark.parametrize("heads,tokens", [(33, (1 << 31) - 1), (64, (1 << 31) - 1), (64, 1 << 30), (96, (1 << 31) - 64)])
+def test_weights_of_too_many_rows(lib, ctx, heads, tokens):
+    """Tile places of a head are whole numbers of 32 bits."""
+    assert _weigh(lib, ctx, 64, heads, 1, tokens) == T.ESHAPE
+    assert "too many rows" in ctx.last_error()
+    assert lib.tabit_kv_weigh_workspace_bytes(tokens, heads, 1, 64, 1, 1, 64) == 0

@@ -130,8 +130,9 @@ size_t tabit_kv_weigh_workspace_bytes(int num_tokens, int num_q_heads, int num_k
   if (max_kv > kMaxKeys) return 0;
   // (a call without keys may still ask for lse)
   if (!valid_sizes(num_tokens, num_q_heads, num_kv_heads, head_dim, num_seqs, max_q, max_kv == 0 ? 1 : max_kv)) return 0;
-  return tabit::kv_weigh_workspace(num_tokens, num_q_heads, num_kv_heads, (head_dim + 31) / 32 * 32, num_seqs,
-                                   max_q, max_kv);
+  const int dim_pad = (head_dim + 31) / 32 * 32;
+  if (!tabit::kv_weigh_fits(num_tokens, num_q_heads, num_kv_heads, dim_pad, num_seqs, max_q, max_kv)) return 0;
+  return tabit::kv_weigh_workspace(num_tokens, num_q_heads, num_kv_heads, dim_pad, num_seqs, max_q, max_kv);
 }
 
 int tabit_kv_weigh(tabit_ctx* ctx, const tabit_kv_cache* cache, const tabit_kv_attention_args* a, float* sums,

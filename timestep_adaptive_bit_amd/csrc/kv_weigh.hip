@@ -999,6 +999,7 @@ bool kv_weigh_fits(int tokens, int q_heads, int kv_heads, int dim_pad, int seqs,
     few_plan_of(seqs, kv_heads, 8, max_kv, nullptr, p);
     return (long long)p.splits * seqs <= most && ((long long)max_kv / 1024 + 1) * seqs <= most;
   }
+  if ((long long)tokens * (q_heads / kv_heads) / 32 + 1 + seqs > 0x7FFFFFFF) return false;    // tile places of a head
   Plan p;
   plan_of(tokens, q_heads, kv_heads, dim_pad, seqs, max_q, max_kv, nullptr, p);
   return (long long)p.row_tiles * seqs <= most && ((p.row_tiles + 3ll) / 4) * p.splits * pairs <= most &&
