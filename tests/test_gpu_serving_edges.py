@@ -98,3 +98,16 @@ def test_columns_of_one_matrix(ctx, rows):
     assert torch.equal(whole[:, :8], before[:, :8]) and torch.equal(whole[:, 8 + N:], before[:, 8 + N:])
     with pytest.raises(T.TabitError):
         ctx.adapter_linear(bank, x, y, cu, which, out=whole[:, 16:16 + N])
+
+
+def test_masks_of_more_words_than_any_tree_has(ctx):
+    """Rows of more than 2^25 words, whose bits pass 32 bits: the node itself and its parent, then zeros."""
+    words = (1 << 25) + 1
+    mask = torch.full((2, words), -1, dtype=torch.int64, device=DEV)
+    parents, cu = S.dev(np.array([-1, 0], np.int32)), S.dev(np.array([0, 2], np.int32))
+    depth = torch.full((2,), 9, dtype=torch.int32, device=DEV)
+    assert T.load().tabit_tree_mask(ctx.handle, parents.data_ptr(), 2, cu.data_ptr(), 1, 2, mask.data_ptr(), words, depth.data_ptr(),
+                                    torch.cuda.current_stream().cuda_stream) == T.OK
+    torch.cuda.synchronize()
+    assert mask[:, 0].tolist() == [1, 3] and depth.tolist() == [0, 1]
+    assert not mask[:, 1:].any()

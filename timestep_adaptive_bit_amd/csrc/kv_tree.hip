@@ -25,7 +25,7 @@ tree_mask_kernel(const int* parents, int tokens, const int* cu_q, int max_q, uin
     int at = i;
     for (int w = words - 1; w >= 0; --w) {
       uint64_t bits = 0;
-      for (; at >= w * 64; at = up[at]) {
+      for (; at >> 6 >= w; at = up[at]) {            // (64 w may pass 32 bits; of no node, -1, it is below)
         bits |= 1ull << (at & 63);
         ++above;
       }
