@@ -8,7 +8,7 @@
 
 namespace {
 
-constexpr int kMaxNodes = 8192;      // of a tree
+using tabit::kMaxNodes;
 constexpr int kMaxKeys = 1 << 30;    // of a sequence: kernels step past the last one by less than as many again
 
 // Sizes that an attention-like launch takes.

@@ -4,8 +4,6 @@
 namespace tabit {
 namespace {
 
-constexpr int kMaxNodes = 8192;
-
 // One workgroup a sequence; a thread follows the parents of its nodes, which fall, through LDS.
 // Bound by the longest path: about 64 cycles a step.
 __global__ void __launch_bounds__(256)

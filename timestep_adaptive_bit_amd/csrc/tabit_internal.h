@@ -149,6 +149,7 @@ int kv_attention_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_
 hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t s);
 
 // Trees of drafted tokens: the same with a.mask, a.mask_words.
+constexpr int kMaxNodes = 8192;  // of a sequence: tree_mask holds their parents in LDS
 int kv_tree_splits(int seqs, int max_q, int q_heads, int kv_heads, int max_kv, int dim_pad);
 hipError_t launch_kv_tree_attention(const KvAttnArgs& a, hipStream_t s);
 hipError_t launch_tree_mask(const int* parents, int tokens, const int* cu_q, int seqs, int max_q,
