@@ -111,3 +111,133 @@ def test_masks_of_more_words_than_any_tree_has(ctx):
     torch.cuda.synchronize()
     assert mask[:, 0].tolist() == [1, 3] and depth.tolist() == [0, 1]
     assert not mask[:, 1:].any()
+
+
+SHAPES = {                 # rows, segments, rank: one kernel for both products, two for single tokens, two of larger tiles
+    "one kernel, rank 16": (20, 5, 16), "one kernel, rank 32": (9, 9, 32), "two kernels, few rows": (40, 8, 64),
+    "two kernels, rank 128": (200, 1, 128), "two kernels, rank 16": (150, 2, 16),
+}
+
+
+def _product(rng, shape, fmt, K=96, N=1184):
+    rows, segments, rank = SHAPES[shape]
+    cu = np.linspace(0, rows, segments + 1).astype(np.int32)
+    which = rng.integers(0, 3, segments).astype(np.int32)
+    bank = T.Adapters(_bf(rng, 3, rank, K, scale=0.1), _bf(rng, 3, N, rank))
+    if fmt == "bf16":
+        x, xs = _bf(rng, rows, K), None
+    elif fmt == "int8":
+        x, xs = S.dev(rng.integers(-127, 128, (rows, K)).astype(np.int8)), S.dev(rng.uniform(0.001, 0.1, rows).astype(np.float32))
+    else:
+        x, xs = S.dev(rng.integers(0, 256, (rows, K // 2), dtype=np.uint8)), S.dev(rng.integers(120, 128, (rows, K // 32), dtype=np.uint8))
+    return bank, x, xs, _bf(rng, rows, N), S.dev(cu), S.dev(which)
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "mxfp4"])
+def test_rows_that_are_no_number(ctx, shape, fmt):
+    """They make NaN of themselves alone, wherever in a tile of rows they lie."""
+    rng = np.random.default_rng(len(shape))
+    bank, x, xs, y, cu, which = _product(rng, shape, fmt)
+    clean = ctx.adapter_linear(bank, x, y, cu, which, x_scale=xs)
+    bad = rng.permutation(len(y))[:2]
+    for t in bad:
+        if fmt == "bf16":
+            x[t, 90] = float("nan")
+        elif fmt == "int8":
+            xs[t] = float("nan")
+        else:
+            xs[t, 2] = 255
+    out = ctx.adapter_linear(bank, x, y, cu, which, x_scale=xs)
+    rest = torch.ones(len(y), dtype=torch.bool, device=DEV)
+    rest[S.dev(bad)] = False
+    assert out[~rest].isnan().all() and torch.equal(out[rest], clean[rest]) and torch.isfinite(clean).all()
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "mxfp4"])
+def test_products_captured(ctx, shape, fmt):
+    """Replays in place, with eager calls on the same workspace in between."""
+    rng = np.random.default_rng(len(shape) + 1)
+    bank, x, xs, y, cu, which = _product(rng, shape, fmt)
+    want = ctx.adapter_linear(bank, x, y, cu, which, x_scale=xs)
+    ws, out = ctx.adapter_workspace(bank, x, len(which)), y.clone()
+
+    def call():
+        ctx.adapter_linear(bank, x, out, cu, which, x_scale=xs, out=out, ws=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for _ in range(3):
+        out.copy_(y)
+        ws.fill_(255)
+        g.replay()
+        eager = ctx.adapter_linear(bank, x, y, cu, which, x_scale=xs, ws=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(eager, want)
+
+
+@pytest.mark.parametrize("rows", [1, 30, 300])
+def test_no_adapters_at_all(ctx, rows):
+    """A bank of none: out = y."""
+    rng = np.random.default_rng(rows)
+    bank = T.Adapters(_bf(rng, 0, 16, 64), _bf(rng, 0, 96, 16))
+    x, y = _bf(rng, rows, 64), _bf(rng, rows, 96)
+    cu, which = S.dev(np.array([0, rows], np.int32)), S.dev(np.array([0], np.int32))
+    assert torch.equal(ctx.adapter_linear(bank, x, y, cu, which), y)
+
+
+# ------------------------------------------------------------------ another stream, moves of one list twice
+def test_calls_on_another_stream(ctx):
+    """Every operator on a side stream, while the default one works: the bits of calls by themselves."""
+    p = A.problem(31, [2500, 90], [20, 8], 8, 2, 64, 16, 32)
+    rng = np.random.default_rng(31)
+    q = S.dev(np.asarray(p["q"], np.float32)).bfloat16()
+    cu, table, lens = S.dev(np.asarray(p["cu"], np.int32)), S.dev(p["table"]), S.dev(np.array(p["lens"], np.int32))
+    parents = S.dev(np.concatenate([S.random_parents(rng, n) for n in (20, 8)]))
+    bank, x, y = T.Adapters(_bf(rng, 2, 16, 64), _bf(rng, 2, 96, 16)), _bf(rng, 28, 64), _bf(rng, 28, 96)
+    which = S.dev(np.array([0, 1], np.int32))
+
+    def run():
+        cache = S.cache_of(p)
+        mask, depth = ctx.tree_mask(parents, cu, 20)
+        o = ctx.kv_tree_attention(cache, q, mask, cu, table, lens, 20, 2500)
+        sums = ctx.kv_weigh(cache, ctx.kv_sums(cache), q, cu, table, lens, 20, 2500)
+        weights = sums.clone()
+        keep, new = ctx.kv_evict(cache, sums, table, lens, 2500, 64, sinks=2, recent=20)
+        ctx.kv_compact(cache, table, keep, new, sums=sums)
+        z = ctx.adapter_linear(bank, x, y, cu, which)
+        return [mask, depth, o, weights, keep, new, sums, cache.k_codes, cache.v_scales, z]
+
+    want = run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    work = torch.randn(4096, 4096, device=DEV)
+    for _ in range(4):
+        work = work @ work * 1e-3
+    with torch.cuda.stream(side):
+        got = run()
+    side.synchronize()
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert torch.equal(a, b), i
+
+
+def test_a_token_named_twice(ctx):
+    """A list that names a token twice puts it in both places; a head's list of one token many times as well."""
+    rng = np.random.default_rng(5)
+    arr = [rng.integers(0, 256, (80, 2, 16, w), dtype=np.uint8) for w in (32, 2, 32, 2)]
+    table = rng.permutation(80).astype(np.int32)[None]
+    for most in (12, 1100):
+        keep = np.sort(rng.integers(most, 1280, (1, 2, most)), axis=2).astype(np.int32)
+        keep[0, 1, most // 2:] = keep[0, 1, -1]
+        cache = T.KVCache(*[S.dev(a) for a in arr], head_dim=64)
+        ctx.kv_compact(cache, S.dev(table), S.dev(keep), S.dev(np.array([most], np.int32)))
+        want = S.compact_want(arr, table, keep, np.array([most]))
+        for n, w in zip(("k_codes", "k_scales", "v_codes", "v_scales"), want):
+            assert np.array_equal(getattr(cache, n).cpu().numpy(), w), n
