@@ -670,10 +670,11 @@ int tabit_tree_mask(tabit_ctx* ctx, const int32_t* parents, int num_tokens, cons
  *   args    as tabit_kv_attention, max_kv at most 2^30; out is not used and must be NULL; lse may be NULL, or
  *           receives the logarithm of each row's sum of exp(score), here of exact weights
  *   sums    device fp32 [num_pages][num_kv_heads][page_size], 16-byte aligned
- *   ws      of tabit_kv_weigh_workspace_bytes bytes, 16-byte aligned
+ *   ws      of tabit_kv_weigh_workspace_bytes bytes, 16-byte aligned (asked for also where one
+ *           kernel does all and does not touch it)
  * Everything is held to fp32 (a query to 2^-21 of the largest element of its block of 32).
  * A row whose own values, position or score with some key it sees is not a number (see
- * tabit_kv_append) adds nothing, nor does a row that sees no key; the sum of a token that is
+ * tabit_kv_append) or passes fp32 adds nothing, nor does a row that sees no key; the sum of a token that is
  * not a number gets nothing.  Sums never become NaN by a call.  Pages of the sequences of a
  * call must be distinct.  The result does not depend on timing.
  */
@@ -749,7 +750,9 @@ size_t tabit_kv_compact_workspace_bytes(int num_seqs, int num_kv_heads, int head
  *               of 8, at least N); out may be y (then with its stride) or not overlap it, and
  *               may not overlap x (columns of one wider matrix do not overlap)
  *   ws          of tabit_adapter_workspace_bytes bytes, 16-byte aligned
- * K and N multiples of 32, at most 32768; 1 <= num_adapters * rank; matrices 16-byte aligned.
+ * K and N multiples of 32, at most 32768; num_adapters may be 0 (out = y); matrices 16-byte
+ * aligned.  What is not finite in x, a or b makes what depends on it infinite or NaN: of a row
+ * of x that row alone.
  */
 typedef struct tabit_adapter_args {
   const void *x, *x_scale;

@@ -220,7 +220,8 @@ struct LongPlan {
 };
 
 // PASS 0 counts the first digit of a chunk's tokens; 1 and 2 find a digit from all chunks' counts and
-// count the next; 3 finds the last and writes the chunk's kept tokens.  Bound as the other, four times: 131072
+// count the next; 3 finds the last and writes the chunk's kept tokens.  Bound as the other, four times, and in 1 to 3
+// by the counts of all chunks, which every workgroup reads before it starts (128 KB, 16 MB a launch of 8 heads): 131072
 // tokens of 8 heads 5.6, 9.3, 8.6 and 10.4 us (one workgroup a head for all of it: 146).
 template <int PASS>
 __global__ void __launch_bounds__(kThreads)

@@ -4,8 +4,9 @@
 namespace tabit {
 namespace {
 
-// One workgroup a sequence; a thread follows the parents of its nodes, which fall, through LDS.
-// Bound by the longest path: about 64 cycles a step.
+// One workgroup a sequence; a thread follows the parents of its nodes (every 256th), which fall, through LDS.
+// Bound by LDS's latency and the sum of a thread's paths, about 53 ns a step: a chain of 64 nodes 4.5 us, of 256
+// 15, of 1024 (2556 steps) 136, of 8192 (135000) 7.2 ms; 8192 nodes whose parents are up to eight before them 1.8 ms.
 __global__ void __launch_bounds__(256)
 tree_mask_kernel(const int* parents, int tokens, const int* cu_q, int max_q, uint64_t* mask, int words, int* depth) {
   __shared__ int up[kMaxNodes];

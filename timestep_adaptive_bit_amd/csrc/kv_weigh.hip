@@ -282,11 +282,12 @@ __device__ __forceinline__ float join_ranges(const KvAttnArgs& a, const Plan& p,
 }
 
 // L of 128 rows, 32 a wave, over one range of keys.  A tile of 64 keys comes to LDS once for all waves, 16
-// keys each, while the tile before is worked on (two stages, one barrier a tile).  Bound by the matrix cores at
-// the power that such operands take: a wave's tile is 20 products, which take 1130 cycles of a SIMD by
-// themselves with random codes (722 with constant ones), 1264 with the exponentials and 1478 in here, batches of
-// equal lengths without a mask; causal ragged ones 1880, their workgroups' ends included (2 x 2048 rows behind
-// 6144 keys at most, 32 heads over 8: 138 us).  Level or slower: one barrier for two tiles, the chains of products
+// keys each, while the tile before is worked on (two stages, one barrier a tile).  A wave's tile is
+// 20 products, 640 cycles of a matrix core, which take a SIMD 1130 by themselves with random codes (722 with
+// constant ones), 1264 with the exponentials and 1478 in here, batches of equal lengths without a mask; causal
+// ragged ones 1880.  Bound there by uneven workgroups and their ends: 2.1 waves are on a SIMD of the three that
+// fit, and the matrix cores are busy for 36% of the cycles where such products alone keep them so for 57%
+// (2 x 2048 rows behind 6144 keys at most, 32 heads over 8: 138 us).  Level or slower: one barrier for two tiles, the chains of products
 // fenced or given a priority.
 template <int NB>
 __global__ void __launch_bounds__(256, 3)
@@ -443,7 +444,8 @@ kv_weigh_join_kernel(KvAttnArgs a, Plan p) {
   if (a.lse != nullptr && rr < n * a.group) write_lse(a, q0, hk, rr, sum, l);
 }
 
-// Sums of 64 keys a wave over all rows that see them; bound as the statistics (150 us there).  (128 keys a wave take
+// Sums of 64 keys a wave over all rows that see them; bound as the statistics (150 us there, matrix cores busy for
+// 34% of the cycles, 2.2 waves on a SIMD of four).  (128 keys a wave take
 // 208 registers and leave two waves a SIMD: 415 us for 315, long prompts, the whole call; a tile's terms in
 // registers, not read from LDS for every product, 64 and 128 keys a wave, 166 and 172 us for 147, this kernel.)  The workgroup's waves go over the row
 // tiles together: a tile's terms come to LDS once for all, straight from memory, while the tile before is
@@ -891,6 +893,8 @@ kv_weigh_add_kernel(KvAttnArgs a, FewPlan p, float* sums, unsigned chunks) {
   }
 }
 
+// The first row past eight is a step: 64 sequences of 8 and 12 rows a key head x up to 8192 keys 96 and 169 us (8
+// key heads of 128), one of 8 and 16 x 1000 keys 11.8 and 19.6.
 bool few_rows(const KvAttnArgs& a) { return (long long)a.max_q * a.group <= 8; }
 
 // Ranges of keys: two workgroups a CU, of at least four tiles (one a wave) each.  A workgroup spends about 5 us
@@ -914,7 +918,8 @@ size_t few_plan_of(int seqs, int kv_heads, int rows, int max_kv, uint8_t* ws, Fe
   return scores + heads * (size_t)p.splits * 64;
 }
 
-// One kernel for short sequences while each (sequence, key head) has a CU to itself (8 waves and 120 KB of LDS).
+// One kernel for short sequences while each (sequence, key head) has a CU to itself (8 waves; of 128 elements 123 KB of
+// LDS with up to four rows, 139 KB with eight).
 // Measured under a graph, two kernels and one, 8 key heads of 128: one row x 1000 keys 12.4 and 10.5 us, x 200 10.5
 // and 8.6, 16 of 700 (64 elements, 16 heads) 14.5 and 10.1; 64 rows x 1000 18.7 and 19.7, 256 x 500 40 and 60.
 bool held(const KvAttnArgs& a) { return a.max_kv <= kHeld && (long long)a.seqs * a.cache.heads <= NUM_CUS; }
