@@ -241,3 +241,31 @@ def test_a_token_named_twice(ctx):
         want = S.compact_want(arr, table, keep, np.array([most]))
         for n, w in zip(("k_codes", "k_scales", "v_codes", "v_scales"), want):
             assert np.array_equal(getattr(cache, n).cpu().numpy(), w), n
+
+
+# ------------------------------------------------------------------ nothing there
+@pytest.mark.parametrize("rows", [1, 2, 40])
+@pytest.mark.parametrize("most", [0, 50, 2000])
+def test_caches_without_pages_or_keys(ctx, rows, most):
+    """Rows that have no key answer zeros and -infinity, whether there are no lengths or no pages; nothing is kept
+    wrongly or written."""
+    rng = np.random.default_rng(rows)
+    cache = T.KVCache.empty(0 if most else 4, 16, 2, 64, 32, DEV)
+    q = _bf(rng, 2 * rows, 8, 64)
+    cu, lens = S.dev(np.array([0, rows, 2 * rows], np.int32)), S.dev(np.array([most, most // 2], np.int32))
+    table = torch.full((2, 128), 3 if not most else 0, dtype=torch.int32, device=DEV)
+    mask, _ = ctx.tree_mask(torch.full((2 * rows,), -1, dtype=torch.int32, device=DEV), cu, rows)
+    lse = torch.full((2 * rows, 8), 7.0, device=DEV)
+    out = ctx.kv_tree_attention(cache, q, mask, cu, table, lens, rows, most, lse=lse)
+    assert not out.any() and lse.isneginf().all()
+    for causal in (True, False):
+        lse.fill_(7.0)
+        sums = torch.full((cache.num_pages, 2, 16), 5.0, device=DEV)
+        ctx.kv_weigh(cache, sums, q, cu, table, lens, rows, most, causal=causal, lse=lse)
+        assert (sums == 5).all() and lse.isneginf().all()
+    keep, new = ctx.kv_evict(cache, sums, table, lens, most, 20, sinks=2, recent=3)
+    # (to the reference: one page, and tables that name another)
+    want, wnew = S.evict_want(np.zeros((1, 2, 16), np.float32), np.full((2, 128), 9), lens.tolist(), 20, 2, 3)
+    assert np.array_equal(keep.cpu().numpy(), want) and np.array_equal(new.cpu().numpy(), wnew)
+    ctx.kv_compact(cache, table, keep, new, sums=sums)
+    assert (sums == 5).all()
